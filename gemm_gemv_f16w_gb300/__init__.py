@@ -42,6 +42,7 @@ EXPORTS = [
     "lq_gemv_argmax", "lq_argmax_f32", "lq_matmul_residual", "lq_matmul_swiglu",
     "lq_gemv_q4_0i", "lq_gemm_q4_0i", "lq_matmul_q4_0i", "lq_pack_q4_0i", "lq_pack_q8_0_rcp",
     "lq_topk_work_bytes", "lq_topk_f32", "lq_gemv_topk", "lq_debug_chain_waits",
+    "lq_kv_pool_bytes", "lq_kv_write", "lq_kv_read", "lq_attn_work_bytes", "lq_attn_paged", "lq_debug_attn_route",
 ]
 _COMPUTE = [n for n in EXPORTS if n.split("_")[1] in ("gemv", "gemm", "matmul")]
 
@@ -114,6 +115,19 @@ def lib() -> ctypes.CDLL:
         L.lq_topk_f32.restype = st
         L.lq_gemv_topk.argtypes = [st, vp, vp, vp, i64, i64, ctypes.c_int, vp, vp, vp, vp]
         L.lq_gemv_topk.restype = st
+        cp, bp = ctypes.POINTER(KVCacheStruct), ctypes.POINTER(KVBatchStruct)
+        L.lq_kv_pool_bytes.argtypes = [ctypes.c_int, i64, i64, i64, i64]
+        L.lq_kv_pool_bytes.restype = ctypes.c_size_t
+        for n in ("lq_kv_write", "lq_kv_read"):
+            f = getattr(L, n)
+            f.argtypes = [cp, bp, vp, i64, vp, i64, vp]
+            f.restype = st
+        L.lq_attn_work_bytes.argtypes = [cp, bp, i64]
+        L.lq_attn_work_bytes.restype = ctypes.c_size_t
+        L.lq_attn_paged.argtypes = [cp, bp, vp, i64, vp, i64, vp, i64, ctypes.c_float, i64, i64, vp, vp]
+        L.lq_attn_paged.restype = st
+        L.lq_debug_attn_route.argtypes = [st]
+        L.lq_debug_attn_route.restype = st
         _lib = L
     return _lib
 
@@ -274,6 +288,124 @@ def lq_matmul_swiglu(fmt, A, W, H, M, I, K, stream=None):
     f = FMT[fmt] if isinstance(fmt, str) else int(fmt)
     _check(lib().lq_matmul_swiglu(f, _ptr(A), _ptr(W), _ptr(H), int(M), int(I), int(K), _stream(stream)),
            "lq_matmul_swiglu")
+
+
+# ---- paged key/value cache and its attention -----------------------------
+class KVCacheStruct(ctypes.Structure):
+    """The lq_kv_cache struct of lq.h."""
+    _fields_ = [("fmt", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class KVBatchStruct(ctypes.Structure):
+    """The lq_kv_batch struct of lq.h."""
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("max_q", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p)]
+
+
+class KVCache:
+    """The K and V pools of a paged cache (lq_kv_cache): allocated here, or
+    the caller's own device buffers ``k`` and ``v``."""
+
+    def __init__(self, fmt, num_pages, page_size, kv_heads, head_dim, k=None, v=None, device=None):
+        code = FMT[fmt] if isinstance(fmt, str) else int(fmt)
+        need = int(lib().lq_kv_pool_bytes(code, int(num_pages), int(page_size), int(kv_heads), int(head_dim)))
+        if need == 0 and num_pages != 0:
+            raise LQError(LQ_ERR_INVALID_ARG, "lq_kv_pool_bytes")
+        pools = []
+        for pool in (k, v):
+            if pool is None:
+                import torch
+                pool = torch.zeros(need, dtype=torch.uint8, device=device or "cuda")
+            elif not isinstance(pool, int) and (not pool.is_contiguous() or pool.numel() * pool.element_size() < need):
+                raise LQError(LQ_ERR_INVALID_ARG, f"KVCache: a pool of {need} contiguous bytes is needed")
+            pools.append(pool)
+        self.k, self.v = pools
+        self.struct = KVCacheStruct(code, int(page_size), int(kv_heads), int(head_dim), int(num_pages),
+                                    _ptr(self.k), _ptr(self.v))
+        self.ref = ctypes.byref(self.struct)
+
+
+class KVBatch:
+    """The tokens of a call (lq_kv_batch): int32 device tensors page_table
+    [batch, max_pages], kv_len [batch] and q_start [batch + 1]."""
+
+    def __init__(self, page_table, kv_len, q_start, tokens, max_q=0):
+        for x, shape in ((page_table, None), (kv_len, (page_table.shape[0],)), (q_start, (page_table.shape[0] + 1,))):
+            if str(x.dtype) != "torch.int32" or not x.is_contiguous() or (shape and tuple(x.shape) != shape):
+                raise LQError(LQ_ERR_INVALID_ARG, "KVBatch: contiguous int32 page_table [batch, max_pages], kv_len [batch] "
+                                                  "and q_start [batch + 1]")
+        self.page_table, self.kv_len, self.q_start, self.tokens = page_table, kv_len, q_start, int(tokens)
+        self.struct = KVBatchStruct(page_table.shape[0], page_table.shape[1], int(tokens), int(max_q), _ptr(page_table),
+                                    _ptr(kv_len), _ptr(q_start))
+        self.ref = ctypes.byref(self.struct)
+
+
+def _rows(x, batch, width, what):
+    """(address, leading dimension) of f32 rows [tokens, heads, head_dim] or
+    [tokens, heads * head_dim]; a raw address is taken as tightly packed."""
+    if x is None or isinstance(x, int):
+        return x or 0, width
+    shape, strides = x.shape, x.stride()
+    per_row = x.numel() // shape[0] if shape[0] else width
+    if str(x.dtype) != "torch.float32" or len(shape) not in (2, 3) or shape[0] < batch.tokens or per_row != width:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 [tokens, heads, head_dim] wanted, got {tuple(shape)} {x.dtype}")
+    if strides[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and strides[1] != shape[2]):
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: heads and dims have to be contiguous")
+    return x.data_ptr(), strides[0] if shape[0] > 1 else width
+
+
+def lq_kv_write(cache, batch, K, V, stream=None) -> None:
+    """Stores the batch's tokens in the cache; K, V: float32 [tokens,
+    kv_heads, head_dim] (token-strided slices allowed). See include/lq.h."""
+    c = cache.struct
+    (k, ldk), (v, ldv) = (_rows(x, batch, c.kv_heads * c.head_dim, "lq_kv_write") for x in (K, V))
+    _check(lib().lq_kv_write(cache.ref, batch.ref, k, ldk, v, ldv, _stream(stream)), "lq_kv_write")
+
+
+def lq_kv_read(cache, batch, K, V, stream=None) -> None:
+    """Reads the batch's tokens back as float32 into K and V (either may be
+    None). See include/lq.h."""
+    c = cache.struct
+    (k, ldk), (v, ldv) = (_rows(x, batch, c.kv_heads * c.head_dim, "lq_kv_read") for x in (K, V))
+    _check(lib().lq_kv_read(cache.ref, batch.ref, k, ldk, v, ldv, _stream(stream)), "lq_kv_read")
+
+
+def attn_work(cache, batch, heads, device=None):
+    """The zero-filled scratch buffer of lq_attn_paged."""
+    import torch
+    nbytes = int(lib().lq_attn_work_bytes(cache.ref, batch.ref, int(heads)))
+    if nbytes == 0:
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_work_bytes")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device or batch.page_table.device)
+
+
+def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=None, heads=None, stream=None) -> None:
+    """Attention of the batch's tokens (Q, O: float32 [tokens, heads,
+    head_dim]) over the cache, causal, with an optional sliding window and
+    sinks; lse: float32 [tokens, heads] or None; work: attn_work(...), which a
+    program keeps (None makes one for this call). ``heads`` is needed where Q
+    is not a three-dimensional tensor. See include/lq.h."""
+    D = cache.struct.head_dim
+    if heads is None:
+        heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // D
+    if work is None:
+        if stream is not None:
+            raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: a call on a stream of its own brings its work buffer")
+        work = attn_work(cache, batch, heads)
+    q, ldq = _rows(Q, batch, heads * D, "lq_attn_paged")
+    o, ldo = _rows(O, batch, heads * D, "lq_attn_paged")
+    if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()):
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: lse is a contiguous float32 [tokens, heads]")
+    _check(lib().lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, _ptr(lse), heads, scale, window, sinks, _ptr(work),
+                               _stream(stream)), "lq_attn_paged")
+
+
+def attn_route(route: int) -> None:
+    """lq_attn_paged's kernel: 0 automatic, 1 generic, 2 warp-level MMAs,
+    3 tcgen05; for tests and comparisons."""
+    _check(lib().lq_debug_attn_route(int(route)), "lq_debug_attn_route")
 
 
 # ---- host packers --------------------------------------------------------

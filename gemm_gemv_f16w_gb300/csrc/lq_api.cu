@@ -17,7 +17,7 @@ namespace lq {
 
 namespace {
 std::atomic<int> g_force_route{0};
-std::atomic<uint64_t> g_route_count[8];
+std::atomic<uint64_t> g_route_count[16];
 std::atomic<unsigned long long> g_wait_ns{0};
 std::mutex g_info_mu;
 DeviceInfo g_info[kMaxDevices];
@@ -60,7 +60,7 @@ unsigned wait_limit_iters() {
 }
 
 void count_route(int route) {
-  if (route >= 0 && route < 8) g_route_count[route].fetch_add(1);
+  if (route >= 0 && route < 16) g_route_count[route].fetch_add(1);
 }
 
 namespace {
@@ -271,7 +271,9 @@ lq_status lq_last_device_error(void) {
   const unsigned d = read_clear_chain_error();
   const unsigned e = read_clear_batch_error();
   const unsigned f = read_clear_small_error();
-  const unsigned v = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : f))));
+  const unsigned g = read_clear_kv_error();
+  const unsigned h = read_clear_attn_error();
+  const unsigned v = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : (f ? f : (g ? g : h))))));
   if (v == 0) return LQ_OK;
   return static_cast<lq_status>(v);
 }
@@ -365,7 +367,7 @@ lq_status lq_debug_force_route(int route) {
   return LQ_OK;
 }
 uint64_t lq_debug_route_count(int route) {
-  if (route < 0 || route > 7) return 0;
+  if (route < 0 || route > 11) return 0;
   return g_route_count[route].load();
 }
 void lq_debug_reset_counts(void) {

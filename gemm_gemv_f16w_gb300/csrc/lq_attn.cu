@@ -1,0 +1,202 @@
+// lq_attn_paged: argument checks, the choice of a kernel, and the generic
+// kernel that takes every geometry.
+//
+// Generic kernel: one CTA per (row, query head). Its eight warps stride over
+// the visible keys, a lane holding the dims lane, lane + 32, ... of the query
+// and the running output; a warp-wide sum gives each logit, and a running
+// maximum and sum (softmax in one pass over the keys) rescale the output when
+// the maximum grows. The warps' partial results are joined through shared
+// memory. It is bound by its serial chain of loads and shuffles per key and
+// reads a shared head's keys once per query head.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "lq_attn.cuh"
+
+namespace lq {
+namespace {
+
+__device__ unsigned g_attn_err;
+__device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attn_err, 0u, code); }
+
+std::atomic<int> g_attn_route{0};
+
+constexpr int kGWarps = 8;
+constexpr int kMaxDim = 256;
+
+template <int FMT>
+__global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
+  __shared__ float part[kGWarps][kMaxDim + 2];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = static_cast<int>(blockIdx.x / a.heads), h = static_cast<int>(blockIdx.x % a.heads);
+  const int D = a.c.head_dim, blocks = D / 32, hk = h / a.group;
+  const int i = kv::find_sequence(a.b, t, lane);
+  if (i < 0) {  // the whole CTA
+    pdl_launch_dependents();
+    return;
+  }
+  const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
+  const int p = s.len - s.rows + (t - s.row0);
+  const kv::Visible see = kv::visible(p, a.window, a.sinks);
+
+  float q[kMaxDim / 32], acc[kMaxDim / 32];
+  const float* qrow = a.Q + t * a.ldq + static_cast<long long>(h) * D;
+#pragma unroll
+  for (int b = 0; b < kMaxDim / 32; ++b) {
+    q[b] = b < blocks ? qrow[b * 32 + lane] * a.scale : 0.0f;
+    acc[b] = 0.0f;
+  }
+  float m = -INFINITY, l = 0.0f;
+  bool any = false;
+  // keys 0 .. sink_end-1, then begin .. p, dealt to the warps in turn
+  const int count = p < 0 ? 0 : see.sink_end + (p - see.begin + 1);
+  const long long scale_at = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
+  for (int n = warp; n < count; n += kGWarps) {
+    const int j = n < see.sink_end ? n : see.begin + (n - see.sink_end);
+    const int page = kv::page_of(a.c, a.b, i, j);
+    if (page < 0) continue;
+    const int slot = j % a.c.page_size;
+    const long long at = page * a.c.page_bytes + hk * a.c.head_bytes;
+    float v[kMaxDim / 32], x = 0.0f;
+#pragma unroll
+    for (int b = 0; b < kMaxDim / 32; ++b) {
+      if (b >= blocks) break;
+      float kd;
+      const unsigned char* kr = a.c.k + at + static_cast<long long>(slot) * a.c.row_bytes;
+      const unsigned char* vr = a.c.v + at + static_cast<long long>(slot) * a.c.row_bytes;
+      if constexpr (FMT == LQ_FMT_F16) {
+        kd = __half2float(reinterpret_cast<const __half*>(kr)[b * 32 + lane]);
+        v[b] = __half2float(reinterpret_cast<const __half*>(vr)[b * 32 + lane]);
+      } else {
+        const float ks = __half2float(reinterpret_cast<const __half*>(a.c.k + at + scale_at)[slot * blocks + b]);
+        const float vs = __half2float(reinterpret_cast<const __half*>(a.c.v + at + scale_at)[slot * blocks + b]);
+        if constexpr (FMT == LQ_FMT_Q8_0) {
+          kd = ks * static_cast<float>(static_cast<signed char>(kr[b * 32 + lane]));
+          v[b] = vs * static_cast<float>(static_cast<signed char>(vr[b * 32 + lane]));
+        } else {
+          const int at4 = b * 16 + (lane & 15), shift = (lane >> 4) * 4;
+          kd = ks * static_cast<float>(static_cast<int>((kr[at4] >> shift) & 15) - 8);
+          v[b] = vs * static_cast<float>(static_cast<int>((vr[at4] >> shift) & 15) - 8);
+        }
+      }
+      x = fmaf(q[b], kd, x);
+    }
+    x = warp_sum(x);
+    any = true;
+    const float to = fmaxf(m, x);
+    const float base = to == -INFINITY ? 0.0f : to;  // every logit so far is -inf
+    const float keep = expf(m - base), w = expf(x - base);
+    m = to;
+    l = l * keep + w;
+#pragma unroll
+    for (int b = 0; b < kMaxDim / 32; ++b)
+      if (b < blocks) acc[b] = acc[b] * keep + w * v[b];
+  }
+  pdl_launch_dependents();
+#pragma unroll
+  for (int b = 0; b < kMaxDim / 32; ++b)
+    if (b < blocks) part[warp][b * 32 + lane] = acc[b];
+  if (lane == 0) {
+    part[warp][kMaxDim] = any ? m : -INFINITY;
+    part[warp][kMaxDim + 1] = l;
+  }
+  const bool seen = __syncthreads_or(any ? 1 : 0) != 0;
+  float top = -INFINITY, sum = 0.0f;
+  for (int w = 0; w < kGWarps; ++w) top = fmaxf(top, part[w][kMaxDim]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  for (int w = 0; w < kGWarps; ++w) sum += part[w][kMaxDim + 1] * expf(part[w][kMaxDim] - base);
+  float* orow = a.O + t * a.ldo + static_cast<long long>(h) * D;
+  for (int d = threadIdx.x; d < D; d += kGWarps * 32) {
+    float o = 0.0f;
+    for (int w = 0; w < kGWarps; ++w) o += part[w][d] * expf(part[w][kMaxDim] - base);
+    if (LQ_IN_BOUNDS(t < a.b.tokens && h < a.heads)) orow[d] = seen ? o / sum : 0.0f;
+  }
+  if (a.lse && threadIdx.x == 0)
+    a.lse[static_cast<long long>(t) * a.heads + h] = seen ? base + logf(sum) : -INFINITY;
+}
+
+}  // namespace
+
+lq_status launch_attn_generic(const AttnArgs& a, int fmt, cudaStream_t stream) {
+  const long long ctas = static_cast<long long>(a.b.tokens) * a.heads;
+  if (ctas > (1LL << 31) - 1) return LQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kGWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void (*kernel)(AttnArgs) = fmt == LQ_FMT_F16    ? attn_generic_kernel<LQ_FMT_F16>
+                             : fmt == LQ_FMT_Q8_0 ? attn_generic_kernel<LQ_FMT_Q8_0>
+                                                  : attn_generic_kernel<LQ_FMT_Q4_0>;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) count_route(kAttnRouteGeneric);
+  return cuda_status(e);
+}
+
+unsigned read_clear_attn_error() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_attn_err, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_attn_err, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace lq
+
+using namespace lq;
+
+extern "C" {
+
+size_t lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, int64_t heads) {
+  bool noop;
+  if (kv_check(cache, batch, &noop) != LQ_OK) return 0;
+  if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
+  return 16;
+}
+
+lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
+                        float* O, int64_t ldo, float* lse, int64_t heads, float scale, int64_t window,
+                        int64_t sinks, void* work, void* stream) {
+  bool noop;
+  lq_status st = kv_check(cache, batch, &noop);
+  if (st != LQ_OK) return st;
+  if (heads < 1 || heads % cache->kv_heads != 0 || window < 0 || sinks < 0 || !std::isfinite(scale))
+    return LQ_ERR_INVALID_ARG;
+  if (noop) return LQ_OK;
+  const int64_t width = heads * cache->head_dim;
+  if (!Q || !O || !work || !aligned_to(Q, 4) || !aligned_to(O, 4) || !aligned_to(lse, 4) || !aligned_to(work, 16))
+    return LQ_ERR_INVALID_ARG;
+  if (ldq < width || ldo < width) return LQ_ERR_INVALID_ARG;
+  if (heads > 65536) return LQ_ERR_UNSUPPORTED;
+  AttnArgs a = {};
+  a.c = kv_cache_view(*cache);
+  a.b = kv_batch_view(*batch);
+  a.Q = Q;
+  a.O = O;
+  a.lse = lse;
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.heads = static_cast<int>(heads);
+  a.group = static_cast<int>(heads / cache->kv_heads);
+  a.scale = scale;
+  const int64_t most = (1LL << 31) - 1;
+  a.window = static_cast<int>(std::min(window, most));
+  a.sinks = static_cast<int>(std::min(sinks, most));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch_attn_generic(a, cache->fmt, s);
+}
+
+lq_status lq_debug_attn_route(int route) {
+  if (route < 0 || route > 3) return LQ_ERR_INVALID_ARG;
+  g_attn_route.store(route);
+  return LQ_OK;
+}
+
+}  // extern "C"

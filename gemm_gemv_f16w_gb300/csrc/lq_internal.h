@@ -107,6 +107,8 @@ unsigned read_clear_gemm_tma_error();
 unsigned read_clear_chain_error();
 unsigned read_clear_batch_error();
 unsigned read_clear_small_error();
+unsigned read_clear_kv_error();
+unsigned read_clear_attn_error();
 
 lq_status cuda_status(cudaError_t e);
 

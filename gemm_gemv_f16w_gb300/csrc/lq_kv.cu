@@ -1,0 +1,366 @@
+// Writing tokens into the paged key/value cache and reading them back.
+//
+// One pass over the data: 8 bytes an element come in or go out as f32, and
+// 2 (f16), 1.0625 (Q8_0) or 0.5625 (Q4_0) as codes and scales, so HBM (or,
+// for a decode step, the launch) bounds both kernels. A warp takes 512
+// consecutive elements of one token's heads, four per lane and load, so that
+// a block of 32 is eight neighbouring lanes: its largest magnitude is three
+// shuffles away, four codes of a lane leave as one 4-byte store (Q4_0: the
+// low-nibble lanes fetch their partners' codes with one shuffle), and the
+// loads of all four groups are in flight before the first is used. The eight
+// warps of a CTA take consecutive tokens, whose rows are neighbours in a page.
+// The rounding rules are those of the host packers (lq_pack.cpp), with the
+// same float32 steps, so the codes are theirs bit for bit.
+#include <algorithm>
+
+#include "lq_device.cuh"
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+namespace lq {
+namespace {
+
+__device__ unsigned g_kv_err;
+__device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_kv_err, 0u, code); }
+
+constexpr int kKvWarps = 8;
+constexpr int kKvGroups = 4;  // 128-element groups of a warp
+constexpr unsigned kLimitBits = 0x477FE000u;  // 65504.0f
+constexpr unsigned kInfBits = 0x7F800000u;
+
+struct KvArgs {
+  kv::Cache c;
+  kv::Batch b;
+  const float* in[2];  // K, V rows (write)
+  float* out[2];       // K, V rows (read; null: skip)
+  long long ld[2];
+  int width;           // kv_heads * head_dim
+  int sides, only;     // 2: K and V; 1: only K (0) or only V (1)
+};
+
+// |x| as bits, clamped to the cache's range; NaNs stay above kInfBits.
+__device__ __forceinline__ unsigned magnitude(float x) {
+  const unsigned u = __float_as_uint(x) & 0x7FFFFFFFu;
+  return u > kInfBits ? u : min(u, kLimitBits);
+}
+__device__ __forceinline__ float clamped(float x) { return fminf(fmaxf(x, -65504.0f), 65504.0f); }
+
+// Destination of four codes: one store where the pool is aligned for it.
+template <bool VEC, class T>
+__device__ __forceinline__ void store4(unsigned char* at, const T (&q)[4]) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(q);
+    else
+      *reinterpret_cast<unsigned*>(at) = *reinterpret_cast<const unsigned*>(q);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<T*>(at)[j] = q[j];
+  }
+}
+
+// Quantises and stores the lane's four elements x (elements e .. e + 3 of the
+// head's row; lanes 8i .. 8i + 7 hold one block). `row` and `scales` are the
+// token's codes and scales; null drops the store (all lanes still take part
+// in the shuffles).
+template <int FMT, bool VEC>
+__device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row, __half* scales, int lane) {
+  const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+  if constexpr (FMT == LQ_FMT_F16) {
+    alignas(8) __half h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __float2half_rn(x[j] == x[j] ? clamped(x[j]) : x[j]);
+    if (row) store4<VEC>(row + 2 * e, h);
+  } else {
+    unsigned top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, magnitude(x[j]));
+    const unsigned mine = top;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool bad = top > kInfBits;  // a NaN in the block
+    float d;
+    alignas(4) unsigned char q[4];
+    if constexpr (FMT == LQ_FMT_Q8_0) {
+      d = __fdiv_rn(__uint_as_float(top), 127.0f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int v = 0;
+        if (!bad && d != 0.0f) v = max(-127, min(127, static_cast<int>(roundf(__fdiv_rn(clamped(x[j]), d)))));
+        q[j] = static_cast<unsigned char>(v);
+      }
+      if (row) store4<VEC>(row + e, q);
+    } else {
+      // the first element of the largest magnitude gives the scale its sign
+      const unsigned holders = __ballot_sync(0xffffffffu, mine == top) >> (lane & 24);
+      const int first = __ffs(static_cast<int>(holders & 0xFFu)) - 1;
+      float m = x[3];
+#pragma unroll
+      for (int j = 2; j >= 0; --j) m = magnitude(x[j]) == mine ? x[j] : m;
+      m = __shfl_sync(0xffffffffu, clamped(m), (lane & 24) + first);
+      d = __fdiv_rn(m, -8.0f);
+      unsigned word = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int v = 8;
+        if (!bad && d != 0.0f) v = min(15, static_cast<int>(__fadd_rn(__fdiv_rn(clamped(x[j]), d), 8.5f)));
+        word |= static_cast<unsigned>(v) << (8 * j);
+      }
+      const unsigned high = __shfl_down_sync(0xffffffffu, word, 4);  // elements + 16
+      word |= high << 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = static_cast<unsigned char>(word >> (8 * j));
+      if (row && (lane & 4) == 0) store4<VEC>(row + (e >> 5) * 16 + (e & 15), q);
+    }
+    if (row && (lane & 7) == 0) scales[e >> 5] = bad ? __ushort_as_half(0x7E00) : __float2half_rn(d);
+  }
+}
+
+// The four elements e .. e + 3 of a stored row.
+template <int FMT, bool VEC>
+__device__ __forceinline__ float4 get(const unsigned char* row, const __half* scales, int e) {
+  if constexpr (FMT == LQ_FMT_F16) {
+    __half h[4];
+    if constexpr (VEC) {
+      *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(row + 2 * e);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = reinterpret_cast<const __half*>(row)[e + j];
+    }
+    return make_float4(__half2float(h[0]), __half2float(h[1]), __half2float(h[2]), __half2float(h[3]));
+  } else {
+    const unsigned char* at = FMT == LQ_FMT_Q8_0 ? row + e : row + (e >> 5) * 16 + (e & 15);
+    unsigned w = 0;
+    if constexpr (VEC) {
+      w = *reinterpret_cast<const unsigned*>(at);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= static_cast<unsigned>(at[j]) << (8 * j);
+    }
+    const float d = __half2float(scales[e >> 5]);
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned byte = (w >> (8 * j)) & 0xFFu;
+      const int q = FMT == LQ_FMT_Q8_0 ? static_cast<int>(static_cast<signed char>(byte))
+                                       : static_cast<int>((e & 16) ? byte >> 4 : byte & 15u) - 8;
+      v[j] = d * static_cast<float>(q);
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// grid: x = groups of kKvWarps tokens, y = sides * (512-element segment) + side
+template <int FMT, bool VEC, bool WRITE>
+__global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = static_cast<int>(blockIdx.x) * kKvWarps + warp;
+  const int which = a.sides == 2 ? static_cast<int>(blockIdx.y & 1u) : a.only;
+  const int segment = static_cast<int>(a.sides == 2 ? blockIdx.y >> 1 : blockIdx.y);
+  const int first = segment * (kKvGroups * 128) + lane * 4;
+  if (t < a.b.tokens) {
+    float4 x[kKvGroups];
+    if constexpr (WRITE) {
+      const float* in = a.in[which] + t * a.ld[which];
+#pragma unroll
+      for (int g = 0; g < kKvGroups; ++g) {
+        const int e = first + g * 128;
+        x[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (e < a.width) {
+          if constexpr (VEC) {
+            x[g] = *reinterpret_cast<const float4*>(in + e);
+          } else {
+            x[g] = make_float4(in[e], in[e + 1], in[e + 2], in[e + 3]);
+          }
+        }
+      }
+    }
+    const int i = kv::find_sequence(a.b, t, lane);
+    int page = -1, slot = 0;
+    if (i >= 0) {
+      const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
+      const int p = s.len - s.rows + (t - s.row0);
+      if (p >= 0) {
+        page = kv::page_of(a.c, a.b, i, p);
+        slot = p % a.c.page_size;
+      }
+    }
+    unsigned char* pool = which ? a.c.v : a.c.k;
+    const int D = a.c.head_dim;
+    const long long scale_at = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
+#pragma unroll
+    for (int g = 0; g < kKvGroups; ++g) {
+      const int e = first + g * 128;
+      if (e - lane * 4 >= a.width) break;  // the warp's last group
+      const int h = e / D, r = e - h * D;
+      unsigned char* row = nullptr;
+      __half* scales = nullptr;
+      if (page >= 0 && e < a.width && LQ_IN_BOUNDS(page < a.c.num_pages && h < a.c.kv_heads)) {
+        unsigned char* head = pool + page * a.c.page_bytes + h * a.c.head_bytes;
+        row = head + static_cast<long long>(slot) * a.c.row_bytes;
+        scales = reinterpret_cast<__half*>(head + scale_at) + slot * (D / 32);
+      }
+      if constexpr (WRITE) {
+        put<FMT, VEC>(x[g], r, row, scales, lane);
+      } else if (e < a.width && i >= 0) {
+        const float4 v = row ? get<FMT, VEC>(row, scales, r) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float* out = a.out[which] + t * a.ld[which] + e;
+        if constexpr (VEC) {
+          *reinterpret_cast<float4*>(out) = v;
+        } else {
+          out[0] = v.x;
+          out[1] = v.y;
+          out[2] = v.z;
+          out[3] = v.w;
+        }
+      }
+    }
+  }
+  pdl_launch_dependents();
+}
+
+template <bool WRITE>
+lq_status launch(int fmt, KvArgs& a, cudaStream_t stream) {
+  a.sides = WRITE || (a.out[0] && a.out[1]) ? 2 : 1;
+  a.only = !WRITE && !a.out[0] ? 1 : 0;
+  const unsigned segments = static_cast<unsigned>((a.width + kKvGroups * 128 - 1) / (kKvGroups * 128));
+  bool vec = a.c.head_bytes % 16 == 0 && aligned_to(a.c.k, 16) && aligned_to(a.c.v, 16);
+  for (int i = 0; i < 2; ++i) {
+    const void* p = WRITE ? static_cast<const void*>(a.in[i]) : static_cast<const void*>(a.out[i]);
+    vec = vec && (!p || (a.ld[i] % 4 == 0 && aligned_to(p, 16)));
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.b.tokens + kKvWarps - 1) / kKvWarps),
+                     static_cast<unsigned>(a.sides) * segments);
+  cfg.blockDim = dim3(kKvWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void (*kernel)(KvArgs) = nullptr;
+  switch (fmt) {
+    case LQ_FMT_F16: kernel = vec ? kv_kernel<LQ_FMT_F16, true, WRITE> : kv_kernel<LQ_FMT_F16, false, WRITE>; break;
+    case LQ_FMT_Q8_0: kernel = vec ? kv_kernel<LQ_FMT_Q8_0, true, WRITE> : kv_kernel<LQ_FMT_Q8_0, false, WRITE>; break;
+    default: kernel = vec ? kv_kernel<LQ_FMT_Q4_0, true, WRITE> : kv_kernel<LQ_FMT_Q4_0, false, WRITE>; break;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+}  // namespace
+
+lq_status kv_check(const lq_kv_cache* cache, const lq_kv_batch* batch, bool* noop) {
+  *noop = false;
+  if (!cache || !batch) return LQ_ERR_INVALID_ARG;
+  const lq_kv_cache& c = *cache;
+  const lq_kv_batch& b = *batch;
+  if (c.fmt == LQ_FMT_Q4_0I) return LQ_ERR_UNSUPPORTED;
+  if (c.fmt != LQ_FMT_F16 && c.fmt != LQ_FMT_Q8_0 && c.fmt != LQ_FMT_Q4_0) return LQ_ERR_INVALID_ARG;
+  if (c.page_size < 1 || c.page_size > 65536 || c.kv_heads < 1 || c.num_pages < 0) return LQ_ERR_INVALID_ARG;
+  if (c.head_dim < 32 || c.head_dim % 32 != 0) return LQ_ERR_INVALID_ARG;
+  if (b.batch < 0 || b.tokens < 0 || b.max_q < 0 || b.max_pages < 0) return LQ_ERR_INVALID_ARG;
+  if (b.batch == 0 || b.tokens == 0) {
+    *noop = true;
+    return LQ_OK;
+  }
+  if (!c.k || !c.v || !aligned_to(c.k, 2) || !aligned_to(c.v, 2)) return LQ_ERR_INVALID_ARG;
+  if (!b.page_table || !b.kv_len || !b.q_start) return LQ_ERR_INVALID_ARG;
+  if (!aligned_to(b.page_table, 4) || !aligned_to(b.kv_len, 4) || !aligned_to(b.q_start, 4)) return LQ_ERR_INVALID_ARG;
+  // 32-bit token, page and row indices inside the kernels
+  const long long most = (1LL << 31) - 1;
+  if (c.head_dim > 256 || c.num_pages > most || b.tokens > (1LL << 30) || c.kv_heads > 4096) return LQ_ERR_UNSUPPORTED;
+  return LQ_OK;
+}
+
+kv::Cache kv_cache_view(const lq_kv_cache& c) {
+  kv::Cache v;
+  v.k = static_cast<unsigned char*>(c.k);
+  v.v = static_cast<unsigned char*>(c.v);
+  v.row_bytes = kv::code_row_bytes(c.fmt, c.head_dim);
+  v.head_bytes = static_cast<long long>(c.page_size) * (v.row_bytes + (c.fmt == LQ_FMT_F16 ? 0 : c.head_dim / 32 * 2));
+  v.page_bytes = v.head_bytes * c.kv_heads;
+  v.page_size = c.page_size;
+  v.kv_heads = c.kv_heads;
+  v.head_dim = c.head_dim;
+  v.num_pages = static_cast<int>(c.num_pages);
+  return v;
+}
+
+kv::Batch kv_batch_view(const lq_kv_batch& b) {
+  kv::Batch v;
+  v.table = b.page_table;
+  v.kv_len = b.kv_len;
+  v.q_start = b.q_start;
+  v.batch = b.batch;
+  v.max_pages = b.max_pages;
+  v.tokens = static_cast<int>(b.tokens);
+  return v;
+}
+
+unsigned read_clear_kv_error() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_kv_err, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_kv_err, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace lq
+
+using namespace lq;
+
+extern "C" {
+
+size_t lq_kv_pool_bytes(int fmt, int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t head_dim) {
+  if (fmt != LQ_FMT_F16 && fmt != LQ_FMT_Q8_0 && fmt != LQ_FMT_Q4_0) return 0;
+  if (num_pages < 0 || num_pages > (1LL << 31) - 1 || page_size < 1 || page_size > 65536) return 0;
+  if (kv_heads < 1 || kv_heads > 4096 || head_dim < 32 || head_dim % 32 != 0 || head_dim > 256) return 0;
+  const size_t row = static_cast<size_t>(kv::code_row_bytes(fmt, static_cast<int>(head_dim))) +
+                     (fmt == LQ_FMT_F16 ? 0 : static_cast<size_t>(head_dim) / 32 * 2);
+  const unsigned __int128 bytes = static_cast<unsigned __int128>(row) * static_cast<size_t>(page_size) *
+                                  static_cast<size_t>(kv_heads) * static_cast<size_t>(num_pages);
+  return bytes > (static_cast<unsigned __int128>(1) << 62) ? 0 : static_cast<size_t>(bytes);
+}
+
+lq_status lq_kv_write(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* K, int64_t ldk,
+                      const float* V, int64_t ldv, void* stream) {
+  bool noop;
+  lq_status st = kv_check(cache, batch, &noop);
+  if (st != LQ_OK || noop) return st;
+  const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+  if (!K || !V || !aligned_to(K, 4) || !aligned_to(V, 4) || ldk < width || ldv < width) return LQ_ERR_INVALID_ARG;
+  KvArgs a = {};
+  a.c = kv_cache_view(*cache);
+  a.b = kv_batch_view(*batch);
+  a.in[0] = K;
+  a.in[1] = V;
+  a.ld[0] = ldk;
+  a.ld[1] = ldv;
+  a.width = static_cast<int>(width);
+  return launch<true>(cache->fmt, a, static_cast<cudaStream_t>(stream));
+}
+
+lq_status lq_kv_read(const lq_kv_cache* cache, const lq_kv_batch* batch, float* K, int64_t ldk, float* V,
+                     int64_t ldv, void* stream) {
+  bool noop;
+  lq_status st = kv_check(cache, batch, &noop);
+  if (st != LQ_OK || noop) return st;
+  const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+  if (!K && !V) return LQ_ERR_INVALID_ARG;
+  if (!aligned_to(K, 4) || !aligned_to(V, 4) || (K && ldk < width) || (V && ldv < width)) return LQ_ERR_INVALID_ARG;
+  KvArgs a = {};
+  a.c = kv_cache_view(*cache);
+  a.b = kv_batch_view(*batch);
+  a.out[0] = K;
+  a.out[1] = V;
+  a.ld[0] = ldk;
+  a.ld[1] = ldv;
+  a.width = static_cast<int>(width);
+  return launch<false>(cache->fmt, a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

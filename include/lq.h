@@ -309,6 +309,110 @@ lq_status lq_matmul_residual(int fmt, const float* A, const void* W, const float
 lq_status lq_matmul_swiglu(int fmt, const float* A, const void* W, float* H,
                            int64_t M, int64_t I, int64_t K, void* stream);
 
+/* ---- paged key/value cache ------------------------------------------------
+ * The keys and values of the tokens decoded so far, in the library's own
+ * formats: f16, Q8_0 or Q4_0 blocks of 32 along the head dimension (the
+ * values and roundings of lq_pack_<fmt>), laid out for streaming. One pool
+ * for K and one for V, each lq_kv_pool_bytes(...) bytes of DEVICE memory:
+ *     pool[num_pages][kv_heads][ codes | scales ]
+ *   codes : page_size rows (tokens) of head_dim codes: f16 values, int8, or
+ *           16 bytes a block (element j in the low, j + 16 in the high nibble
+ *           of byte j)
+ *   scales: page_size rows of head_dim / 32 f16 scales (quantised formats)
+ * so that a (page, head) is one contiguous run with its codes on 16-byte
+ * boundaries (page_size a multiple of 16).
+ *
+ * A batch names the tokens a call works on. Sequence i has kv_len[i] tokens
+ * in all, of which the last q_start[i+1] - q_start[i] are this call's: rows
+ * q_start[i] .. q_start[i+1]-1 of the call's K, V, Q or O, at positions
+ * kv_len[i] - (q_start[i+1] - q_start[i]) .. kv_len[i] - 1. Position p lives
+ * in page page_table[i * max_pages + p / page_size], slot p % page_size.
+ * kv_len, q_start (batch + 1 entries, not decreasing, from 0) and page_table
+ * are DEVICE arrays, read when the kernel runs; the two structs are host
+ * memory, read during the call.
+ *   - A page outside 0 .. num_pages-1 (-1, say, for a page that a sliding
+ *     window has left behind) is never accessed: writes to it are dropped,
+ *     reads give zeros, its keys are invisible to attention. Rows outside
+ *     0 .. tokens-1 and positions below 0 or past max_pages * page_size are
+ *     treated likewise; kv_len beyond max_pages * page_size counts as that.
+ *   - `tokens` is the number of rows of K, V, Q and O; rows that belong to
+ *     no sequence are left as they are. max_q is the largest number of new
+ *     tokens of a sequence, or 0 if unknown; it only steers which kernel
+ *     runs, any value gives the same results.
+ *   - Rows are addressed by a leading dimension in floats, ld >= heads *
+ *     head_dim (heads follow one another), so that K, V and Q can be slices
+ *     of one fused projection's output.
+ *   - head_dim a multiple of 32, 1 <= page_size <= 65536, pointers aligned to
+ *     their elements (pools: 2 bytes), else LQ_ERR_INVALID_ARG; head_dim
+ *     > 256 or LQ_FMT_Q4_0I -> LQ_ERR_UNSUPPORTED. batch == 0 or tokens == 0:
+ *     LQ_OK, nothing is launched.
+ * (The pages keep an f32 or f16 cache beside their attention kernels:
+ * kv_cache_append_f32 and flash_attn_decode_paged_f32, ferrum-kernels
+ * src/attention/metal/pipelines.rs; decode_attention and prefill_attention_
+ * batched, lattice-inference src/forward/metal_qwen35.rs.) */
+typedef struct {
+  int32_t fmt;       /* LQ_FMT_F16, LQ_FMT_Q8_0 or LQ_FMT_Q4_0 */
+  int32_t page_size; /* tokens a page */
+  int32_t kv_heads;
+  int32_t head_dim;
+  int64_t num_pages;
+  void*   k;         /* DEVICE, lq_kv_pool_bytes each */
+  void*   v;
+} lq_kv_cache;
+
+typedef struct {
+  int32_t batch;
+  int32_t max_pages;         /* row length of page_table */
+  int64_t tokens;
+  int64_t max_q;
+  const int32_t* page_table; /* DEVICE, batch * max_pages */
+  const int32_t* kv_len;     /* DEVICE, batch */
+  const int32_t* q_start;    /* DEVICE, batch + 1 */
+} lq_kv_batch;
+
+/* Bytes of one pool (K or V); 0 for arguments out of range. */
+size_t lq_kv_pool_bytes(int fmt, int64_t num_pages, int64_t page_size, int64_t kv_heads,
+                        int64_t head_dim);
+
+/* Stores the batch's tokens (K, V: f32 rows of kv_heads * head_dim). Values
+ * beyond +-65504, infinities among them, are clamped to it first (the cache
+ * has f16's range in every format); a NaN is kept: as the element in f16, as
+ * a NaN scale of its block of 32 in the quantised formats. */
+lq_status lq_kv_write(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* K, int64_t ldk,
+                      const float* V, int64_t ldv, void* stream);
+/* The inverse: the batch's tokens as f32 (exact: d * q). K or V may be NULL.
+ * With q_start covering whole sequences it reads back all of the cache. */
+lq_status lq_kv_read(const lq_kv_cache* cache, const lq_kv_batch* batch, float* K, int64_t ldk, float* V,
+                     int64_t ldv, void* stream);
+
+/* ---- attention over the paged cache ---------------------------------------
+ * For every row t of the batch (position p) and query head h, with the key /
+ * value head h / (heads / kv_heads):
+ *     O[t,h] = sum_j softmax_j(scale * Q[t,h] . k_j) v_j
+ * over the visible positions j: j <= p, and, with window > 0, j > p - window
+ * or j < sinks (the last `window` positions, itself among them, and the
+ * first `sinks`). window == 0: no window, sinks has no effect. The new
+ * tokens' own keys and values are read from the cache (lq_kv_write first).
+ * A row that sees nothing gets zeros, and -inf in lse. Invisible keys have
+ * no influence, NaN and infinities among them included.
+ *   lse (NULL or tokens * heads floats, row t at lse + t * heads): the
+ *     natural logarithm of the sum of exp(scale * Q . k), by which results
+ *     over parts of a context can be joined.
+ *   work: lq_attn_work_bytes(...) bytes of DEVICE memory, 16-byte aligned,
+ *     zero-filled before its first use; each call leaves it ready for the
+ *     next. It depends on the geometry alone, not on lengths, serves one
+ *     call at a time and may be shared by calls on one stream.
+ * Every product is exact to f32's precision: f16 operands in two parts with
+ * f32 accumulation on the tensor cores, softmax and sums in f32; the result
+ * is within 2e-5 of the 64-bit one (2-norms) for logits of ordinary size.
+ * The order of the sums does not vary from run to run. O must not overlap Q.
+ *   heads a multiple of kv_heads, scale finite, window and sinks >= 0, ldq
+ *   and ldo >= heads * head_dim, else LQ_ERR_INVALID_ARG. */
+size_t    lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, int64_t heads);
+lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
+                        float* O, int64_t ldo, float* lse, int64_t heads, float scale, int64_t window,
+                        int64_t sinks, void* work, void* stream);
+
 /* ---- status ---------------------------------------------------------- */
 const char* lq_status_string(lq_status s);
 /* Synchronises the current device, then reads and clears its device status
@@ -326,7 +430,8 @@ const char* lq_version(void);
  * lq_debug_route_count(r) counts launches taken by route r (r = 0 counts
  * the fast GEMV, r = 4 the decode chain, r = 6 the A pre-pass launches of
  * route 2, r = 7 the route-2 GEMMs run as CTA pairs); counters are
- * process-wide. */
+ * process-wide. Attention counts its kernels as 8 (generic), 9 (warp-level
+ * MMAs) and 10 (tcgen05). */
 lq_status lq_debug_force_route(int route);
 uint64_t  lq_debug_route_count(int route);
 void      lq_debug_reset_counts(void);
@@ -357,6 +462,10 @@ lq_status lq_debug_gemm_rings(int a_stages, int raw_stages);
  * default): never. Both give the same results; pairs measured slower, so
  * this is for comparisons. */
 void      lq_debug_gemm_pairs(int on);
+/* lq_attn_paged's kernel: 0 = automatic, 1 = generic (any geometry), 2 =
+ * rows of 8 on warp-level MMAs, 3 = tiles of 128 rows on tcgen05
+ * (LQ_ERR_UNSUPPORTED where the forced kernel does not take the geometry). */
+lq_status lq_debug_attn_route(int route);
 
 #ifdef __cplusplus
 }
