@@ -265,15 +265,13 @@ const char* lq_status_string(lq_status s) {
 
 lq_status lq_last_device_error(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return LQ_ERR_CUDA;
-  const unsigned a = read_clear_gemv_error();
-  const unsigned b = read_clear_gemm_error();
-  const unsigned c = read_clear_gemm_tma_error();
-  const unsigned d = read_clear_chain_error();
-  const unsigned e = read_clear_batch_error();
-  const unsigned f = read_clear_small_error();
-  const unsigned g = read_clear_kv_error();
-  const unsigned h = read_clear_attn_error();
-  const unsigned v = a ? a : (b ? b : (c ? c : (d ? d : (e ? e : (f ? f : (g ? g : h))))));
+  unsigned v = 0;  // the first error of any unit; all are cleared
+  for (unsigned (*read)() : {read_clear_gemv_error, read_clear_gemm_error, read_clear_gemm_tma_error, read_clear_chain_error,
+                             read_clear_batch_error, read_clear_small_error, read_clear_kv_error, read_clear_attn_error,
+                             read_clear_attn_warp_error}) {
+    const unsigned e = read();
+    v = v ? v : e;
+  }
   if (v == 0) return LQ_OK;
   return static_cast<lq_status>(v);
 }

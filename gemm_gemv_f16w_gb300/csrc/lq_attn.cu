@@ -158,7 +158,7 @@ size_t lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, in
   bool noop;
   if (kv_check(cache, batch, &noop) != LQ_OK) return 0;
   if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
-  return 16;
+  return attn_warp_work_bytes();
 }
 
 lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
@@ -190,6 +190,13 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   a.window = static_cast<int>(std::min(window, most));
   a.sinks = static_cast<int>(std::min(sinks, most));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int route = g_attn_route.load();
+  if (route == 3) return LQ_ERR_UNSUPPORTED;
+  if (route == 1) return launch_attn_generic(a, cache->fmt, s);
+  // the most rows of a sequence, as far as the host knows
+  const int64_t q = batch->max_q > 0 ? std::min(batch->max_q, batch->tokens) : batch->tokens;
+  const int rows = static_cast<int>(std::min<int64_t>(q * a.group, 1 << 30));
+  if (route == 2 || attn_warp_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   return launch_attn_generic(a, cache->fmt, s);
 }
 

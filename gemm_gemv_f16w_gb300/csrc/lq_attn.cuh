@@ -23,4 +23,16 @@ constexpr int kAttnRouteGeneric = 8, kAttnRouteWarp = 9, kAttnRouteTile = 10;
 
 lq_status launch_attn_generic(const AttnArgs& a, int fmt, cudaStream_t stream);
 
+// The work buffer: arrival counters (zero between calls), then partial results.
+constexpr int kAttnMaxCtas = 256;
+constexpr size_t kAttnCounterBytes = 4096;
+
+// Rows of 8 on warp-level MMAs (lq_attn_warp.cu); `rows`: the most rows
+// (tokens * group) a sequence is expected to have, small_rows: sequences with
+// more are left to another kernel (0: none are). LQ_ERR_UNSUPPORTED outside
+// its geometries.
+bool attn_warp_eligible(const AttnArgs& a);
+size_t attn_warp_work_bytes();
+lq_status launch_attn_warp(const AttnArgs& a, int fmt, int rows, int small_rows, void* work, cudaStream_t stream);
+
 }  // namespace lq
