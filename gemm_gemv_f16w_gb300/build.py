@@ -25,7 +25,7 @@ DEBUG_LIB = os.path.join(PKG, "liblq_debug.so")
 
 CUDA_SOURCES = ["lq_api.cu", "lq_gemv.cu", "lq_gemv_chain.cu", "lq_gemv_batch.cu", "lq_argmax.cu", "lq_topk.cu", "lq_gemm.cu", "lq_gemm_tma.cu",
                 "lq_noalloc.cu", "lq_gemm_small.cu", "lq_kv.cu", "lq_attn.cu",
-                "lq_attn_warp.cu"]
+                "lq_attn_warp.cu", "lq_attn_tile.cu"]
 CXX_SOURCES = ["lq_pack.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -268,7 +268,7 @@ lq_status lq_last_device_error(void) {
   unsigned v = 0;  // the first error of any unit; all are cleared
   for (unsigned (*read)() : {read_clear_gemv_error, read_clear_gemm_error, read_clear_gemm_tma_error, read_clear_chain_error,
                              read_clear_batch_error, read_clear_small_error, read_clear_kv_error, read_clear_attn_error,
-                             read_clear_attn_warp_error}) {
+                             read_clear_attn_warp_error, read_clear_attn_tile_error}) {
     const unsigned e = read();
     v = v ? v : e;
   }

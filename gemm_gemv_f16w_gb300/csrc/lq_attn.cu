@@ -24,6 +24,7 @@ std::atomic<int> g_attn_route{0};
 
 constexpr int kGWarps = 8;
 constexpr int kMaxDim = 256;
+constexpr int kAttnFewRows = 32;  // rows of a sequence up to which the warp-level kernel runs
 
 template <int FMT>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
@@ -158,7 +159,7 @@ size_t lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, in
   bool noop;
   if (kv_check(cache, batch, &noop) != LQ_OK) return 0;
   if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
-  return attn_warp_work_bytes();
+  return std::max(attn_warp_work_bytes(), attn_tile_work_bytes(cache->head_dim));
 }
 
 lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
@@ -174,7 +175,7 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   if (!Q || !O || !work || !aligned_to(Q, 4) || !aligned_to(O, 4) || !aligned_to(lse, 4) || !aligned_to(work, 16))
     return LQ_ERR_INVALID_ARG;
   if (ldq < width || ldo < width) return LQ_ERR_INVALID_ARG;
-  if (heads > 65536) return LQ_ERR_UNSUPPORTED;
+  if (heads > 65536 || batch->tokens * heads > (1LL << 31) - 1) return LQ_ERR_UNSUPPORTED;
   AttnArgs a = {};
   a.c = kv_cache_view(*cache);
   a.b = kv_batch_view(*batch);
@@ -191,13 +192,22 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   a.sinks = static_cast<int>(std::min(sinks, most));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int route = g_attn_route.load();
-  if (route == 3) return LQ_ERR_UNSUPPORTED;
   if (route == 1) return launch_attn_generic(a, cache->fmt, s);
-  // the most rows of a sequence, as far as the host knows
+  // the most rows (tokens x query heads a key/value head) of a sequence, as
+  // far as the host knows
   const int64_t q = batch->max_q > 0 ? std::min(batch->max_q, batch->tokens) : batch->tokens;
   const int rows = static_cast<int>(std::min<int64_t>(q * a.group, 1 << 30));
-  if (route == 2 || attn_warp_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
-  return launch_attn_generic(a, cache->fmt, s);
+  if (route == 2) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
+  if (route == 3) return launch_attn_tile(a, cache->fmt, 0, work, s);
+  if (!attn_warp_eligible(a)) return launch_attn_generic(a, cache->fmt, s);
+  if (rows <= kAttnFewRows || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
+  // one sequence: all of it is one kernel's; else each kernel takes its own
+  const int split = a.b.batch > 1 ? kAttnFewRows : 0;
+  if (split) {
+    st = launch_attn_warp(a, cache->fmt, split, split, work, s);
+    if (st != LQ_OK) return st;
+  }
+  return launch_attn_tile(a, cache->fmt, split, work, s);
 }
 
 lq_status lq_debug_attn_route(int route) {

@@ -35,4 +35,10 @@ bool attn_warp_eligible(const AttnArgs& a);
 size_t attn_warp_work_bytes();
 lq_status launch_attn_warp(const AttnArgs& a, int fmt, int rows, int small_rows, void* work, cudaStream_t stream);
 
+// Tiles of 128 rows on tcgen05 (lq_attn_tile.cu); sequences with at most
+// small_rows rows are left to another kernel (0: none are).
+bool attn_tile_eligible(const AttnArgs& a);
+size_t attn_tile_work_bytes(int head_dim);
+lq_status launch_attn_tile(const AttnArgs& a, int fmt, int small_rows, void* work, cudaStream_t stream);
+
 }  // namespace lq

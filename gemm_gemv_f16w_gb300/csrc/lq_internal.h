@@ -110,6 +110,7 @@ unsigned read_clear_small_error();
 unsigned read_clear_kv_error();
 unsigned read_clear_attn_error();
 unsigned read_clear_attn_warp_error();
+unsigned read_clear_attn_tile_error();
 
 lq_status cuda_status(cudaError_t e);
 
