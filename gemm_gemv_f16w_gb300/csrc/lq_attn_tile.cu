@@ -84,7 +84,7 @@ struct Geo {
   static constexpr int SMEM = Q + NU * UNIT + 1024 + 1024;  // alignment, barriers
   static constexpr int SLOT = kRows * (D + 2);             // floats of a partial result
   // registers a thread of the warpgroups: together the launch's 4 * 128
-  static constexpr int REG_SOFTMAX = D == 128 ? 200 : 168, REG_LOAD = D == 128 ? 80 : 128, REG_MMA = D == 128 ? 32 : 48;
+  static constexpr int REG_SOFTMAX = D == 128 ? 200 : 168, REG_LOAD = D == 128 ? 72 : 128, REG_MMA = D == 128 ? 40 : 48;
   static_assert(2 * REG_SOFTMAX + REG_LOAD + REG_MMA <= 512);
 };
 
@@ -129,6 +129,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// One lane of a converged warp, the same every time; the compiler knows that
+// it is one, and keeps the MMAs' descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -141,6 +148,23 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const float2 f = __half22float2(h);
   hi = h2(h);
   lo = h2(__floats2half2_rn(x - f.x, y - f.y));
+}
+// Four int8 codes (a word) as two f16 pairs: (code + 128) in the mantissa of
+// 1024, less 1152; both steps are exact.
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  const __half2 bias = __half2half2(__ushort_as_half(0xE480));  // -1152
+  w ^= 0x80808080u;
+  p0 = h2(__hadd2(as_h2(__byte_perm(w, 0x64646464u, 0x4140)), bias));
+  p1 = h2(__hadd2(as_h2(__byte_perm(w, 0x64646464u, 0x4342)), bias));
+}
+// The nibbles of four bytes, less 8, as f16 pairs: low nibbles, high nibbles.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& l0, uint32_t& l1, uint32_t& h0, uint32_t& h1) {
+  const __half2 bias = __half2half2(__ushort_as_half(0xE408));  // -1032
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  l0 = h2(__hadd2(as_h2(__byte_perm(lo, 0x64646464u, 0x4140)), bias));
+  l1 = h2(__hadd2(as_h2(__byte_perm(lo, 0x64646464u, 0x4342)), bias));
+  h0 = h2(__hadd2(as_h2(__byte_perm(hi, 0x64646464u, 0x4140)), bias));
+  h1 = h2(__hadd2(as_h2(__byte_perm(hi, 0x64646464u, 0x4342)), bias));
 }
 // The exact split of a dequantised pair: hi toward zero, lo the rest.
 __device__ __forceinline__ void split2_rz(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -369,39 +393,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
       const int head = w.h * a.group + (row ? rho % a.group : 0);
       const int pos = w.s.len - w.s.rows + min(rho, rows_all - 1) / a.group;
       float om[D], M = kNoMax, l = 0.0f, f = 0.0f;
+      const long long src_off = t * a.ldq + static_cast<long long>(head) * D;
       if (active) {
-        // the row's query, scaled to the top of f16's range, in two parts
-        const float* src = a.Q + t * a.ldq + static_cast<long long>(head) * D;
-        float top = 0.0f;
-#pragma unroll
-        for (int d = 0; d < D; d += 4) {
+        // the warp's 32 query rows, one or two at a time: scaled to the top of
+        // f16's range, in two parts
+        constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes a row, rows at a time
+        const int sub = lane / LPR, l4 = lane % LPR;
+        const uint32_t live = __ballot_sync(0xffffffffu, row);
+        const uint32_t col = (l4 >> 4) * G::GROUP + (l4 & 1) * 8;  // column group, half of a 16-byte chunk
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int rr = r0 + sub;
+          const float* src = a.Q + __shfl_sync(0xffffffffu, src_off, rr) + l4 * 4;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (row) {
+          if ((live >> rr) & 1u) {
             if (P.vec_q) {
-              v = ldg128f(src + d);
+              v = ldg128f(src);
             } else {
-              v = make_float4(src[d], src[d + 1], src[d + 2], src[d + 3]);
+              v = make_float4(src[0], src[1], src[2], src[3]);
             }
           }
-          om[d] = v.x;
-          om[d + 1] = v.y;
-          om[d + 2] = v.z;
-          om[d + 3] = v.w;
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        }
-        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-        const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
-        const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
-        f = fabsf(a.scale) * kLog2e / sigma;
+          float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            split2(om[c * 8 + 2 * j] * (sigma * sign), om[c * 8 + 2 * j + 1] * (sigma * sign), hi[j], lo[j]);
-          const uint32_t at = (c >> 3) * G::GROUP + tc::sw128_offset(r, c & 7);
-          *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(q_lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+          const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
+          const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
+          const float fr = __shfl_sync(0xffffffffu, fabsf(a.scale) * kLog2e / sigma, (lane % RPI) * LPR);
+          if (lane / RPI == r0 / RPI) f = fr;
+          uint2 hi, lo;
+          split2(v.x * (sigma * sign), v.y * (sigma * sign), hi.x, lo.x);
+          split2(v.z * (sigma * sign), v.w * (sigma * sign), hi.y, lo.y);
+          const uint32_t at = col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
+          *reinterpret_cast<uint2*>(q_hi + at) = hi;
+          *reinterpret_cast<uint2*>(q_lo + at) = lo;
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar->q_ready[q]);
@@ -424,35 +449,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
           const int key = j0 + j;
           return ((pages >> (j >> 4)) & 1u) && key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
         };
-        auto logits = [&](int j, uint32_t (&s)[16]) {  // raw sums of keys j .. j + 15
+        // raw sums of keys j .. j + 15: asked for, and (after wait_ld) put together
+        auto ask = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16]) {
           tmem_ld16(s_at + j, s);
+          if constexpr (QUANT) tmem_ld16(s_at + 64 + j, s2);
+        };
+        auto sum = [&](uint32_t (&s)[16], uint32_t (&s2)[16]) {
           if constexpr (QUANT) {
-            uint32_t s2[16];
-            tmem_ld16(s_at + 64 + j, s2);
-            tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(s2[i]));
-          } else {
-            tc::wait_ld();
+            for (int i = 0; i < 16; i += 2) {
+              const float2 x = fadd2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                     make_float2(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1])));
+              s[i] = __float_as_uint(x.x);
+              s[i + 1] = __float_as_uint(x.y);
+            }
           }
         };
+        uint32_t sa[16], sb[16], sa2[16], sb2[16];  // two chunks in turn
         float top = -INFINITY;
-        if (!edge) {
-#pragma unroll
-          for (int j = 0; j < KT; j += 16) {
-            uint32_t s[16];
-            logits(j, s);
+        auto largest = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16], bool masked) {
+          sum(s, s2);
+          if (!masked) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sees(j + i) ? __uint_as_float(s[i]) * f : -INFINITY);
+          }
+        };
+        if (!edge) {
+          ask(0, sa, sa2);
+#pragma unroll
+          for (int j = 0; j < KT; j += 32) {
+            tc::wait_ld();
+            ask(j + 16, sb, sb2);
+            largest(j, sa, sa2, false);
+            tc::wait_ld();
+            if (j + 32 < KT) ask(j + 32, sa, sa2);
+            largest(j + 16, sb, sb2, false);
           }
           top *= f;
         } else {
 #pragma unroll 1
           for (int j = 0; j < KT; j += 16) {
-            uint32_t s[16];
-            logits(j, s);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sees(j + i) ? __uint_as_float(s[i]) * f : -INFINITY);
+            ask(j, sa, sa2);
+            tc::wait_ld();
+            largest(j, sa, sa2, true);
           }
         }
         float keep = 1.0f;
@@ -463,40 +505,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
           l *= keep;
         }
         // weights, in two parts, over the logits: 16 columns a 16 keys
-        auto weights = [&](int j, bool masked) {
-          uint32_t s[16], w16[16];
-          logits(j, s);
+        const float2 ff = make_float2(f, f), mm = make_float2(-M, -M);
+        float2 l2 = make_float2(0.0f, 0.0f);
+        auto weights = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16], bool masked) {
+          sum(s, s2);
+          uint32_t w16[16];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(s[i]), f, -M)), p1 = ex2(fmaf(__uint_as_float(s[i + 1]), f, -M));
+            const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
+            float2 p = make_float2(ex2(x.x), ex2(x.y));
             if (masked) {
-              p0 = sees(j + i) ? p0 : 0.0f;
-              p1 = sees(j + i + 1) ? p1 : 0.0f;
+              p.x = sees(j + i) ? p.x : 0.0f;
+              p.y = sees(j + i + 1) ? p.y : 0.0f;
             }
-            l += p0 + p1;
-            split2(p0, p1, w16[i / 2], w16[8 + i / 2]);
+            l2 = fadd2(l2, p);
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            const float2 hf = __half22float2(h);
+            const float2 r2 = fadd2(p, make_float2(-hf.x, -hf.y));
+            w16[i / 2] = h2(h);
+            w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
           }
           tmem_st16(s_at + j, w16);
         };
         if (!edge) {
+          ask(0, sa, sa2);
 #pragma unroll
-          for (int j = 0; j < KT; j += 16) weights(j, false);
+          for (int j = 0; j < KT; j += 32) {
+            tc::wait_ld();
+            ask(j + 16, sb, sb2);
+            weights(j, sa, sa2, false);
+            tc::wait_ld();
+            if (j + 32 < KT) ask(j + 32, sa, sa2);
+            weights(j + 16, sb, sb2, false);
+          }
         } else {
 #pragma unroll 1
-          for (int j = 0; j < KT; j += 16) weights(j, true);
+          for (int j = 0; j < KT; j += 16) {
+            ask(j, sa, sa2);
+            tc::wait_ld();
+            weights(j, sa, sa2, true);
+          }
         }
+        l += l2.x + l2.y;
         tc::wait_st();
         tc::fence_before_sync();
         mbar_arrive(&bar->p_ready[q]);
         if (!wait(&bar->o_full[q], parity)) goto out;
         tc::fence_after_sync();
+        {
+          const float2 kk = make_float2(keep, keep);
+          auto add = [&](int d, const uint32_t (&o)[16]) {
 #pragma unroll
-        for (int d = 0; d < D; d += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_at + d, o);
-          tc::wait_ld();
+            for (int i = 0; i < 16; i += 2) {
+              const float2 x = ffma2(make_float2(om[d + i], om[d + i + 1]), kk, make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])));
+              om[d + i] = x.x;
+              om[d + i + 1] = x.y;
+            }
+          };
+          tmem_ld16(o_at, sa);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) om[d + i] = fmaf(om[d + i], keep, __uint_as_float(o[i]));
+          for (int d = 0; d < D; d += 32) {
+            tc::wait_ld();
+            tmem_ld16(o_at + d + 16, sb);
+            add(d, sa);
+            tc::wait_ld();
+            if (d + 32 < D) tmem_ld16(o_at + d + 32, sa);
+            add(d + 16, sb);
+          }
         }
         tc::fence_before_sync();
         // values that are not finite reach the rows that see them here
@@ -522,27 +597,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
       }
       {
         // ---- the unit's result, or its part -------------------------------------
-        auto write_row = [&](float sum) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // 0: the row sees nothing; NaN stays
-          float* out = a.O + t * a.ldo + static_cast<long long>(head) * D;
-          if (!LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads)) return;
+        // rows go out through the query rows' shared memory (their MMAs are done; a
+        // warp's rows of all parts are its own): whole rows, 16 bytes a lane
+        auto write_rows = [&]() {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing; NaN stays
+          __syncwarp();
 #pragma unroll
-          for (int d = 0; d < D; d += 4) {
-            const float4 v = make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
-            if (P.vec_o) {
-              *reinterpret_cast<float4*>(out + d) = v;
-            } else {
-              out[d] = v.x;
-              out[d + 1] = v.y;
-              out[d + 2] = v.z;
-              out[d + 3] = v.w;
+          for (int d = 0; d < D; d += 4)
+            *reinterpret_cast<float4*>(q_hi + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
+                make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
+          __syncwarp();
+          constexpr int LPR = D / 4, RPI = 32 / LPR;
+          const int sub = lane / LPR, l4 = lane % LPR;
+          const uint32_t live = __ballot_sync(0xffffffffu, row && LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads));
+          const long long off = t * a.ldo + static_cast<long long>(head) * D;
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += RPI) {
+            const int rr = r0 + sub;
+            float* out = a.O + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
+            const float4 v =
+                *reinterpret_cast<const float4*>(q_hi + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
+            if ((live >> rr) & 1u) {
+              if (P.vec_o) {
+                *reinterpret_cast<float4*>(out) = v;
+              } else {
+                out[0] = v.x;
+                out[1] = v.y;
+                out[2] = v.z;
+                out[3] = v.w;
+              }
             }
           }
-          if (a.lse) a.lse[static_cast<long long>(t) * a.heads + head] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+          if (row && a.lse) a.lse[static_cast<long long>(t) * a.heads + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
         };
         const bool whole = w.k0 == 0 && w.k1 == w.n;
         if (whole) {
-          if (row) write_row(l);
+          if (active) write_rows();
         } else {
           // the unit's CTAs are c0 .. c1; c0's slot 2 c0 + 1, the others' 2 c
           const long long unit_x = x0 + (mine - walk.left) - w.k0;
@@ -567,14 +657,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
           }
           mbar_arrive(&bar->join);
           if (!wait(&bar->join, joins++ & 1u)) goto out;
-          if (bar->last && row) {
+          if (bar->last && active) {
             __threadfence();
             M = kNoMax;
-            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + D * kRows + rr));
+            for (int c = c0; row && c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + D * kRows + rr));
             l = 0.0f;
 #pragma unroll
             for (int d = 0; d < D; ++d) om[d] = 0.0f;
-            for (int c = c0; c <= c1; ++c) {
+            for (int c = c0; row && c <= c1; ++c) {
               const float* from = slot_of(c);
               const float scale = ex2(__ldcg(from + D * kRows + rr) - M);
               l = fmaf(scale, __ldcg(from + (D + 1) * kRows + rr), l);
@@ -587,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 om[d + 3] = fmaf(scale, v.w, om[d + 3]);
               }
             }
-            write_row(l);
+            write_rows();
           }
         }
       }
@@ -646,19 +736,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     while (on && alive) {
       const Work& w = walk.w;
       const kv::Visible v0 = kv::visible(max(w.p0, 0), a.window, a.sinks);
+      auto group_at = [&](int j) -> long long {
+        const int key = j + lane * 16;
+        const int page = lane < KT / 16 ? kv::page_of(a.c, a.b, w.i, key) : -1;
+        return page < 0 ? -1 : page * a.c.page_bytes + w.h * a.c.head_bytes + static_cast<long long>(key % a.c.page_size) * G::ROW;
+      };
+      long long ahead = -1;
       for (int k = w.k0; k < w.k1 && alive; ++k, ++tile) {
         const int j0 = walk.key_of(k);
-        // pages of the tile's groups of 16 keys, one lane each
-        int page = -1;
-        if (lane < KT / 16) page = kv::page_of(a.c, a.b, w.i, j0 + lane * 16);
-        const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0);
+        // the tile's groups of 16 keys, one lane each: where their rows begin (-1: nowhere)
+        const long long base = k == w.k0 ? group_at(j0) : ahead;
+        if (k + 1 < w.k1) ahead = group_at(walk.key_of(k + 1));
+        const uint32_t pages = __ballot_sync(0xffffffffu, base >= 0);
         const bool mixed = w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && (a.window == 0 || j0 > w.p1 - a.window || j0 + KT <= a.sinks));
         if (tl == 0) {
           bar->info[tile % kInfo] = make_int2(
               j0, static_cast<int>(pages | (w.rt * kRows + 128 < w.s.rows * a.group ? kTwo : 0u) | (k == w.k0 ? kFirst : 0u)));
           for (int j = 0; j < 4; ++j) bar->bad[(tile + kInfo / 2) % kInfo][j] = 0;
         }
-        auto some_row_sees = [&](int key) { return key <= w.p1 && (key >= v0.begin || key < v0.sink_end); };
+        const bool all = pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= w.p1 && (j0 >= v0.begin || j0 + KT <= v0.sink_end);
+        auto some_row_sees = [&](int key) { return all || (key <= w.p1 && (key >= v0.begin || key < v0.sink_end)); };
         if constexpr (!QUANT) {
           constexpr int CH = D / 8, PASS = kLoaders / CH, N = KT / PASS;  // chunks a row, rows a pass, passes
           const int row0 = tl / CH, ch = tl % CH;
@@ -674,15 +771,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
               break;
             }
             const unsigned char* pool = side ? a.c.v : a.c.k;
-            const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::GROUP;
+            const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::GROUP + tc::sw128_offset(row0, ch & 7);
+            const unsigned char* const src = pool + row0 * G::ROW + ch * 16;
 #pragma unroll 4
-            for (int n = 0; n < N; ++n) {
-              const int row = row0 + n * PASS;
-              const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-              const int slot = (j0 + row) % a.c.page_size;
-              const bool there = pg >= 0 && some_row_sees(j0 + row) && LQ_IN_BOUNDS(pg < a.c.num_pages && w.h < a.c.kv_heads);
-              copy16(dst + tc::sw128_offset(row, ch & 7),
-                     pool + max(pg, 0) * a.c.page_bytes + w.h * a.c.head_bytes + static_cast<long long>(slot) * G::ROW + ch * 16, there);
+            for (int n = 0; n < N; ++n) {  // rows row0 + n PASS: the same place in a swizzle atom, one group of 16 a pass
+              const long long at = __shfl_sync(0xffffffffu, base, n * PASS / 16);
+              const bool there = at >= 0 && some_row_sees(j0 + row0 + n * PASS);
+              copy16(dst + n * PASS * 128, src + max(at, 0ll) + (n * PASS % 16) * G::ROW, there);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (pending) {
@@ -702,26 +797,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
           uint4 raw[2][N];
           __half sc[2][N];
 #pragma unroll
-          for (int side = 0; side < 2; ++side)
+          for (int n = 0; n < N; ++n) {  // PASS = 16 or 32 rows a pass
+            const int row = row0 + n * PASS;
+            const long long at = __shfl_sync(0xffffffffu, base, row >> 4);
+            const bool there = at >= 0 && some_row_sees(j0 + row);
+            // the scales lie after the page's codes: slot * D / 32 of them in
+            const long long slot = (j0 + (row & ~15)) % a.c.page_size;
+            const long long sat = at - slot * G::ROW + static_cast<long long>(a.c.page_size) * G::ROW + (slot + (row & 15)) * (D / 16) + (ch >> 1) * 2;
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-              const int row = row0 + n * PASS;
-              const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-              const int slot = (j0 + row) % a.c.page_size;
+            for (int side = 0; side < 2; ++side) {
               raw[side][n] = make_uint4(0u, 0u, 0u, 0u);
               sc[side][n] = __ushort_as_half(0);
-              if (pg >= 0 && some_row_sees(j0 + row) && LQ_IN_BOUNDS(pg < a.c.num_pages && w.h < a.c.kv_heads)) {
-                const unsigned char* at = (side ? a.c.v : a.c.k) + pg * a.c.page_bytes + w.h * a.c.head_bytes;
+              const unsigned char* pool = side ? a.c.v : a.c.k;
+              if (there) {
                 if constexpr (FMT == LQ_FMT_Q8_0) {
-                  raw[side][n] = *reinterpret_cast<const uint4*>(at + static_cast<long long>(slot) * G::ROW + ch * 16);
+                  raw[side][n] = *reinterpret_cast<const uint4*>(pool + at + (row & 15) * G::ROW + ch * 16);
                 } else {
-                  const uint2 x = *reinterpret_cast<const uint2*>(at + static_cast<long long>(slot) * G::ROW + ch * 8);
+                  const uint2 x = *reinterpret_cast<const uint2*>(pool + at + (row & 15) * G::ROW + ch * 8);
                   raw[side][n].x = x.x;
                   raw[side][n].y = x.y;
                 }
-                sc[side][n] = reinterpret_cast<const __half*>(at + static_cast<long long>(a.c.page_size) * G::ROW)[slot * (D / 32) + ch / 2];
+                sc[side][n] = *reinterpret_cast<const __half*>(pool + sat);
               }
             }
+          }
           for (int side = 0; side < 2; ++side, ++unit) {
             if (!wait(&bar->empty[unit % NU], ((unit / NU) & 1u) ^ 1u)) {
               alive = false;
@@ -731,9 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
 #pragma unroll
             for (int n = 0; n < N; ++n) {
               const int row = row0 + n * PASS;
-              float d = __half2float(side ? sc[1][n] : sc[0][n]);
-              if (side == 1 && mixed && !(fabsf(d) <= 65504.0f)) {
-                d = 0.0f;
+              __half d = side ? sc[1][n] : sc[0][n];
+              if (side == 1 && mixed && !(fabsf(__half2float(d)) <= 65504.0f)) {
+                d = __ushort_as_half(0);
                 atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
               }
               const uint4 x = side ? raw[1][n] : raw[0][n];
@@ -741,15 +840,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
               uint32_t hi[8], lo[8];
               if constexpr (FMT == LQ_FMT_Q8_0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const uint32_t u = w4[i >> 1] ^ 0x80808080u;
-                  split2_rz((s8_to_magic(u, 2 * (i & 1)) - kMagicS8) * d, (s8_to_magic(u, 2 * (i & 1) + 1) - kMagicS8) * d, hi[i], lo[i]);
-                }
-              } else {
+                for (int i = 0; i < 4; ++i) codes8(w4[i], hi[2 * i], hi[2 * i + 1]);
+              } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // 0..3 low nibbles, 4..7 high ones
-                  const uint32_t u = (i < 4 ? w4[(i & 3) >> 1] : w4[(i & 3) >> 1] >> 4) & 0x0F0F0F0Fu;
-                  split2_rz((s8_to_magic(u, 2 * (i & 1)) - kMagicQ4) * d, (s8_to_magic(u, 2 * (i & 1) + 1) - kMagicQ4) * d, hi[i], lo[i]);
+                for (int i = 0; i < 2; ++i) codes4(w4[i], hi[2 * i], hi[2 * i + 1], hi[4 + 2 * i], hi[4 + 2 * i + 1]);
+              }
+              const __half2 d2 = __half2half2(d);
+              if (!(fabsf(__half2float(d)) >= (FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f))) {
+                // code * d in f16, and what it leaves: exact by the fused multiply-add
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const __half2 c2 = as_h2(hi[i]), prod = __hmul2_rn(c2, d2);
+                  hi[i] = h2(prod);
+                  lo[i] = h2(__hfma2(c2, d2, __hneg2(prod)));
+                }
+              } else {  // the top of f16's range: rounded toward zero, through f32
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float2 c2 = __half22float2(as_h2(hi[i]));
+                  const float df = __half2float(d);
+                  split2_rz(c2.x * df, c2.y * df, hi[i], lo[i]);
                 }
               }
               // 16-byte chunks of the row: the second column group's threads start with their second
@@ -780,79 +890,99 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
       constexpr uint32_t kQK = tc::idesc_f16_f32(128, 128);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
       const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
-      uint32_t unit = 0;
-      uint32_t units0 = 0, units1 = 0, tiles0 = 0, tiles1 = 0;  // units begun, tiles done by a row tile
+      uint32_t seen[2] = {0, 0}, units[2] = {0, 0};  // tiles, units of a row tile
       bool alive = true;
-      for (uint32_t tile = 0; tile < mine && alive; ++tile) {
-        // S = Q K^T
-        if (!wait(&bar->full[unit % NU], (unit / NU) & 1u)) break;
-        const uint32_t flags = static_cast<uint32_t>(bar->info[tile % kInfo].y);
-        const int nq = flags & kTwo ? 2 : 1;
+      auto at_unit = [&](uint32_t u) { return ring_at + (u % NU) * G::UNIT; };
+      // S = Q K^T of row tile q with the keys of ring unit u
+      auto qk = [&](int q, uint32_t u, bool first) {
+        if (first) alive = wait(&bar->q_ready[q], (q ? units[1]++ : units[0]++) & 1u);
+        if (!alive) return;
+        tc::fence_after_sync();
+        if (elect_one()) {
+          const uint64_t b0 = tc::desc_sw128_kmajor(at_unit(u));
+          const uint64_t a0 = tc::desc_sw128_kmajor(q_at + q * 2 * G::QPART);
 #pragma unroll 1
-        for (int q = 0; q < nq; ++q) {
-          if (flags & kFirst) {
-            alive = wait(&bar->q_ready[q], (q ? units1 : units0) & 1u);
-            if (q) ++units1; else ++units0;
-          }
-          // the previous tile's PV has read P, which S overwrites
-          const uint32_t before = q ? tiles1 : tiles0;
-          if (alive && before > 0) alive = wait(&bar->o_full[q], (before - 1) & 1u);
-          if (!alive) break;
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint64_t b0 = tc::desc_sw128_kmajor(ring_at + (unit % NU) * G::UNIT);
-            const uint64_t a0 = tc::desc_sw128_kmajor(q_at + q * 2 * G::QPART);
-#pragma unroll
-            for (int part = 1; part >= 0; --part)  // low parts first
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                const uint32_t off = (c >> 2) * G::GROUP + (c & 3) * 32;
-                tc::mma_bf16(tmem + q * 128, a0 + ((part * G::QPART + off) >> 4), b0 + (off >> 4), kQK, part == 1 && c == 0 ? 0u : 1u);
-              }
-            tc::commit(&bar->s_full[q]);
-            mbar_arrive(&bar->s_full[q]);
-          }
-          __syncwarp();
-        }
-        if (!alive) break;
-        if (lane == 0) tc::commit(&bar->empty[unit % NU]);
-        __syncwarp();
-        ++unit;
-        // O = P V
-        if (!wait(&bar->full[unit % NU], (unit / NU) & 1u)) break;
-#pragma unroll 1
-        for (int q = 0; q < nq; ++q) {
-          alive = wait(&bar->p_ready[q], (q ? tiles1 : tiles0) & 1u);
-          if (!alive) break;
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint64_t b0 = desc_mn(ring_at + (unit % NU) * G::UNIT);
-            const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
-            constexpr int KS = KT / 16;
-#pragma unroll
-            for (int c = 0; c < KS; ++c)  // p_lo v_hi
-              tc::mma_f16_ts(o, p + 16 * c + 8, b0 + c * 128, kPV, c == 0 ? 0u : 1u);
-            if constexpr (QUANT) {
-#pragma unroll
-              for (int c = 0; c < KS; ++c)  // p_hi v_lo
-                tc::mma_f16_ts(o, p + 16 * c, b0 + (KS + c) * 128, kPV, 1u);
+          for (int part = 1; part >= 0; --part)  // low parts first
+#pragma unroll 4
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t off = (c >> 2) * G::GROUP + (c & 3) * 32;
+              tc::mma_bf16(tmem + q * 128, a0 + ((part * G::QPART + off) >> 4), b0 + (off >> 4), kQK, part == 1 && c == 0 ? 0u : 1u);
             }
-#pragma unroll
-            for (int c = 0; c < KS; ++c)  // p_hi v_hi
-              tc::mma_f16_ts(o, p + 16 * c, b0 + c * 128, kPV, 1u);
-            tc::commit(&bar->o_full[q]);
-            mbar_arrive(&bar->o_full[q]);
-          }
-          __syncwarp();
-          if (q) ++tiles1; else ++tiles0;
+          tc::commit(&bar->s_full[q]);
+          mbar_arrive(&bar->s_full[q]);
         }
-        if (!alive) break;
-        if (lane == 0) tc::commit(&bar->empty[unit % NU]);
         __syncwarp();
-        ++unit;
+      };
+      // O = P V of row tile q with the values of ring unit u
+      auto pv = [&](int q, uint32_t u) {
+        alive = wait(&bar->p_ready[q], (q ? seen[1]++ : seen[0]++) & 1u);
+        if (!alive) return;
+        tc::fence_after_sync();
+        if (elect_one()) {
+          const uint64_t b0 = desc_mn(at_unit(u));
+          const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
+          constexpr int KS = KT / 16;
+#pragma unroll 4
+          for (int c = 0; c < KS; ++c)  // p_lo v_hi
+            tc::mma_f16_ts(o, p + 16 * c + 8, b0 + c * 128, kPV, c == 0 ? 0u : 1u);
+          if constexpr (QUANT) {
+#pragma unroll 4
+            for (int c = 0; c < KS; ++c)  // p_hi v_lo
+              tc::mma_f16_ts(o, p + 16 * c, b0 + (KS + c) * 128, kPV, 1u);
+          }
+#pragma unroll 4
+          for (int c = 0; c < KS; ++c)  // p_hi v_hi
+            tc::mma_f16_ts(o, p + 16 * c, b0 + c * 128, kPV, 1u);
+          tc::commit(&bar->o_full[q]);
+          mbar_arrive(&bar->o_full[q]);
+        }
+        __syncwarp();
+      };
+      auto filled = [&](uint32_t u) { return wait(&bar->full[u % NU], (u / NU) & 1u); };
+      auto release = [&](uint32_t u) {
+        if (elect_one()) tc::commit(&bar->empty[u % NU]);
+        __syncwarp();
+      };
+      // Order: PV of a row tile, then its next QK, while the other's softmax
+      // runs. MMAs of one thread run in order, so that QK may overwrite the P
+      // that the PV before it reads. Between units both PVs come first: the
+      // next queries are written when both row tiles are done.
+      uint32_t flags = 0;
+      if (mine > 0) {
+        alive = filled(0);
+        if (alive) {
+          flags = static_cast<uint32_t>(bar->info[0].y);
+          qk(0, 0, true);
+          if (alive && (flags & kTwo)) qk(1, 0, true);
+          if (alive) release(0);
+        }
+      }
+#pragma unroll 1
+      for (uint32_t tile = 0; tile < mine && alive; ++tile) {
+        const uint32_t v = 2 * tile + 1, k = v + 1;
+        const bool two = (flags & kTwo) != 0, more = tile + 1 < mine;
+        alive = filled(v);
+        if (alive) pv(0, v);
+        if (!alive) break;
+        uint32_t next = 0;
+        if (more) {
+          alive = filled(k);
+          if (!alive) break;
+          next = static_cast<uint32_t>(bar->info[(tile + 1) % kInfo].y);
+          if (!(next & kFirst)) qk(0, k, false);
+        }
+        if (alive && two) pv(1, v);
+        if (!alive) break;
+        release(v);
+        if (more) {
+          if (next & kFirst) qk(0, k, true);
+          if (alive && (next & kTwo)) qk(1, k, (next & kFirst) != 0);
+          if (alive) release(k);
+          flags = next;
+        }
       }
       // everything issued has to be done before the tensor memory is freed
-      if (lane == 0) tc::commit(&bar->drain);
+      if (elect_one()) tc::commit(&bar->drain);
       __syncwarp();
       mbar_wait(&bar->drain, 0, kDrainWaitNs);
     }
