@@ -187,7 +187,7 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   a.heads = static_cast<int>(heads);
   a.group = static_cast<int>(heads / cache->kv_heads);
   a.scale = scale;
-  const int64_t most = (1LL << 31) - 1;
+  const int64_t most = 1LL << 30;  // past every position (kv_check)
   a.window = static_cast<int>(std::min(window, most));
   a.sinks = static_cast<int>(std::min(sinks, most));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -37,9 +37,15 @@
 // the order of the keys.
 // Every wait is bounded; on timeout the kernel records LQ_ERR_DEVICE_TIMEOUT,
 // lets its copies and MMAs finish, frees TMEM and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstddef>
+#include <cstring>
+#include <type_traits>
 
 #include "lq_attn.cuh"
 #include "lq_tcgen05.cuh"
@@ -54,7 +60,8 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;          // query rows of a unit: two tiles of 128
 constexpr int kLoaders = 128;       // loader threads
 constexpr int kMinTiles = 4;        // key tiles worth a CTA
-constexpr int kInfo = 16;           // tiles of bookkeeping kept
+constexpr int kInfo = 8;            // tiles of bookkeeping kept
+constexpr int kUnits = 8;           // units of bookkeeping kept
 constexpr int kMaxBatch = 4096;     // sequences whose totals fit in shared memory
 constexpr float kNoMax = -1e30f;    // M before the first key
 constexpr float kLift = 11.0f;
@@ -67,6 +74,7 @@ struct TileParams {
   float* parts;
   int small_rows;  // sequences with at most this many rows are another kernel's
   int vec_q, vec_o;
+  int tma;         // f16: the tensor maps of the pools are there
   unsigned long long wait_ns;
   unsigned wait_iters;
 };
@@ -81,30 +89,58 @@ struct Geo {
   static constexpr int NU = D == 128 ? 3 : 6;              // ring of units
   static constexpr int QPART = HALVES * GROUP;             // hi or lo of a row tile
   static constexpr int Q = 4 * QPART;                      // [row tile][hi, lo]
-  static constexpr int SMEM = Q + NU * UNIT + 1024 + 1024;  // alignment, barriers
+  static constexpr int SMEM = Q + NU * UNIT + 1024 + 2048;  // alignment, barriers
   static constexpr int SLOT = kRows * (D + 2);             // floats of a partial result
   // registers a thread of the warpgroups: together the launch's 4 * 128
   static constexpr int REG_SOFTMAX = D == 128 ? 200 : 168, REG_LOAD = D == 128 ? 72 : 128, REG_MMA = D == 128 ? 40 : 48;
   static_assert(2 * REG_SOFTMAX + REG_LOAD + REG_MMA <= 512);
 };
 
+// What the loaders know of a unit and tell the softmax threads.
+struct UnitInfo {
+  int tiles;         // key tiles of it here; 0: no more units
+  int rho0, rows;    // its first row, and all rows of its sequence and head
+  int row0, pos0;    // the sequence's first row of the call, and that row's position
+  int head0;         // the first query head
+  int seq, kv_head;
+  int c0, c1, slot;  // the CTAs it spans and this one's slot of partial sums; c0 == c1: it is whole here
+  int pad;
+};
+
+// What the planning warp knows of a key tile and tells the loaders and, through
+// the MMAs' barriers, the softmax threads.
+struct TileInfo {
+  int j0;                     // first key
+  uint32_t flags;
+  int p1, begin, sink_end;    // keys that rows of the unit see: [begin, p1] and [0, sink_end)
+  // where the rows of each group of 16 keys begin: f16 their row of the pool,
+  // quantised the byte offsets of codes and scales (2 entries a group); -1: nowhere
+  alignas(16) long long at[8];
+};
+static_assert(offsetof(TileInfo, at) % 16 == 0 && sizeof(TileInfo) % 16 == 0);
+
 struct Bars {
   uint64_t full[6], empty[6];
   uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
+  uint64_t unit[kUnits], unit_free[kUnits];
+  uint64_t join;  // the softmax threads of a unit that spans CTAs
   uint64_t drain;
   uint32_t tmem;
   volatile int abort;
   int last;
   int start_i, start_h, start_rt, start_k;
-  long long total;
-  uint64_t join;             // the softmax threads of a unit that spans CTAs
-  // first key; bit g: the page of keys 16 g .. is there, kTwo, kFirst
-  int2 info[kInfo];
-  uint32_t bad[kInfo][4];    // keys whose values are not finite (kept out of the MMA)
+  long long per, mine;
+  uint64_t told[kInfo], done[kInfo];   // a tile is described / its units are filled
+  alignas(16) TileInfo info[kInfo];
+  alignas(16) uint32_t bad[kInfo][4];  // keys whose values are not finite (kept out of the MMA)
+  alignas(16) UnitInfo units[kUnits];
 };
-static_assert(sizeof(Bars) <= 1024);
-constexpr uint32_t kTwo = 1u << 8;    // both row tiles of the unit have rows
-constexpr uint32_t kFirst = 1u << 9;  // the unit's first tile here
+static_assert(sizeof(Bars) <= 2048 && offsetof(Bars, info) % 16 == 0 && offsetof(Bars, bad) % 16 == 0);
+// TileInfo.flags: bit g < 8: the page of keys 16 g .. is there
+constexpr uint32_t kTwo = 1u << 8;     // both row tiles of the unit have rows
+constexpr uint32_t kFirst = 1u << 9;   // the unit's first tile here
+constexpr uint32_t kMixed = 1u << 10;  // some key is seen by some of the rows only
+constexpr uint32_t kAll = 1u << 11;    // every key is there and seen by some row
 
 __device__ __forceinline__ uint64_t desc_mn(uint32_t at) {  // 128-byte swizzle, MN-major: 64-dim groups, 8-key groups
   uint64_t d = 0;
@@ -187,7 +223,8 @@ struct Work {
   kv::Seq s;
   int n, sink_tiles, first;  // tiles [0, sink_tiles) and [first, ...)
   int k0, k1;
-  int p0, p1;  // positions of its first and last row
+  int p0, p1;                // positions of its first and last row
+  int begin, sink_end;       // keys that its rows see: [begin, p1] and [0, sink_end)
 };
 
 template <int KT>
@@ -196,6 +233,8 @@ __device__ __forceinline__ void unit_tiles(Work& w, const AttnArgs& a) {
   w.p0 = w.s.len - w.s.rows + rho0 / a.group;
   w.p1 = w.s.len - w.s.rows + min(rho0 + kRows - 1, rows - 1) / a.group;
   const kv::Visible v = kv::visible(max(w.p0, 0), a.window, a.sinks);
+  w.begin = v.begin;
+  w.sink_end = v.sink_end;
   w.first = v.begin / KT;
   w.sink_tiles = min((v.sink_end + KT - 1) / KT, w.first);
   w.n = w.p1 < 0 ? 1 : w.sink_tiles + w.p1 / KT + 1 - w.first;  // one empty tile where there is no key
@@ -205,48 +244,104 @@ __device__ __forceinline__ bool takes(const kv::Seq& s, const TileParams& P) {
   return s.rows > 0 && s.rows * P.a.group > P.small_rows;
 }
 
-// Walks a CTA's range of tiles unit by unit; every role walks for itself.
+// The first sequence from i on that has work here.
+__device__ __forceinline__ void enter(Work& w, const TileParams& P, int i) {
+  for (;; ++i) {
+    w.s = kv::sequence(P.a.b, P.a.c.page_size, i);
+    if (takes(w.s, P)) break;
+  }
+  w.i = i;
+  w.row_tiles = (w.s.rows * P.a.group + kRows - 1) / kRows;
+}
+
+__device__ __forceinline__ long long scan32(long long mine, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, mine, o);
+    if (lane >= o) mine += up;
+  }
+  return mine;
+}
+
+// This CTA's range of all units' tiles, in the order (sequence, key/value
+// head, row tile, key tile): its first unit and its length, into `bar`.
 template <int KT>
-struct Walk {
-  Work w;
-  long long left;  // tiles of the range from w.k0 on
-  __device__ __forceinline__ void enter(const TileParams& P, int i) {
-    for (;; ++i) {
-      w.s = kv::sequence(P.a.b, P.a.c.page_size, i);
-      if (takes(w.s, P)) break;
-    }
-    w.i = i;
-    w.row_tiles = (w.s.rows * P.a.group + kRows - 1) / kRows;
-  }
-  __device__ __forceinline__ void begin(const TileParams& P, const Bars* b, long long tiles) {
-    enter(P, b->start_i);
-    w.h = b->start_h;
-    w.rt = b->start_rt;
-    left = tiles;
-    unit_tiles<KT>(w, P.a);
-    w.k0 = b->start_k;
-    w.k1 = static_cast<int>(min(static_cast<long long>(w.n), w.k0 + left));
-  }
-  __device__ __forceinline__ bool next(const TileParams& P) {
-    left -= w.k1 - w.k0;
-    if (left <= 0) return false;
-    if (++w.rt == w.row_tiles) {
-      w.rt = 0;
-      if (++w.h == P.a.c.kv_heads) {
-        w.h = 0;
-        enter(P, w.i + 1);
+__device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* totals, int warp, int lane) {
+  const AttnArgs& a = P.a;
+#pragma unroll 1
+  for (int i = warp; i < a.b.batch; i += kThreads / 32) {
+    Work w;
+    w.s = kv::sequence(a.b, a.c.page_size, i);
+    long long sum = 0;
+    if (takes(w.s, P)) {
+      const int rts = (w.s.rows * a.group + kRows - 1) / kRows;
+#pragma unroll 1
+      for (w.rt = lane; w.rt < rts; w.rt += 32) {
+        unit_tiles<KT>(w, a);
+        sum += w.n;
       }
     }
-    unit_tiles<KT>(w, P.a);
-    w.k0 = 0;
-    w.k1 = static_cast<int>(min(static_cast<long long>(w.n), left));
-    return true;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) totals[i] = sum;
   }
-  __device__ __forceinline__ int key_of(int k) const { return (k < w.sink_tiles ? k : w.first + (k - w.sink_tiles)) * KT; }
-};
+  __syncthreads();
+  if (warp != 0) return;
+  long long all = 0;
+#pragma unroll 1
+  for (int i = lane; i < a.b.batch; i += 32) all += totals[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  all *= a.c.kv_heads;
+  const long long per = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
+  long long x = per * blockIdx.x;
+  const long long mine = min(per, all - x);
+  int i = 0, h = 0, rt = 0;
+  if (mine > 0) {
+#pragma unroll 1
+    for (int base = 0;; base += 32) {  // the sequence
+      const long long here = base + lane < a.b.batch ? totals[base + lane] * a.c.kv_heads : 0, incl = scan32(here, lane);
+      const unsigned past = __ballot_sync(0xffffffffu, x < incl);
+      if (past) {
+        const int at = __ffs(static_cast<int>(past)) - 1;
+        i = base + at;
+        x -= __shfl_sync(0xffffffffu, incl - here, at);
+        break;
+      }
+      x -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    h = static_cast<int>(x / totals[i]);
+    x -= h * totals[i];
+    Work w;
+    w.s = kv::sequence(a.b, a.c.page_size, i);
+#pragma unroll 1
+    for (int base = 0;; base += 32) {  // the row tile
+      w.rt = base + lane;
+      unit_tiles<KT>(w, a);
+      const long long here = w.rt * kRows < w.s.rows * a.group ? w.n : 0, incl = scan32(here, lane);
+      const unsigned past = __ballot_sync(0xffffffffu, x < incl);
+      if (past) {
+        const int at = __ffs(static_cast<int>(past)) - 1;
+        rt = base + at;
+        x -= __shfl_sync(0xffffffffu, incl - here, at);
+        break;
+      }
+      x -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  if (lane == 0) {
+    bar->per = per;
+    bar->mine = mine;
+    bar->start_i = i;
+    bar->start_h = h;
+    bar->start_rt = rt;
+    bar->start_k = static_cast<int>(x);
+  }
+}
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams P) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ TileParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using G = Geo<FMT, D>;
   constexpr int KT = G::KT, NU = G::NU;
   constexpr bool QUANT = FMT != LQ_FMT_F16;
@@ -268,99 +363,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
       mbar_init(&bar->p_ready[q], 128);
       mbar_init(&bar->o_full[q], 2);
     }
+    for (int u = 0; u < kUnits; ++u) {
+      mbar_init(&bar->unit[u], 1);
+      mbar_init(&bar->unit_free[u], 256);
+    }
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->join, 256);
     bar->abort = 0;
-    for (int k = 0; k < kInfo; ++k)
-      for (int j = 0; j < 4; ++j) bar->bad[k][j] = 0;
+    for (int k = 0; k < kInfo; ++k) {
+      mbar_init(&bar->told[k], 1);
+      mbar_init(&bar->done[k], kLoaders);
+    }
+    for (int k = 0; k < kInfo; ++k) *reinterpret_cast<uint4*>(bar->bad[k]) = make_uint4(0u, 0u, 0u, 0u);
     fence_barrier_init();
   }
   pdl_wait();
-
-  // ---- this CTA's range of all units' tiles -----------------------------------
-  long long* const totals = reinterpret_cast<long long*>(ring);
-  for (int i = warp; i < a.b.batch; i += kThreads / 32) {
-    Work w;
-    w.s = kv::sequence(a.b, a.c.page_size, i);
-    long long sum = 0;
-    if (takes(w.s, P)) {
-      const int rts = (w.s.rows * a.group + kRows - 1) / kRows;
-      for (w.rt = lane; w.rt < rts; w.rt += 32) {
-        unit_tiles<KT>(w, a);
-        sum += w.n;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) totals[i] = sum * a.c.kv_heads;
-  }
-  __syncthreads();
-  auto scan32 = [&](long long mine) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, mine, o);
-      if (lane >= o) mine += up;
-    }
-    return mine;
-  };
-  if (warp == 0) {
-    long long total = 0;
-    for (int i = lane; i < a.b.batch; i += 32) total += totals[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
-    long long x = per * blockIdx.x;
-    if (lane == 0) bar->total = total;
-    if (x < total) {
-      int i = 0;
-      for (int base = 0;; base += 32) {
-        const long long mine = base + lane < a.b.batch ? totals[base + lane] : 0, incl = scan32(mine);
-        const unsigned past = __ballot_sync(0xffffffffu, x < incl);
-        if (past) {
-          const int at = __ffs(static_cast<int>(past)) - 1;
-          i = base + at;
-          x -= __shfl_sync(0xffffffffu, incl - mine, at);
-          break;
-        }
-        x -= __shfl_sync(0xffffffffu, incl, 31);
-      }
-      const long long head = totals[i] / a.c.kv_heads;
-      const int h = static_cast<int>(x / head);
-      x -= h * head;
-      Work w;
-      w.s = kv::sequence(a.b, a.c.page_size, i);
-      for (int base = 0;; base += 32) {
-        w.rt = base + lane;
-        unit_tiles<KT>(w, a);
-        const long long mine = w.rt * kRows < w.s.rows * a.group ? w.n : 0, incl = scan32(mine);
-        const unsigned past = __ballot_sync(0xffffffffu, x < incl);
-        if (past) {
-          const int at = __ffs(static_cast<int>(past)) - 1;
-          const long long k = x - __shfl_sync(0xffffffffu, incl - mine, at);
-          if (lane == 0) {
-            bar->start_i = i;
-            bar->start_h = h;
-            bar->start_rt = base + at;
-            bar->start_k = static_cast<int>(k);
-          }
-          break;
-        }
-        x -= __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-  }
+  plan<KT>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
   if (warp == 12) {
     tc::tmem_alloc(&bar->tmem, 512);
     tc::tmem_relinquish();
   }
+  fence_proxy_async_smem();  // the totals lay where copies will land
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bar->tmem;
-  const long long total = bar->total;
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
-  const long long x0 = per * blockIdx.x;
-  const long long mine = min(per, total - x0);  // tiles of this CTA
 
   auto wait = [&](uint64_t* b, uint32_t parity) {  // by whole warps
     const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity, P.wait_ns, P.wait_iters));
@@ -379,124 +406,134 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     const uint32_t s_at = tmem + lanes + q * 128, o_at = tmem + lanes + 256 + q * D;
     unsigned char* const q_hi = smem + q * 2 * G::QPART;
     unsigned char* const q_lo = q_hi + G::QPART;
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
     uint32_t tile = 0, tiles_q = 0, joins = 0;  // tiles done by the CTA, by this row tile
-    Walk<KT> walk;
-    bool on = mine > 0;
-    if (on) walk.begin(P, bar, mine);
-    while (on) {
-      const Work& w = walk.w;
-      const int rho = w.rt * kRows + q * 128 + r, rows_all = w.s.rows * a.group;
-      const bool active = w.rt * kRows + q * 128 < rows_all;  // the row tile has rows
-      const bool row = rho < rows_all;
-      const int t = w.s.row0 + (row ? rho / a.group : 0);
-      const int head = w.h * a.group + (row ? rho % a.group : 0);
-      const int pos = w.s.len - w.s.rows + min(rho, rows_all - 1) / a.group;
+#pragma unroll 1
+    for (uint32_t un = 0;; ++un) {
+      if (!wait(&bar->unit[un % kUnits], (un / kUnits) & 1u)) break;
+      const UnitInfo& w = bar->units[un % kUnits];
+      const int tiles = w.tiles;
+      if (tiles == 0) break;
+      const int rho = w.rho0 + q * 128 + r;
+      const bool active = w.rho0 + q * 128 < w.rows;  // the row tile has rows
+      const bool row = rho < w.rows;
+      const int token = min(rho, w.rows - 1) / a.group;
+      const int t = w.row0 + token, head = w.head0 + (min(rho, w.rows - 1) - token * a.group), pos = w.pos0 + token;
       float om[D], M = kNoMax, l = 0.0f, f = 0.0f;
-      const long long src_off = t * a.ldq + static_cast<long long>(head) * D;
       if (active) {
         // the warp's 32 query rows, one or two at a time: scaled to the top of
         // f16's range, in two parts
         constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes a row, rows at a time
-        const int sub = lane / LPR, l4 = lane % LPR;
+        const int l4 = lane % LPR;
+        const long long off = t * a.ldq + static_cast<long long>(head) * D;
         const uint32_t live = __ballot_sync(0xffffffffu, row);
         const uint32_t col = (l4 >> 4) * G::GROUP + (l4 & 1) * 8;  // column group, half of a 16-byte chunk
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += RPI) {
-          const int rr = r0 + sub;
-          const float* src = a.Q + __shfl_sync(0xffffffffu, src_off, rr) + l4 * 4;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if ((live >> rr) & 1u) {
-            if (P.vec_q) {
-              v = ldg128f(src);
-            } else {
-              v = make_float4(src[0], src[1], src[2], src[3]);
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+          float4 v[8 / RPI];
+#pragma unroll
+          for (int i = 0; i < 8 / RPI; ++i) {
+            const int rr = r0 + i * RPI + lane / LPR;
+            const float* src = a.Q + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if ((live >> rr) & 1u) {
+              if (P.vec_q) {
+                v[i] = ldg128f(src);
+              } else {
+                v[i] = make_float4(src[0], src[1], src[2], src[3]);
+              }
             }
           }
-          float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-          const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
-          const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
-          const float fr = __shfl_sync(0xffffffffu, fabsf(a.scale) * kLog2e / sigma, (lane % RPI) * LPR);
-          if (lane / RPI == r0 / RPI) f = fr;
-          uint2 hi, lo;
-          split2(v.x * (sigma * sign), v.y * (sigma * sign), hi.x, lo.x);
-          split2(v.z * (sigma * sign), v.w * (sigma * sign), hi.y, lo.y);
-          const uint32_t at = col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
-          *reinterpret_cast<uint2*>(q_hi + at) = hi;
-          *reinterpret_cast<uint2*>(q_lo + at) = lo;
+          for (int i = 0; i < 8 / RPI; ++i) {
+            const int rr = r0 + i * RPI + lane / LPR;
+            float top = fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+            const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
+            const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
+            // the row's own lane keeps the factor that takes S back to base-2 logits
+            const float back = __uint_as_float(static_cast<unsigned>(254 - es) << 23);
+            const float fr = __shfl_sync(0xffffffffu, back, (lane % RPI) * LPR);
+            if (lane / RPI == (r0 + i * RPI) / RPI) f = fr;
+            const float sg = a.scale < 0.0f ? -sigma : sigma;
+            uint2 hi, lo;
+            split2(v[i].x * sg, v[i].y * sg, hi.x, lo.x);
+            split2(v[i].z * sg, v[i].w * sg, hi.y, lo.y);
+            const uint32_t at = col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
+            *reinterpret_cast<uint2*>(q_hi + at) = hi;
+            *reinterpret_cast<uint2*>(q_lo + at) = lo;
+          }
         }
+        f *= fabsf(a.scale) * kLog2e;
         fence_proxy_async_smem();
         mbar_arrive(&bar->q_ready[q]);
 #pragma unroll
         for (int d = 0; d < D; ++d) om[d] = 0.0f;
       }
-      for (int k = w.k0; k < w.k1; ++k, ++tile) {
-        if (!active) continue;
-        const uint32_t parity = tiles_q++ & 1u;
-        if (!wait(&bar->s_full[q], parity)) goto out;
+      bool ok = true;
+      if (!active) tile += tiles;
+#pragma unroll 1
+      for (int k = 0; k < (active ? tiles : 0); ++k, ++tile, ++tiles_q) {
+        ok = wait(&bar->s_full[q], tiles_q & 1u);
+        if (!ok) break;
         tc::fence_after_sync();
-        const int2 info = bar->info[tile % kInfo];
-        const int j0 = info.x;
-        const uint32_t pages = static_cast<uint32_t>(info.y) & 0xFFu;
-        constexpr uint32_t kAll = (1u << (KT / 16)) - 1u;
-        const bool clear = pages == kAll && j0 + KT - 1 <= pos &&
+        const int j0 = bar->info[tile % kInfo].j0;
+        const uint32_t pages = bar->info[tile % kInfo].flags & 0xFFu;
+        const bool clear = pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= pos &&
                            (a.window == 0 || j0 > pos - a.window || j0 + KT <= a.sinks);
         const bool edge = __any_sync(0xffffffffu, !clear);
-        auto sees = [&](int j) {  // key j of the tile
-          const int key = j0 + j;
-          return ((pages >> (j >> 4)) & 1u) && key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
+        // bit i: the row sees key j + i of the tile (i < 32; j a multiple of 16)
+        auto vis32 = [&](int j) -> uint32_t {
+          const int last = pos - j0 - j;  // keys up to here are not ahead of the row
+          uint32_t m = last < 0 ? 0u : (last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u);
+          if (a.window != 0) {
+            const int from = last >= a.window ? last - a.window + 1 : 0;  // keys from here on are in the window
+            const int sink = min(max(a.sinks - j0 - j, 0), 32);           // keys below are sinks
+            m &= (from >= 32 ? 0u : 0xFFFFFFFFu << from) | (sink >= 32 ? 0xFFFFFFFFu : (1u << sink) - 1u);
+          }
+          const uint32_t pg = pages >> (j >> 4);
+          return m & ((pg & 1u ? 0xFFFFu : 0u) | (pg & 2u ? 0xFFFF0000u : 0u));
         };
-        // raw sums of keys j .. j + 15: asked for, and (after wait_ld) put together
-        auto ask = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16]) {
-          tmem_ld16(s_at + j, s);
-          if constexpr (QUANT) tmem_ld16(s_at + 64 + j, s2);
-        };
-        auto sum = [&](uint32_t (&s)[16], uint32_t (&s2)[16]) {
-          if constexpr (QUANT) {
+        // Over the raw sums of all keys of the tile, 16 at a time. f16 caches have
+        // the registers to ask for the next 16 meanwhile.
+        auto each = [&](auto&& what) {
+          uint32_t s[16], next[16];
+          if constexpr (!QUANT) tmem_ld16(s_at, next);
+#pragma unroll 1
+          for (int j = 0; j < KT; j += 16) {
+            const uint32_t vis = edge ? vis32(j) : 0u;
+            if constexpr (QUANT) {
+              tmem_ld16(s_at + j, s);
+              tmem_ld16(s_at + 64 + j, next);
+              tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 x = fadd2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                     make_float2(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1])));
-              s[i] = __float_as_uint(x.x);
-              s[i + 1] = __float_as_uint(x.y);
+              for (int i = 0; i < 16; i += 2) {
+                const float2 x = fadd2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                       make_float2(__uint_as_float(next[i]), __uint_as_float(next[i + 1])));
+                s[i] = __float_as_uint(x.x);
+                s[i + 1] = __float_as_uint(x.y);
+              }
+            } else {
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[i] = next[i];
+              if (j + 16 < KT) tmem_ld16(s_at + j + 16, next);
             }
+            what(j, s, vis);
           }
         };
-        uint32_t sa[16], sb[16], sa2[16], sb2[16];  // two chunks in turn
         float top = -INFINITY;
-        auto largest = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16], bool masked) {
-          sum(s, s2);
-          if (!masked) {
+        each([&](int, uint32_t (&s)[16], uint32_t vis) {
+          if (!edge) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(s[i]));
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sees(j + i) ? __uint_as_float(s[i]) * f : -INFINITY);
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, (vis >> i) & 1u ? __uint_as_float(s[i]) : -INFINITY);
           }
-        };
-        if (!edge) {
-          ask(0, sa, sa2);
-#pragma unroll
-          for (int j = 0; j < KT; j += 32) {
-            tc::wait_ld();
-            ask(j + 16, sb, sb2);
-            largest(j, sa, sa2, false);
-            tc::wait_ld();
-            if (j + 32 < KT) ask(j + 32, sa, sa2);
-            largest(j + 16, sb, sb2, false);
-          }
-          top *= f;
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < KT; j += 16) {
-            ask(j, sa, sa2);
-            tc::wait_ld();
-            largest(j, sa, sa2, true);
-          }
-        }
+        });
+        top = top == -INFINITY ? top : top * f;
         float keep = 1.0f;
         if (top > M + 15.0f) {
           const float to = fmaxf(M, top - kLift);
@@ -505,55 +542,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
           l *= keep;
         }
         // weights, in two parts, over the logits: 16 columns a 16 keys
-        const float2 ff = make_float2(f, f), mm = make_float2(-M, -M);
+        const float2 ff = make_float2(f, f), mm = make_float2(-M, -M), minus = make_float2(-1.0f, -1.0f);
         float2 l2 = make_float2(0.0f, 0.0f);
-        auto weights = [&](int j, uint32_t (&s)[16], uint32_t (&s2)[16], bool masked) {
-          sum(s, s2);
+        each([&](int j, uint32_t (&s)[16], uint32_t vis) {
           uint32_t w16[16];
+          auto make = [&](bool masked) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
-            float2 p = make_float2(ex2(x.x), ex2(x.y));
-            if (masked) {
-              p.x = sees(j + i) ? p.x : 0.0f;
-              p.y = sees(j + i + 1) ? p.y : 0.0f;
+            for (int i = 0; i < 16; i += 2) {
+              const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
+              float2 p = make_float2(ex2(x.x), ex2(x.y));
+              if (masked) {
+                p.x = (vis >> i) & 1u ? p.x : 0.0f;
+                p.y = (vis >> (i + 1)) & 1u ? p.y : 0.0f;
+              }
+              l2 = fadd2(l2, p);
+              const __half2 h = __floats2half2_rn(p.x, p.y);
+              const float2 r2 = ffma2(__half22float2(h), minus, p);
+              w16[i / 2] = h2(h);
+              w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
             }
-            l2 = fadd2(l2, p);
-            const __half2 h = __floats2half2_rn(p.x, p.y);
-            const float2 hf = __half22float2(h);
-            const float2 r2 = fadd2(p, make_float2(-hf.x, -hf.y));
-            w16[i / 2] = h2(h);
-            w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
-          }
+          };
+          if (edge) make(true); else make(false);
           tmem_st16(s_at + j, w16);
-        };
-        if (!edge) {
-          ask(0, sa, sa2);
-#pragma unroll
-          for (int j = 0; j < KT; j += 32) {
-            tc::wait_ld();
-            ask(j + 16, sb, sb2);
-            weights(j, sa, sa2, false);
-            tc::wait_ld();
-            if (j + 32 < KT) ask(j + 32, sa, sa2);
-            weights(j + 16, sb, sb2, false);
-          }
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < KT; j += 16) {
-            ask(j, sa, sa2);
-            tc::wait_ld();
-            weights(j, sa, sa2, true);
-          }
-        }
+        });
         l += l2.x + l2.y;
         tc::wait_st();
         tc::fence_before_sync();
         mbar_arrive(&bar->p_ready[q]);
-        if (!wait(&bar->o_full[q], parity)) goto out;
+        ok = wait(&bar->o_full[q], tiles_q & 1u);
+        if (!ok) break;
         tc::fence_after_sync();
-        {
+        const uint4 bad = *reinterpret_cast<const uint4*>(bar->bad[tile % kInfo]);
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
           const float2 kk = make_float2(keep, keep);
+          uint32_t sa[16], sb[16];
           auto add = [&](int d, const uint32_t (&o)[16]) {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
@@ -572,317 +595,311 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             if (d + 32 < D) tmem_ld16(o_at + d + 32, sa);
             add(d + 16, sb);
           }
+          if (pass == 1 || (bad.x | bad.y | bad.z | bad.w) == 0u) break;
+          // values that are not finite were kept out of the MMA: once more, with
+          // their sums over the keys that each row sees in O's place
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16] = {};
+#pragma unroll 1
+            for (int j = 0; j < KT; ++j) {
+              const uint32_t word = j < 32 ? bad.x : (j < 64 ? bad.y : (j < 96 ? bad.z : bad.w));
+              if (!((word >> (j & 31)) & 1u) || !((vis32(j & ~31) >> (j & 31)) & 1u)) continue;
+              const int page = kv::page_of(a.c, a.b, w.seq, j0 + j);
+              if (page < 0) continue;
+              const int slot = (j0 + j) % a.c.page_size;
+              const unsigned char* at = a.c.v + page * a.c.page_bytes + w.kv_head * a.c.head_bytes;
+              const __half* h16 = QUANT ? reinterpret_cast<const __half*>(at + static_cast<long long>(a.c.page_size) * G::ROW) + slot * (D / 32) + d / 32
+                                        : reinterpret_cast<const __half*>(at) + static_cast<long long>(slot) * D + d;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float v = __half2float(h16[QUANT ? 0 : i]);
+                if (!(fabsf(v) <= 65504.0f)) o[i] += QUANT ? v - v : v;  // a block's scale: NaN
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sa[i] = __float_as_uint(o[i]);
+            tmem_st16(o_at + d, sa);
+          }
+          tc::wait_st();
+          keep = 1.0f;
         }
         tc::fence_before_sync();
-        // values that are not finite reach the rows that see them here
-        for (int word = 0; word < KT / 32; ++word) {
-          uint32_t bits = bar->bad[tile % kInfo][word];
-          while (bits) {
-            const int j = word * 32 + __ffs(static_cast<int>(bits)) - 1;
-            bits &= bits - 1;
-            if (!row || !sees(j)) continue;
-            const int page = kv::page_of(a.c, a.b, w.i, j0 + j);
-            if (page < 0) continue;
-            const int slot = (j0 + j) % a.c.page_size;
-            const unsigned char* at = a.c.v + page * a.c.page_bytes + w.h * a.c.head_bytes;
-            const __half* h16 = QUANT ? reinterpret_cast<const __half*>(at + static_cast<long long>(a.c.page_size) * G::ROW) + slot * (D / 32)
-                                      : reinterpret_cast<const __half*>(at) + static_cast<long long>(slot) * D;
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-              const float v = __half2float(h16[QUANT ? d / 32 : d]);
-              if (!(fabsf(v) <= 65504.0f)) om[d] += QUANT ? v - v : v;  // a block's scale: NaN
-            }
-          }
-        }
       }
-      {
-        // ---- the unit's result, or its part -------------------------------------
-        // rows go out through the query rows' shared memory (their MMAs are done; a
-        // warp's rows of all parts are its own): whole rows, 16 bytes a lane
-        auto write_rows = [&]() {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing; NaN stays
-          __syncwarp();
+      if (!ok) break;
+
+      // ---- the unit's result, or its part -----------------------------------------
+      bool writes = active;
+      if (w.c0 != w.c1) {
+        auto slot_of = [&](int c) { return P.parts + static_cast<long long>(c == w.c0 ? 2 * c + 1 : 2 * c) * G::SLOT + (q * 128 + r) * 4; };
+        if (row) {
+          float* to = P.parts + static_cast<long long>(w.slot) * G::SLOT + (q * 128 + r) * 4;
 #pragma unroll
           for (int d = 0; d < D; d += 4)
-            *reinterpret_cast<float4*>(q_hi + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
-                make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
-          __syncwarp();
-          constexpr int LPR = D / 4, RPI = 32 / LPR;
-          const int sub = lane / LPR, l4 = lane % LPR;
-          const uint32_t live = __ballot_sync(0xffffffffu, row && LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads));
-          const long long off = t * a.ldo + static_cast<long long>(head) * D;
-#pragma unroll 4
-          for (int r0 = 0; r0 < 32; r0 += RPI) {
-            const int rr = r0 + sub;
-            float* out = a.O + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
-            const float4 v =
-                *reinterpret_cast<const float4*>(q_hi + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
-            if ((live >> rr) & 1u) {
-              if (P.vec_o) {
-                *reinterpret_cast<float4*>(out) = v;
-              } else {
-                out[0] = v.x;
-                out[1] = v.y;
-                out[2] = v.z;
-                out[3] = v.w;
-              }
-            }
-          }
-          if (row && a.lse) a.lse[static_cast<long long>(t) * a.heads + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
-        };
-        const bool whole = w.k0 == 0 && w.k1 == w.n;
-        if (whole) {
-          if (active) write_rows();
-        } else {
-          // the unit's CTAs are c0 .. c1; c0's slot 2 c0 + 1, the others' 2 c
-          const long long unit_x = x0 + (mine - walk.left) - w.k0;
-          const int c0 = static_cast<int>(unit_x / per), c1 = static_cast<int>((unit_x + w.n - 1) / per);
-          const int rr = q * 128 + r;
-          auto slot_of = [&](int c) { return P.parts + static_cast<long long>(c == c0 ? 2 * c0 + 1 : 2 * c) * G::SLOT; };
-          if (row) {
-            float* to = slot_of(static_cast<int>(blockIdx.x));
-#pragma unroll
-            for (int d = 0; d < D; d += 4)
-              reinterpret_cast<float4*>(to)[(d / 4) * kRows + rr] = make_float4(om[d], om[d + 1], om[d + 2], om[d + 3]);
-            to[D * kRows + rr] = M;
-            to[(D + 1) * kRows + rr] = l;
-          }
+            *reinterpret_cast<float4*>(to + d * kRows) = make_float4(om[d], om[d + 1], om[d + 2], om[d + 3]);
+          *reinterpret_cast<float2*>(to + D * kRows - (q * 128 + r) * 2) = make_float2(M, l);
+        }
+        __threadfence();
+        mbar_arrive(&bar->join);
+        if (!wait(&bar->join, joins++ & 1u)) break;
+        if (tid == 0) {
+          const int before = atomicAdd(P.counters + w.c0, 1);
+          bar->last = before == w.c1 - w.c0;
+          if (before == w.c1 - w.c0) P.counters[w.c0] = 0;
+        }
+        mbar_arrive(&bar->join);
+        if (!wait(&bar->join, joins++ & 1u)) break;
+        writes = active && bar->last;
+        if (writes && row) {  // in the order of the keys
           __threadfence();
-          mbar_arrive(&bar->join);
-          if (!wait(&bar->join, joins++ & 1u)) goto out;
-          if (tid == 0) {
-            const int before = atomicAdd(P.counters + c0, 1);
-            bar->last = before == c1 - c0;
-            if (before == c1 - c0) P.counters[c0] = 0;
-          }
-          mbar_arrive(&bar->join);
-          if (!wait(&bar->join, joins++ & 1u)) goto out;
-          if (bar->last && active) {
-            __threadfence();
-            M = kNoMax;
-            for (int c = c0; row && c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + D * kRows + rr));
-            l = 0.0f;
+          M = kNoMax;
+          l = 0.0f;
 #pragma unroll
-            for (int d = 0; d < D; ++d) om[d] = 0.0f;
-            for (int c = c0; row && c <= c1; ++c) {
-              const float* from = slot_of(c);
-              const float scale = ex2(__ldcg(from + D * kRows + rr) - M);
-              l = fmaf(scale, __ldcg(from + (D + 1) * kRows + rr), l);
+          for (int d = 0; d < D; ++d) om[d] = 0.0f;
+#pragma unroll 1
+          for (int c = w.c0; c <= w.c1; ++c) {
+            const float* from = slot_of(c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D * kRows - (q * 128 + r) * 2));
+            const float to = fmaxf(M, ml.x), f1 = ex2(M - to), f2 = ex2(ml.x - to);
+            M = to;
+            l = l * f1 + ml.y * f2;
 #pragma unroll
-              for (int d = 0; d < D; d += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(from) + (d / 4) * kRows + rr);
-                om[d] = fmaf(scale, v.x, om[d]);
-                om[d + 1] = fmaf(scale, v.y, om[d + 1]);
-                om[d + 2] = fmaf(scale, v.z, om[d + 2]);
-                om[d + 3] = fmaf(scale, v.w, om[d + 3]);
-              }
+            for (int d = 0; d < D; d += 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + d * kRows));
+              om[d] = om[d] * f1 + v.x * f2;
+              om[d + 1] = om[d + 1] * f1 + v.y * f2;
+              om[d + 2] = om[d + 2] * f1 + v.z * f2;
+              om[d + 3] = om[d + 3] * f1 + v.w * f2;
             }
-            write_rows();
           }
         }
       }
-      on = walk.next(P);
+      if (writes) {
+        // rows go out through the query rows' shared memory (their MMAs are done; a
+        // warp's rows of all parts are its own): whole rows, 16 bytes a lane
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing; NaN stays
+        __syncwarp();
+#pragma unroll
+        for (int d = 0; d < D; d += 4)
+          *reinterpret_cast<float4*>(q_hi + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
+              make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
+        __syncwarp();
+        constexpr int LPR = D / 4, RPI = 32 / LPR;
+        const int l4 = lane % LPR;
+        const uint32_t live = __ballot_sync(0xffffffffu, row && LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads));
+        const long long off = t * a.ldo + static_cast<long long>(head) * D;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int rr = r0 + lane / LPR;
+          float* out = a.O + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
+          const float4 v = *reinterpret_cast<const float4*>(q_hi + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
+          if ((live >> rr) & 1u) {
+            if (P.vec_o) {
+              *reinterpret_cast<float4*>(out) = v;
+            } else {
+              out[0] = v.x;
+              out[1] = v.y;
+              out[2] = v.z;
+              out[3] = v.w;
+            }
+          }
+        }
+        if (row && a.lse) a.lse[static_cast<long long>(t) * a.heads + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+        __syncwarp();
+      }
+      mbar_arrive(&bar->unit_free[un % kUnits]);
     }
-  out:;
   } else if (wg == 2) {
     // ================= loader ========================================================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::REG_LOAD));
     const int tl = tid & 127;
-    uint32_t unit = 0, tile = 0;
-    uint32_t pending = 0;  // f16: units issued whose copies are not yet reported
+    constexpr int CPR = QUANT ? D / 16 : D / 8;          // chunks a row: 16 codes, or 16 bytes of f16
+    constexpr int PASS = kLoaders / CPR, N = KT / PASS;  // rows a pass, passes
+    const int row0 = tl / CPR, ch = tl % CPR;
+    const long long total = bar->mine;
     bool alive = true;
-    Walk<KT> walk;
-    bool on = mine > 0;
-    if (on) walk.begin(P, bar, mine);
 
     // the values of a unit's chunks that this thread copied: those that are not
     // finite are taken out and their keys noted
     auto screen = [&](uint32_t at_unit, uint32_t tile_no) {
-      constexpr int CH = D / 8, PASS = kLoaders / CH, N = KT / PASS;
-      const int row0 = tl / CH, ch = tl % CH;
 #pragma unroll 1
       for (int n = 0; n < N; ++n) {
         const int row = row0 + n * PASS;
         unsigned char* at = ring + at_unit + (ch >> 3) * G::GROUP + tc::sw128_offset(row, ch & 7);
         uint4 v = *reinterpret_cast<uint4*>(at);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t w4[4] = {v.x, v.y, v.z, v.w};
         bool bad = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if ((w[j] & 0x7C00u) == 0x7C00u) {
-            w[j] &= 0xFFFF0000u;
+          if ((w4[j] & 0x7C00u) == 0x7C00u) {
+            w4[j] &= 0xFFFF0000u;
             bad = true;
           }
-          if ((w[j] & 0x7C000000u) == 0x7C000000u) {
-            w[j] &= 0xFFFFu;
+          if ((w4[j] & 0x7C000000u) == 0x7C000000u) {
+            w4[j] &= 0xFFFFu;
             bad = true;
           }
         }
         if (bad) {
-          *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(at) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           atomicOr(&bar->bad[tile_no % kInfo][row >> 5], 1u << (row & 31));
         }
       }
     };
-    uint32_t pend_unit = 0, pend_tile = 0;
-    bool pend_screen = false;
-    auto report = [&]() {  // f16: the oldest pending unit has landed
-      if (pend_screen) screen((pend_unit % NU) * G::UNIT, pend_tile);
-      fence_proxy_async_smem();
-      mbar_arrive(&bar->full[pend_unit % NU]);
-      pending = 0;
-    };
 
-    while (on && alive) {
-      const Work& w = walk.w;
-      const kv::Visible v0 = kv::visible(max(w.p0, 0), a.window, a.sinks);
-      auto group_at = [&](int j) -> long long {
-        const int key = j + lane * 16;
-        const int page = lane < KT / 16 ? kv::page_of(a.c, a.b, w.i, key) : -1;
-        return page < 0 ? -1 : page * a.c.page_bytes + w.h * a.c.head_bytes + static_cast<long long>(key % a.c.page_size) * G::ROW;
-      };
-      long long ahead = -1;
-      for (int k = w.k0; k < w.k1 && alive; ++k, ++tile) {
-        const int j0 = walk.key_of(k);
-        // the tile's groups of 16 keys, one lane each: where their rows begin (-1: nowhere)
-        const long long base = k == w.k0 ? group_at(j0) : ahead;
-        if (k + 1 < w.k1) ahead = group_at(walk.key_of(k + 1));
-        const uint32_t pages = __ballot_sync(0xffffffffu, base >= 0);
-        const bool mixed = w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && (a.window == 0 || j0 > w.p1 - a.window || j0 + KT <= a.sinks));
-        if (tl == 0) {
-          bar->info[tile % kInfo] = make_int2(
-              j0, static_cast<int>(pages | (w.rt * kRows + 128 < w.s.rows * a.group ? kTwo : 0u) | (k == w.k0 ? kFirst : 0u)));
-          for (int j = 0; j < 4; ++j) bar->bad[(tile + kInfo / 2) % kInfo][j] = 0;
+    uint32_t unit = 0, pend = 0;  // ring units filled; f16: unit whose copies are not yet reported, plus one
+    bool pend_screen = false;
+    using Raw = typename std::conditional<FMT == LQ_FMT_Q8_0, uint4, uint2>::type;
+    Raw ahead[N];
+    __half sc_ahead[N];
+    auto fetch = [&](int n, const TileInfo& c, int side) {  // quantised: codes and scale of pass n
+      const int row = row0 + n * PASS;
+      const longlong2 at = *reinterpret_cast<const longlong2*>(&c.at[2 * (row >> 4)]);
+      const int key = c.j0 + row;
+      ahead[n] = Raw{};
+      sc_ahead[n] = __ushort_as_half(0);
+      if ((c.flags & kAll) || (at.x >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end))) {
+        const unsigned char* const pool = side ? a.c.v : a.c.k;
+        ahead[n] = *reinterpret_cast<const Raw*>(pool + at.x + (row & 15) * G::ROW + ch * (G::ROW * 16 / D));
+        sc_ahead[n] = *reinterpret_cast<const __half*>(pool + at.y + (row & 15) * (D / 16) + (ch >> 1) * 2);
+      }
+    };
+    auto report = [&]() {  // f16: the pending unit has landed
+      const uint32_t u = pend - 1;
+      if (pend_screen) screen((u % NU) * G::UNIT, u / 2);
+      fence_proxy_async_smem();
+      mbar_arrive(&bar->full[u % NU]);
+      pend = 0;
+    };
+#pragma unroll 1
+    for (uint32_t tile = 0; tile < total && alive; ++tile) {  // loader
+      const TileInfo& c = bar->info[tile % kInfo];
+      if (!QUANT || tile == 0) {
+        alive = wait(&bar->told[tile % kInfo], (tile / kInfo) & 1u);
+        if (!alive) break;
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) fetch(n, c, 0);
         }
-        const bool all = pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= w.p1 && (j0 >= v0.begin || j0 + KT <= v0.sink_end);
-        auto some_row_sees = [&](int key) { return all || (key <= w.p1 && (key >= v0.begin || key < v0.sink_end)); };
+      }
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side, ++unit) {
+        uint64_t* const e = &bar->empty[unit % NU];
+        const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
+        uint64_t* const fl = &bar->full[unit % NU];
         if constexpr (!QUANT) {
-          constexpr int CH = D / 8, PASS = kLoaders / CH, N = KT / PASS;  // chunks a row, rows a pass, passes
-          const int row0 = tl / CH, ch = tl % CH;
-          for (int side = 0; side < 2; ++side, ++unit) {
-            uint64_t* const e = &bar->empty[unit % NU];
-            const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
-            if (pending && !__all_sync(0xffffffffu, mbar_test_wait(e, parity))) {  // about to wait: report what landed
+          if (pend && !__all_sync(0xffffffffu, mbar_test_wait(e, parity))) {  // about to wait: report what landed
+            wait_copies<0>();
+            report();
+          }
+          alive = wait(e, parity);
+          if (!alive) break;
+          if (P.tma && (c.flags & (kAll | kMixed)) == kAll) {  // every key is every row's: the copy engine's boxes of 16 keys x 64 dims
+            if (pend) {
               wait_copies<0>();
               report();
             }
-            if (!wait(e, parity)) {
-              alive = false;
-              break;
+            if (warp == 8) {
+              if (lane == 0) mbar_arrive_expect_tx(fl, G::UNIT);
+              __syncwarp();
+              if (lane < KT / 16) {
+                const int r16 = static_cast<int>(c.at[lane]);
+#pragma unroll
+                for (int h = 0; h < G::HALVES; ++h)
+                  tc::tma_load_2d(ring + (unit % NU) * G::UNIT + h * G::GROUP + lane * 2048, side ? &mv : &mk, h * 64, r16, fl);
+              }
+              if (lane != 0) mbar_arrive(fl);
+              __syncwarp();
+            } else {
+              mbar_arrive(fl);
             }
-            const unsigned char* pool = side ? a.c.v : a.c.k;
-            const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::GROUP + tc::sw128_offset(row0, ch & 7);
-            const unsigned char* const src = pool + row0 * G::ROW + ch * 16;
+            continue;
+          }
+          const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::GROUP + tc::sw128_offset(row0, ch & 7);
+          const unsigned char* const src = (side ? a.c.v : a.c.k) + row0 * G::ROW + ch * 16;
 #pragma unroll 4
-            for (int n = 0; n < N; ++n) {  // rows row0 + n PASS: the same place in a swizzle atom, one group of 16 a pass
-              const long long at = __shfl_sync(0xffffffffu, base, n * PASS / 16);
-              const bool there = at >= 0 && some_row_sees(j0 + row0 + n * PASS);
-              copy16(dst + n * PASS * 128, src + max(at, 0ll) + (n * PASS % 16) * G::ROW, there);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (pending) {
-              wait_copies<1>();
-              report();
-            }
-            pending = 1;
-            pend_unit = unit;
-            pend_tile = tile;
-            pend_screen = side == 1 && mixed;
+          for (int n = 0; n < N; ++n) {  // rows row0 + n PASS: the same place in a swizzle atom, one group of 16 a pass
+            const long long at = c.at[n * PASS / 16];
+            const int key = c.j0 + row0 + n * PASS;
+            const bool there = at >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end);
+            copy16(dst + n * PASS * 128, src + max(at, 0ll) * G::ROW + (n * PASS % 16) * G::ROW, there);
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (pend) {
+            wait_copies<1>();
+            report();
+          }
+          pend = unit + 1;
+          pend_screen = side == 1 && (c.flags & kMixed);
         } else {
-          // 16 codes a chunk: Q8_0 16 bytes (elements 16 c ..), Q4_0 8 bytes of a
-          // block (elements 8 (c & 1) .. of both its halves)
-          constexpr int CH = D / 16, PASS = kLoaders / CH, N = KT / PASS;
-          const int row0 = tl / CH, ch = tl % CH;
-          uint4 raw[2][N];
-          __half sc[2][N];
+          const bool mixed = side == 1 && (c.flags & kMixed);
+          // the next unit: this tile's V, or the next tile's K
+          bool more = side == 0 || tile + 1 < total;
+          if (side == 1 && more) {
+            alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
+            if (!alive) break;
+          }
+          const TileInfo& nc = side == 0 ? c : bar->info[(tile + 1) % kInfo];
+          alive = wait(e, parity);
+          if (!alive) break;
+          unsigned char* const dst = ring + (unit % NU) * G::UNIT;
 #pragma unroll
-          for (int n = 0; n < N; ++n) {  // PASS = 16 or 32 rows a pass
+          for (int n = 0; n < N; ++n) {
             const int row = row0 + n * PASS;
-            const long long at = __shfl_sync(0xffffffffu, base, row >> 4);
-            const bool there = at >= 0 && some_row_sees(j0 + row);
-            // the scales lie after the page's codes: slot * D / 32 of them in
-            const long long slot = (j0 + (row & ~15)) % a.c.page_size;
-            const long long sat = at - slot * G::ROW + static_cast<long long>(a.c.page_size) * G::ROW + (slot + (row & 15)) * (D / 16) + (ch >> 1) * 2;
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-              raw[side][n] = make_uint4(0u, 0u, 0u, 0u);
-              sc[side][n] = __ushort_as_half(0);
-              const unsigned char* pool = side ? a.c.v : a.c.k;
-              if (there) {
-                if constexpr (FMT == LQ_FMT_Q8_0) {
-                  raw[side][n] = *reinterpret_cast<const uint4*>(pool + at + (row & 15) * G::ROW + ch * 16);
-                } else {
-                  const uint2 x = *reinterpret_cast<const uint2*>(pool + at + (row & 15) * G::ROW + ch * 8);
-                  raw[side][n].x = x.x;
-                  raw[side][n].y = x.y;
-                }
-                sc[side][n] = *reinterpret_cast<const __half*>(pool + sat);
-              }
+            __half d = sc_ahead[n];
+            alignas(16) uint32_t w4[4];
+            *reinterpret_cast<Raw*>(w4) = ahead[n];
+            if (more) fetch(n, nc, side ^ 1);  // on its way while the others are converted
+            if (mixed && !(fabsf(__half2float(d)) <= 65504.0f)) {
+              d = __ushort_as_half(0);
+              atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
             }
-          }
-          for (int side = 0; side < 2; ++side, ++unit) {
-            if (!wait(&bar->empty[unit % NU], ((unit / NU) & 1u) ^ 1u)) {
-              alive = false;
-              break;
+            uint32_t hi[8], lo[8];
+            if constexpr (FMT == LQ_FMT_Q8_0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) codes8(w4[i], hi[2 * i], hi[2 * i + 1]);
+            } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
+#pragma unroll
+              for (int i = 0; i < 2; ++i) codes4(w4[i], hi[2 * i], hi[2 * i + 1], hi[4 + 2 * i], hi[4 + 2 * i + 1]);
             }
-            unsigned char* const dst = ring + (unit % NU) * G::UNIT;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-              const int row = row0 + n * PASS;
-              __half d = side ? sc[1][n] : sc[0][n];
-              if (side == 1 && mixed && !(fabsf(__half2float(d)) <= 65504.0f)) {
-                d = __ushort_as_half(0);
-                atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
-              }
-              const uint4 x = side ? raw[1][n] : raw[0][n];
-              const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-              uint32_t hi[8], lo[8];
-              if constexpr (FMT == LQ_FMT_Q8_0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) codes8(w4[i], hi[2 * i], hi[2 * i + 1]);
-              } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
-#pragma unroll
-                for (int i = 0; i < 2; ++i) codes4(w4[i], hi[2 * i], hi[2 * i + 1], hi[4 + 2 * i], hi[4 + 2 * i + 1]);
-              }
+            if (!(fabsf(__half2float(d)) >= (FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f))) {
+              // code * d in f16, and what it leaves: exact by the fused multiply-add
               const __half2 d2 = __half2half2(d);
-              if (!(fabsf(__half2float(d)) >= (FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f))) {
-                // code * d in f16, and what it leaves: exact by the fused multiply-add
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const __half2 c2 = as_h2(hi[i]), prod = __hmul2_rn(c2, d2);
-                  hi[i] = h2(prod);
-                  lo[i] = h2(__hfma2(c2, d2, __hneg2(prod)));
-                }
-              } else {  // the top of f16's range: rounded toward zero, through f32
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float2 c2 = __half22float2(as_h2(hi[i]));
-                  const float df = __half2float(d);
-                  split2_rz(c2.x * df, c2.y * df, hi[i], lo[i]);
-                }
+              for (int i = 0; i < 8; ++i) {
+                const __half2 c2 = as_h2(hi[i]), prod = __hmul2_rn(c2, d2);
+                hi[i] = h2(prod);
+                lo[i] = h2(__hfma2(c2, d2, __hneg2(prod)));
               }
-              // 16-byte chunks of the row: the second column group's threads start with their second
+            } else {  // the top of f16's range: rounded toward zero, through f32
+              const float df = __half2float(d);
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const int part = s ^ ((ch >> 2) & 1);
-                const int c16 = FMT == LQ_FMT_Q8_0 ? 2 * ch + part : (ch >> 1) * 4 + (ch & 1) + 2 * part;
-                const uint32_t at = (c16 >> 3) * G::GROUP;
-                const uint4 vh = part ? make_uint4(hi[4], hi[5], hi[6], hi[7]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                const uint4 vl = part ? make_uint4(lo[4], lo[5], lo[6], lo[7]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(row, c16 & 7)) = vh;
-                *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(64 + row, c16 & 7)) = vl;
+              for (int i = 0; i < 8; ++i) {
+                const float2 c2 = __half22float2(as_h2(hi[i]));
+                split2_rz(c2.x * df, c2.y * df, hi[i], lo[i]);
               }
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar->full[unit % NU]);
+            // 16-byte chunks of the row: the second column group's threads start with their second
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int part = s ^ ((ch >> 2) & 1);
+              const int c16 = FMT == LQ_FMT_Q8_0 ? 2 * ch + part : (ch >> 1) * 4 + (ch & 1) + 2 * part;
+              const uint32_t at = (c16 >> 3) * G::GROUP;
+              const uint4 vh = part ? make_uint4(hi[4], hi[5], hi[6], hi[7]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              const uint4 vl = part ? make_uint4(lo[4], lo[5], lo[6], lo[7]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(row, c16 & 7)) = vh;
+              *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(64 + row, c16 & 7)) = vl;
+            }
           }
+          fence_proxy_async_smem();
+          mbar_arrive(fl);
         }
       }
-      if (alive) on = walk.next(P);
+      mbar_arrive(&bar->done[tile % kInfo]);
     }
     wait_copies<0>();
-    if (pending) report();
+    if (pend) report();
   } else {
     // ================= MMA issue =======================================================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::REG_MMA));
@@ -890,101 +907,203 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
       constexpr uint32_t kQK = tc::idesc_f16_f32(128, 128);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
       const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
-      uint32_t seen[2] = {0, 0}, units[2] = {0, 0};  // tiles, units of a row tile
+      uint32_t seen0 = 0, seen1 = 0, units0 = 0, units1 = 0;  // tiles, units of a row tile
+      const long long mine = bar->mine;
       bool alive = true;
       auto at_unit = [&](uint32_t u) { return ring_at + (u % NU) * G::UNIT; };
-      // S = Q K^T of row tile q with the keys of ring unit u
-      auto qk = [&](int q, uint32_t u, bool first) {
-        if (first) alive = wait(&bar->q_ready[q], (q ? units[1]++ : units[0]++) & 1u);
-        if (!alive) return;
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint64_t b0 = tc::desc_sw128_kmajor(at_unit(u));
-          const uint64_t a0 = tc::desc_sw128_kmajor(q_at + q * 2 * G::QPART);
-#pragma unroll 1
-          for (int part = 1; part >= 0; --part)  // low parts first
-#pragma unroll 4
-            for (int c = 0; c < D / 16; ++c) {
-              const uint32_t off = (c >> 2) * G::GROUP + (c & 3) * 32;
-              tc::mma_bf16(tmem + q * 128, a0 + ((part * G::QPART + off) >> 4), b0 + (off >> 4), kQK, part == 1 && c == 0 ? 0u : 1u);
-            }
-          tc::commit(&bar->s_full[q]);
-          mbar_arrive(&bar->s_full[q]);
-        }
-        __syncwarp();
-      };
-      // O = P V of row tile q with the values of ring unit u
-      auto pv = [&](int q, uint32_t u) {
-        alive = wait(&bar->p_ready[q], (q ? seen[1]++ : seen[0]++) & 1u);
-        if (!alive) return;
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint64_t b0 = desc_mn(at_unit(u));
-          const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
-          constexpr int KS = KT / 16;
-#pragma unroll 4
-          for (int c = 0; c < KS; ++c)  // p_lo v_hi
-            tc::mma_f16_ts(o, p + 16 * c + 8, b0 + c * 128, kPV, c == 0 ? 0u : 1u);
-          if constexpr (QUANT) {
-#pragma unroll 4
-            for (int c = 0; c < KS; ++c)  // p_hi v_lo
-              tc::mma_f16_ts(o, p + 16 * c, b0 + (KS + c) * 128, kPV, 1u);
-          }
-#pragma unroll 4
-          for (int c = 0; c < KS; ++c)  // p_hi v_hi
-            tc::mma_f16_ts(o, p + 16 * c, b0 + c * 128, kPV, 1u);
-          tc::commit(&bar->o_full[q]);
-          mbar_arrive(&bar->o_full[q]);
-        }
-        __syncwarp();
-      };
       auto filled = [&](uint32_t u) { return wait(&bar->full[u % NU], (u / NU) & 1u); };
-      auto release = [&](uint32_t u) {
-        if (elect_one()) tc::commit(&bar->empty[u % NU]);
-        __syncwarp();
-      };
       // Order: PV of a row tile, then its next QK, while the other's softmax
       // runs. MMAs of one thread run in order, so that QK may overwrite the P
       // that the PV before it reads. Between units both PVs come first: the
       // next queries are written when both row tiles are done.
       uint32_t flags = 0;
-      if (mine > 0) {
-        alive = filled(0);
-        if (alive) {
-          flags = static_cast<uint32_t>(bar->info[0].y);
-          qk(0, 0, true);
-          if (alive && (flags & kTwo)) qk(1, 0, true);
-          if (alive) release(0);
-        }
-      }
 #pragma unroll 1
-      for (uint32_t tile = 0; tile < mine && alive; ++tile) {
-        const uint32_t v = 2 * tile + 1, k = v + 1;
-        const bool two = (flags & kTwo) != 0, more = tile + 1 < mine;
-        alive = filled(v);
-        if (alive) pv(0, v);
-        if (!alive) break;
+      for (long long tile = -1; tile < mine && mine > 0 && alive; ++tile) {
+        const uint32_t v = static_cast<uint32_t>(2 * tile + 1), k = v + 1;  // ring units of this tile's V and the next one's K
+        const bool more = tile + 1 < mine;
         uint32_t next = 0;
-        if (more) {
+        if (tile >= 0) alive = filled(v);
+        if (tile < 0 && alive) {
           alive = filled(k);
-          if (!alive) break;
-          next = static_cast<uint32_t>(bar->info[(tile + 1) % kInfo].y);
-          if (!(next & kFirst)) qk(0, k, false);
+          next = bar->info[0].flags;
         }
-        if (alive && two) pv(1, v);
+        bool have = tile < 0;
+#pragma unroll 1
+        for (int s = 0; s < 4 && alive; ++s) {
+          // 0 PV of row tile 0, 1 its QK, 2 PV of row tile 1, 3 its QK; between units 0, 2, 1, 3
+          if (s == 1 && more && !have) {
+            alive = filled(k);
+            if (!alive) break;
+            next = bar->info[(tile + 1) % kInfo].flags;
+            have = true;
+          }
+          int op = s;
+          if ((next & kFirst) && (s == 1 || s == 2)) op = 3 - s;
+          const int q = op >> 1;
+          if ((op & 1) == 0) {  // O = P V
+            if (tile < 0) continue;
+            const bool does = q == 0 || (flags & kTwo);
+            if (does) {
+              alive = wait(&bar->p_ready[q], (q ? seen1 : seen0) & 1u);
+              if (!alive) break;
+              if (q) ++seen1; else ++seen0;
+              tc::fence_after_sync();
+            }
+            if (elect_one()) {
+              if (does) {
+                const uint64_t b0 = desc_mn(at_unit(v));
+                const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
+                constexpr int KS = KT / 16;
+                // p_lo v_hi, (quantised) p_hi v_lo, p_hi v_hi: the small ones first
+#pragma unroll 1
+                for (int part = 0; part < 3; ++part) {
+                  if (!QUANT && part == 1) continue;
+                  const uint32_t pa = p + (part == 0 ? 8 : 0);
+                  const uint64_t b = b0 + (part == 1 ? KS * 128 : 0);
+#pragma unroll 4
+                  for (int c = 0; c < KS; ++c) tc::mma_f16_ts(o, pa + 16 * c, b + c * 128, kPV, part == 0 && c == 0 ? 0u : 1u);
+                }
+                tc::commit(&bar->o_full[q]);
+                mbar_arrive(&bar->o_full[q]);
+              }
+              if (q == 1) tc::commit(&bar->empty[v % NU]);  // the last reader of V
+            }
+            __syncwarp();
+          } else if (more) {  // S = Q K^T of the next tile
+            const bool does = q == 0 || (next & kTwo);
+            if (does) {
+              if (next & kFirst) {
+                alive = wait(&bar->q_ready[q], (q ? units1 : units0) & 1u);
+                if (!alive) break;
+                if (q) ++units1; else ++units0;
+              }
+              tc::fence_after_sync();
+            }
+            if (elect_one()) {
+              if (does) {
+                const uint64_t b0 = tc::desc_sw128_kmajor(at_unit(k));
+                const uint64_t a0 = tc::desc_sw128_kmajor(q_at + q * 2 * G::QPART);
+#pragma unroll 1
+                for (int part = 1; part >= 0; --part) {  // low parts first
+#pragma unroll 4
+                  for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t off = (c >> 2) * G::GROUP + (c & 3) * 32;
+                    tc::mma_bf16(tmem + q * 128, a0 + ((part * G::QPART + off) >> 4), b0 + (off >> 4), kQK, part == 1 && c == 0 ? 0u : 1u);
+                  }
+                }
+                tc::commit(&bar->s_full[q]);
+                mbar_arrive(&bar->s_full[q]);
+              }
+              if (q == 1) tc::commit(&bar->empty[k % NU]);  // the last reader of K
+            }
+            __syncwarp();
+          }
+        }
         if (!alive) break;
-        release(v);
-        if (more) {
-          if (next & kFirst) qk(0, k, true);
-          if (alive && (next & kTwo)) qk(1, k, (next & kFirst) != 0);
-          if (alive) release(k);
-          flags = next;
-        }
+        flags = next;
       }
       // everything issued has to be done before the tensor memory is freed
       if (elect_one()) tc::commit(&bar->drain);
       __syncwarp();
       mbar_wait(&bar->drain, 0, kDrainWaitNs);
+    } else if (warp == 13) {
+      // ---- walks the CTA's tiles a few ahead of the loaders ----------------------------
+      const long long total = bar->mine, per = bar->per;
+      long long left = total;  // tiles from the walk's on
+      uint32_t un = 0;
+      int k = 0;
+      bool alive = true, first = true;
+      Work w;
+      if (total > 0) {
+        enter(w, P, bar->start_i);
+        w.h = bar->start_h;
+        w.rt = bar->start_rt;
+        w.k0 = bar->start_k;
+      }
+#pragma unroll 1
+      for (uint32_t tile = 0; left > 0; ++tile, --left) {
+        if (first) {  // a unit
+          unit_tiles<KT>(w, a);
+          w.k1 = static_cast<int>(min(static_cast<long long>(w.n), w.k0 + left));
+          if (un >= kUnits) alive = wait(&bar->unit_free[un % kUnits], ((un / kUnits) & 1u) ^ 1u);
+          if (!alive) break;
+          if (lane == 0) {
+            const long long ux = per * blockIdx.x + (total - left) - w.k0;  // its first tile among all
+            UnitInfo& u = bar->units[un % kUnits];
+            u.tiles = w.k1 - w.k0;
+            u.rho0 = w.rt * kRows;
+            u.rows = w.s.rows * a.group;
+            u.row0 = w.s.row0;
+            u.pos0 = w.s.len - w.s.rows;
+            u.head0 = w.h * a.group;
+            u.seq = w.i;
+            u.kv_head = w.h;
+            const bool whole = w.k0 == 0 && w.k1 == w.n;
+            u.c0 = whole ? 0 : static_cast<int>(ux / per);
+            u.c1 = whole ? 0 : static_cast<int>((ux + w.n - 1) / per);
+            u.slot = 2 * static_cast<int>(blockIdx.x) + (w.k0 == 0 ? 1 : 0);
+            mbar_arrive(&bar->unit[un % kUnits]);
+          }
+          __syncwarp();
+          ++un;
+          k = w.k0;
+        }
+        const int j0 = (k < w.sink_tiles ? k : w.first + (k - w.sink_tiles)) * KT;
+        // pages of the tile's groups of 16 keys, one lane each
+        const int key = j0 + lane * 16;
+        const int page = lane < KT / 16 ? kv::page_of(a.c, a.b, w.i, key) : -1;
+        const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0);
+        // A slot is free when every softmax thread is done with its tile: so when
+        // the loaders have filled the tile four on (its V took the place of one
+        // whose PV came after that).
+        if (tile >= kInfo / 2) {
+          alive = wait(&bar->done[(tile - kInfo / 2) % kInfo], ((tile - kInfo / 2) / kInfo) & 1u);
+          if (!alive) break;
+        }
+        TileInfo& ti = bar->info[tile % kInfo];
+        if (lane < KT / 16) {
+          const int slot = key % a.c.page_size;
+          if constexpr (!QUANT) {
+            ti.at[lane] = page < 0 ? -1 : (static_cast<long long>(page) * a.c.kv_heads + w.h) * a.c.page_size + slot;
+          } else {
+            const long long head = page * a.c.page_bytes + w.h * a.c.head_bytes;
+            ti.at[2 * lane] = page < 0 ? -1 : head + static_cast<long long>(slot) * G::ROW;
+            ti.at[2 * lane + 1] = head + static_cast<long long>(a.c.page_size) * G::ROW + slot * (D / 16);
+          }
+        }
+        if (lane == 0) {
+          const bool every = a.window == 0 || j0 > w.p1 - a.window || j0 + KT <= a.sinks;
+          uint32_t flags = pages;
+          if (w.rt * kRows + 128 < w.s.rows * a.group) flags |= kTwo;
+          if (first) flags |= kFirst;
+          if (w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && every)) flags |= kMixed;
+          if (pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= w.p1 && (j0 >= w.begin || j0 + KT <= w.sink_end)) flags |= kAll;
+          ti.j0 = j0;
+          ti.flags = flags;
+          ti.p1 = w.p1;
+          ti.begin = w.begin;
+          ti.sink_end = w.sink_end;
+          *reinterpret_cast<uint4*>(bar->bad[tile % kInfo]) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->told[tile % kInfo]);
+        first = ++k == w.k1 && left > 1;
+        if (first) {
+          if (++w.rt == w.row_tiles) {
+            w.rt = 0;
+            if (++w.h == a.c.kv_heads) {
+              w.h = 0;
+              enter(w, P, w.i + 1);
+            }
+          }
+          w.k0 = 0;
+        }
+      }
+      if (alive && un >= kUnits) alive = wait(&bar->unit_free[un % kUnits], ((un / kUnits) & 1u) ^ 1u);
+      if (lane == 0) {  // no more units
+        bar->units[un % kUnits].tiles = 0;
+        mbar_arrive(&bar->unit[un % kUnits]);
+      }
     }
   }
   pdl_launch_dependents();
@@ -993,6 +1112,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 12) tc::tmem_dealloc(tmem, 512);
+}
+
+// An f16 pool as rows of head_dim values, in boxes of 16 rows x 64 dims.
+bool pool_map(CUtensorMap* map, const void* pool, const kv::Cache& c) {
+  const long long rows = static_cast<long long>(c.num_pages) * c.kv_heads * c.page_size;
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encode_tiled());
+  if (!encode || rows < 16 || rows > (1LL << 31) - 1) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim) * 2};
+  const cuuint32_t box[2] = {64, 16}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(pool), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT, int D>
@@ -1018,7 +1150,11 @@ lq_status run(const TileParams& p, int ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tile_kernel<FMT, D>, p);
+  CUtensorMap maps[2];
+  std::memset(maps, 0, sizeof(maps));
+  TileParams q = p;
+  q.tma = FMT == LQ_FMT_F16 && pool_map(&maps[0], p.a.c.k, p.a.c) && pool_map(&maps[1], p.a.c.v, p.a.c);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tile_kernel<FMT, D>, q, maps[0], maps[1]);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) count_route(kAttnRouteTile);
   return cuda_status(e);

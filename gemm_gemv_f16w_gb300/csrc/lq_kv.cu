@@ -272,6 +272,7 @@ lq_status kv_check(const lq_kv_cache* cache, const lq_kv_batch* batch, bool* noo
   if (!aligned_to(b.page_table, 4) || !aligned_to(b.kv_len, 4) || !aligned_to(b.q_start, 4)) return LQ_ERR_INVALID_ARG;
   // 32-bit token, page and row indices inside the kernels
   const long long most = (1LL << 31) - 1;
+  if (static_cast<int64_t>(b.max_pages) * c.page_size > (1LL << 30)) return LQ_ERR_UNSUPPORTED;
   if (c.head_dim > 256 || c.num_pages > most || b.tokens > (1LL << 30) || c.kv_heads > 4096) return LQ_ERR_UNSUPPORTED;
   return LQ_OK;
 }

@@ -344,7 +344,8 @@ lq_status lq_matmul_swiglu(int fmt, const float* A, const void* W, float* H,
  *     of one fused projection's output.
  *   - head_dim a multiple of 32, 1 <= page_size <= 65536, pointers aligned to
  *     their elements (pools: 2 bytes), else LQ_ERR_INVALID_ARG; head_dim
- *     > 256 or LQ_FMT_Q4_0I -> LQ_ERR_UNSUPPORTED. batch == 0 or tokens == 0:
+ *     > 256, LQ_FMT_Q4_0I or max_pages * page_size > 2^30 ->
+ *     LQ_ERR_UNSUPPORTED. batch == 0 or tokens == 0:
  *     LQ_OK, nothing is launched.
  * (The pages keep an f32 or f16 cache beside their attention kernels:
  * kv_cache_append_f32 and flash_attn_decode_paged_f32, ferrum-kernels
