@@ -428,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t live = __ballot_sync(0xffffffffu, row);
         const uint32_t col = (l4 >> 4) * G::GROUP + (l4 & 1) * 8;  // column group, half of a 16-byte chunk
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += 8) {
-          float4 v[8 / RPI];
+        for (int r0 = 0; r0 < 32; r0 += 16) {
+          float4 v[16 / RPI];
 #pragma unroll
-          for (int i = 0; i < 8 / RPI; ++i) {
+          for (int i = 0; i < 16 / RPI; ++i) {
             const int rr = r0 + i * RPI + lane / LPR;
             const float* src = a.Q + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
             v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8 / RPI; ++i) {
+          for (int i = 0; i < 16 / RPI; ++i) {
             const int rr = r0 + i * RPI + lane / LPR;
             float top = fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
 #pragma unroll
@@ -495,44 +495,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t pg = pages >> (j >> 4);
           return m & ((pg & 1u ? 0xFFFFu : 0u) | (pg & 2u ? 0xFFFF0000u : 0u));
         };
-        // Over the raw sums of all keys of the tile, 16 at a time. f16 caches have
-        // the registers to ask for the next 16 meanwhile.
-        auto each = [&](auto&& what) {
-          uint32_t s[16], next[16];
-          if constexpr (!QUANT) tmem_ld16(s_at, next);
+        // Over the raw sums of all keys of the tile, 16 at a time. (Asking for the
+        // next 16 ahead of time costs more in register moves than it hides.)
+        auto each = [&](auto&& what, bool masked) {
 #pragma unroll 1
           for (int j = 0; j < KT; j += 16) {
-            const uint32_t vis = edge ? vis32(j) : 0u;
+            uint32_t s[16];
+            tmem_ld16(s_at + j, s);
+            const uint32_t vis = masked ? vis32(j) : 0u;
             if constexpr (QUANT) {
-              tmem_ld16(s_at + j, s);
-              tmem_ld16(s_at + 64 + j, next);
+              uint32_t low[16];
+              tmem_ld16(s_at + 64 + j, low);
               tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
                 const float2 x = fadd2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                       make_float2(__uint_as_float(next[i]), __uint_as_float(next[i + 1])));
+                                       make_float2(__uint_as_float(low[i]), __uint_as_float(low[i + 1])));
                 s[i] = __float_as_uint(x.x);
                 s[i + 1] = __float_as_uint(x.y);
               }
             } else {
               tc::wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) s[i] = next[i];
-              if (j + 16 < KT) tmem_ld16(s_at + j + 16, next);
             }
             what(j, s, vis);
           }
         };
         float top = -INFINITY;
-        each([&](int, uint32_t (&s)[16], uint32_t vis) {
-          if (!edge) {
+        // (two loops each: merged into one, the masks cost every tile 1.4 times as much)
+        if (!edge) {
+          each([&](int, uint32_t (&s)[16], uint32_t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(s[i]));
-          } else {
+          }, false);
+        } else {
+          each([&](int, uint32_t (&s)[16], uint32_t vis) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, (vis >> i) & 1u ? __uint_as_float(s[i]) : -INFINITY);
-          }
-        });
+          }, true);
+        }
         top = top == -INFINITY ? top : top * f;
         float keep = 1.0f;
         if (top > M + 15.0f) {
@@ -544,27 +544,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // weights, in two parts, over the logits: 16 columns a 16 keys
         const float2 ff = make_float2(f, f), mm = make_float2(-M, -M), minus = make_float2(-1.0f, -1.0f);
         float2 l2 = make_float2(0.0f, 0.0f);
-        each([&](int j, uint32_t (&s)[16], uint32_t vis) {
+        auto weights = [&](int j, uint32_t (&s)[16], uint32_t vis, bool masked) {
           uint32_t w16[16];
-          auto make = [&](bool masked) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
-              float2 p = make_float2(ex2(x.x), ex2(x.y));
-              if (masked) {
-                p.x = (vis >> i) & 1u ? p.x : 0.0f;
-                p.y = (vis >> (i + 1)) & 1u ? p.y : 0.0f;
-              }
-              l2 = fadd2(l2, p);
-              const __half2 h = __floats2half2_rn(p.x, p.y);
-              const float2 r2 = ffma2(__half22float2(h), minus, p);
-              w16[i / 2] = h2(h);
-              w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
+          for (int i = 0; i < 16; i += 2) {
+            const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
+            float2 p = make_float2(ex2(x.x), ex2(x.y));
+            if (masked) {
+              p.x = (vis >> i) & 1u ? p.x : 0.0f;
+              p.y = (vis >> (i + 1)) & 1u ? p.y : 0.0f;
             }
-          };
-          if (edge) make(true); else make(false);
+            l2 = fadd2(l2, p);
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            const float2 r2 = ffma2(__half22float2(h), minus, p);
+            w16[i / 2] = h2(h);
+            w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
+          }
           tmem_st16(s_at + j, w16);
-        });
+        };
+        if (!edge) {
+          each([&](int j, uint32_t (&s)[16], uint32_t) { weights(j, s, 0u, false); }, false);
+        } else {
+          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true); }, true);
+        }
         l += l2.x + l2.y;
         tc::wait_st();
         tc::fence_before_sync();
@@ -751,18 +753,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t unit = 0, pend = 0;  // ring units filled; f16: unit whose copies are not yet reported, plus one
     bool pend_screen = false;
     using Raw = typename std::conditional<FMT == LQ_FMT_Q8_0, uint4, uint2>::type;
-    Raw ahead[N];
-    __half sc_ahead[N];
-    auto fetch = [&](int n, const TileInfo& c, int side) {  // quantised: codes and scale of pass n
-      const int row = row0 + n * PASS;
-      const longlong2 at = *reinterpret_cast<const longlong2*>(&c.at[2 * (row >> 4)]);
-      const int key = c.j0 + row;
-      ahead[n] = Raw{};
-      sc_ahead[n] = __ushort_as_half(0);
-      if ((c.flags & kAll) || (at.x >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end))) {
-        const unsigned char* const pool = side ? a.c.v : a.c.k;
-        ahead[n] = *reinterpret_cast<const Raw*>(pool + at.x + (row & 15) * G::ROW + ch * (G::ROW * 16 / D));
-        sc_ahead[n] = *reinterpret_cast<const __half*>(pool + at.y + (row & 15) * (D / 16) + (ch >> 1) * 2);
+    Raw ahead[2];
+    __half sc_ahead[2];
+    // Quantised: codes and scales of passes 2 nn and 2 nn + 1 of a side.
+    auto fetch = [&](int nn, const TileInfo& c, int side) {
+      const unsigned char* const pool = (side ? a.c.v : a.c.k) + ch * (G::ROW * 16 / D);
+      const unsigned char* const scales = (side ? a.c.v : a.c.k) + (ch >> 1) * 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = row0 + (2 * nn + i) * PASS;
+        const longlong2 at = *reinterpret_cast<const longlong2*>(&c.at[2 * (row >> 4)]);
+        const int key = c.j0 + row;
+        ahead[i] = Raw{};
+        sc_ahead[i] = __ushort_as_half(0);
+        if (at.x >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end)) {
+          ahead[i] = *reinterpret_cast<const Raw*>(pool + at.x + (row & 15) * G::ROW);
+          sc_ahead[i] = *reinterpret_cast<const __half*>(scales + at.y + (row & 15) * (D / 16));
+        }
       }
     };
     auto report = [&]() {  // f16: the pending unit has landed
@@ -778,17 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!QUANT || tile == 0) {
         alive = wait(&bar->told[tile % kInfo], (tile / kInfo) & 1u);
         if (!alive) break;
-        if constexpr (QUANT) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) fetch(n, c, 0);
-        }
+        if constexpr (QUANT) fetch(0, c, 0);
       }
+      if constexpr (!QUANT) {
 #pragma unroll 1
-      for (int side = 0; side < 2; ++side, ++unit) {
-        uint64_t* const e = &bar->empty[unit % NU];
-        const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
-        uint64_t* const fl = &bar->full[unit % NU];
-        if constexpr (!QUANT) {
+        for (int side = 0; side < 2; ++side, ++unit) {
+          uint64_t* const e = &bar->empty[unit % NU];
+          const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
+          uint64_t* const fl = &bar->full[unit % NU];
           if (pend && !__all_sync(0xffffffffu, mbar_test_wait(e, parity))) {  // about to wait: report what landed
             wait_copies<0>();
             report();
@@ -832,25 +836,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pend = unit + 1;
           pend_screen = side == 1 && (c.flags & kMixed);
-        } else {
-          const bool mixed = side == 1 && (c.flags & kMixed);
-          // the next unit: this tile's V, or the next tile's K
-          bool more = side == 0 || tile + 1 < total;
-          if (side == 1 && more) {
-            alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
+        }
+      } else {
+        // Two passes at a time, K's and then V's, in one small loop (straight code
+        // for all passes is bound by instruction fetches: 1.4 times as long); the
+        // next two are on their way meanwhile.
+#pragma unroll 1
+        for (int it = 0; it < N; ++it) {
+          const int side = it / (N / 2), nn = it % (N / 2);
+          if (nn == 0) {
+            alive = wait(&bar->empty[unit % NU], ((unit / NU) & 1u) ^ 1u);
             if (!alive) break;
           }
-          const TileInfo& nc = side == 0 ? c : bar->info[(tile + 1) % kInfo];
-          alive = wait(e, parity);
-          if (!alive) break;
           unsigned char* const dst = ring + (unit % NU) * G::UNIT;
+          alignas(16) uint32_t w4[2][4];
+          __half d2[2];
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int row = row0 + n * PASS;
-            __half d = sc_ahead[n];
-            alignas(16) uint32_t w4[4];
-            *reinterpret_cast<Raw*>(w4) = ahead[n];
-            if (more) fetch(n, nc, side ^ 1);  // on its way while the others are converted
+          for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<Raw*>(w4[i]) = ahead[i];
+            d2[i] = sc_ahead[i];
+          }
+          if (it + 1 < N) {
+            fetch((it + 1) % (N / 2), c, (it + 1) / (N / 2));
+          } else if (tile + 1 < total) {
+            alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
+            if (!alive) break;
+            fetch(0, bar->info[(tile + 1) % kInfo], 0);
+          }
+          const bool mixed = side == 1 && (c.flags & kMixed);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = row0 + (2 * nn + i) * PASS;
+            __half d = d2[i];
             if (mixed && !(fabsf(__half2float(d)) <= 65504.0f)) {
               d = __ushort_as_half(0);
               atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
@@ -858,26 +875,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t hi[8], lo[8];
             if constexpr (FMT == LQ_FMT_Q8_0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) codes8(w4[i], hi[2 * i], hi[2 * i + 1]);
+              for (int n = 0; n < 4; ++n) codes8(w4[i][n], hi[2 * n], hi[2 * n + 1]);
             } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
 #pragma unroll
-              for (int i = 0; i < 2; ++i) codes4(w4[i], hi[2 * i], hi[2 * i + 1], hi[4 + 2 * i], hi[4 + 2 * i + 1]);
+              for (int n = 0; n < 2; ++n) codes4(w4[i][n], hi[2 * n], hi[2 * n + 1], hi[4 + 2 * n], hi[4 + 2 * n + 1]);
             }
             if (!(fabsf(__half2float(d)) >= (FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f))) {
               // code * d in f16, and what it leaves: exact by the fused multiply-add
-              const __half2 d2 = __half2half2(d);
+              const __half2 dd = __half2half2(d);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __half2 c2 = as_h2(hi[i]), prod = __hmul2_rn(c2, d2);
-                hi[i] = h2(prod);
-                lo[i] = h2(__hfma2(c2, d2, __hneg2(prod)));
+              for (int n = 0; n < 8; ++n) {
+                const __half2 c2 = as_h2(hi[n]), prod = __hmul2_rn(c2, dd);
+                hi[n] = h2(prod);
+                lo[n] = h2(__hfma2(c2, dd, __hneg2(prod)));
               }
             } else {  // the top of f16's range: rounded toward zero, through f32
               const float df = __half2float(d);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 c2 = __half22float2(as_h2(hi[i]));
-                split2_rz(c2.x * df, c2.y * df, hi[i], lo[i]);
+              for (int n = 0; n < 8; ++n) {
+                const float2 c2 = __half22float2(as_h2(hi[n]));
+                split2_rz(c2.x * df, c2.y * df, hi[n], lo[n]);
               }
             }
             // 16-byte chunks of the row: the second column group's threads start with their second
@@ -885,17 +902,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < 2; ++s) {
               const int part = s ^ ((ch >> 2) & 1);
               const int c16 = FMT == LQ_FMT_Q8_0 ? 2 * ch + part : (ch >> 1) * 4 + (ch & 1) + 2 * part;
-              const uint32_t at = (c16 >> 3) * G::GROUP;
-              const uint4 vh = part ? make_uint4(hi[4], hi[5], hi[6], hi[7]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              const uint4 vl = part ? make_uint4(lo[4], lo[5], lo[6], lo[7]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(row, c16 & 7)) = vh;
-              *reinterpret_cast<uint4*>(dst + at + tc::sw128_offset(64 + row, c16 & 7)) = vl;
+              unsigned char* const to = dst + (c16 >> 3) * G::GROUP + tc::sw128_offset(row, c16 & 7);
+              *reinterpret_cast<uint4*>(to) = part ? make_uint4(hi[4], hi[5], hi[6], hi[7]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(to + 64 * 128) = part ? make_uint4(lo[4], lo[5], lo[6], lo[7]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
           }
-          fence_proxy_async_smem();
-          mbar_arrive(fl);
+          if (nn == N / 2 - 1) {
+            fence_proxy_async_smem();
+            mbar_arrive(&bar->full[unit % NU]);
+            ++unit;
+          }
         }
       }
+      if (!alive) break;
       mbar_arrive(&bar->done[tile % kInfo]);
     }
     wait_copies<0>();
@@ -1045,6 +1064,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&bar->unit[un % kUnits]);
           }
           __syncwarp();
+          if (un > 0) {  // its queries, towards the softmax threads
+#pragma unroll 1
+            for (int r = lane; r < kRows; r += 32) {
+              const int rho = w.rt * kRows + r, token = rho / a.group;
+              const float* src = a.Q + (w.s.row0 + token) * a.ldq + static_cast<long long>(w.h * a.group + rho - token * a.group) * D;
+              if (P.vec_q && rho < w.s.rows * a.group) bulk_prefetch_l2(src, D * 4);
+            }
+          }
           ++un;
           k = w.k0;
         }
