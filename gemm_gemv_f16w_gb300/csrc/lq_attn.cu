@@ -192,7 +192,8 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   a.sinks = static_cast<int>(std::min(sinks, most));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int route = g_attn_route.load();
-  if (route == 1) return launch_attn_generic(a, cache->fmt, s);
+  // (without pages the other kernels have no address that they may read)
+  if (route == 1 || a.c.num_pages == 0) return launch_attn_generic(a, cache->fmt, s);
   // the most rows (tokens x query heads a key/value head) of a sequence, as
   // far as the host knows
   const int64_t q = batch->max_q > 0 ? std::min(batch->max_q, batch->tokens) : batch->tokens;

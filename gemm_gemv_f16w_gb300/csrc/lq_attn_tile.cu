@@ -75,8 +75,7 @@ struct TileParams {
   int small_rows;  // sequences with at most this many rows are another kernel's
   int vec_q, vec_o;
   int tma;         // f16: the tensor maps of the pools are there
-  unsigned long long wait_ns;
-  unsigned wait_iters;
+  unsigned wait_hint, wait_clocks;  // how long a poll may block (ns), how long a wait may last (SM cycles)
 };
 
 template <int FMT, int D>
@@ -126,7 +125,6 @@ struct Bars {
   uint64_t join;  // the softmax threads of a unit that spans CTAs
   uint64_t drain;
   uint32_t tmem;
-  volatile int abort;
   int last;
   int start_i, start_h, start_rt, start_k;
   long long per, mine;
@@ -142,14 +140,29 @@ constexpr uint32_t kFirst = 1u << 9;   // the unit's first tile here
 constexpr uint32_t kMixed = 1u << 10;  // some key is seen by some of the rows only
 constexpr uint32_t kAll = 1u << 11;    // every key is there and seen by some row
 
-__device__ __forceinline__ uint64_t desc_mn(uint32_t at) {  // 128-byte swizzle, MN-major: 64-dim groups, 8-key groups
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((at & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((128u * 128u) >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Shared-memory matrix descriptors, 128-byte swizzle, as words: the low one has
+// the address (>> 4) and the leading byte offset, the high one the stride
+// (1024: groups of 8 rows) and the mode. Queries and keys are K-major (leading
+// offset unused); values are MN-major: 64-dim groups 128 rows apart, 8-key groups.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16); }
+// D[tmem] = A B or (ADD) D + A B, f16, A from shared memory or from tensor memory.
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "n"(kDescHigh), "r"(idesc), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "n"(kDescHigh), "r"(idesc), "n"(ADD ? 1 : 0)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
@@ -164,6 +177,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// Waits for the phase of `parity` for at most `clocks` cycles of the SM (below
+// 2^32, so that 32 bits tell). As little code as can be: the roles' loops
+// share the instruction cache.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint32_t hint, uint32_t clocks) {
+  const uint32_t at = smem_u32(bar), t0 = static_cast<uint32_t>(clock());
+  uint32_t ok;
+  do {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(hint)
+        : "memory");
+  } while (ok == 0u && static_cast<uint32_t>(clock()) - t0 < clocks);
+  return ok != 0u;
 }
 // One lane of a converged warp, the same every time; the compiler knows that
 // it is one, and keeps the MMAs' descriptors in uniform registers.
@@ -369,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->join, 256);
-    bar->abort = 0;
     for (int k = 0; k < kInfo; ++k) {
       mbar_init(&bar->told[k], 1);
       mbar_init(&bar->done[k], kLoaders);
@@ -389,13 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = bar->tmem;
 
+  bool in_time = true;  // no wait of this warp has run out
   auto wait = [&](uint64_t* b, uint32_t parity) {  // by whole warps
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity, P.wait_ns, P.wait_iters));
-    if (!ok) {
-      if (lane == 0) record_error(kDevErrTimeout);
-      bar->abort = 1;
-    }
-    return ok;
+    in_time = __all_sync(0xffffffffu, wait_for(b, parity, P.wait_hint, P.wait_clocks));
+    return in_time;
   };
 
   if (wg < 2) {
@@ -755,8 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Raw = typename std::conditional<FMT == LQ_FMT_Q8_0, uint4, uint2>::type;
     Raw ahead[2];
     __half sc_ahead[2];
-    // Quantised: codes and scales of passes 2 nn and 2 nn + 1 of a side.
-    auto fetch = [&](int nn, const TileInfo& c, int side) {
+    bool there[2];
+    // Quantised: codes and scales of the tile's two passes `it`, K's and then V's.
+    auto fetch = [&](int it, const TileInfo& c) {
+      const int side = it / (N / 2), nn = it % (N / 2);
       const unsigned char* const pool = (side ? a.c.v : a.c.k) + ch * (G::ROW * 16 / D);
       const unsigned char* const scales = (side ? a.c.v : a.c.k) + (ch >> 1) * 2;
 #pragma unroll
@@ -764,12 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = row0 + (2 * nn + i) * PASS;
         const longlong2 at = *reinterpret_cast<const longlong2*>(&c.at[2 * (row >> 4)]);
         const int key = c.j0 + row;
-        ahead[i] = Raw{};
-        sc_ahead[i] = __ushort_as_half(0);
-        if (at.x >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end)) {
-          ahead[i] = *reinterpret_cast<const Raw*>(pool + at.x + (row & 15) * G::ROW);
-          sc_ahead[i] = *reinterpret_cast<const __half*>(scales + at.y + (row & 15) * (D / 16));
-        }
+        // unconditional loads (a branch around them holds the loop up): a key that
+        // is not there reads the pool's first bytes, its scale becomes zero at use
+        there[i] = at.x >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end);
+        ahead[i] = *reinterpret_cast<const Raw*>(pool + (there[i] ? at.x + (row & 15) * G::ROW : 0));
+        sc_ahead[i] = *reinterpret_cast<const __half*>(scales + (there[i] ? at.y + (row & 15) * (D / 16) : 0));
       }
     };
     auto report = [&]() {  // f16: the pending unit has landed
@@ -785,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!QUANT || tile == 0) {
         alive = wait(&bar->told[tile % kInfo], (tile / kInfo) & 1u);
         if (!alive) break;
-        if constexpr (QUANT) fetch(0, c, 0);
+        if constexpr (QUANT) fetch(0, c);
       }
       if constexpr (!QUANT) {
 #pragma unroll 1
@@ -838,9 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           pend_screen = side == 1 && (c.flags & kMixed);
         }
       } else {
-        // Two passes at a time, K's and then V's, in one small loop (straight code
-        // for all passes is bound by instruction fetches: 1.4 times as long); the
-        // next two are on their way meanwhile.
+        // Two passes at a time, K's and then V's, in a small loop (straight code for
+        // all passes is bound by instruction fetches); two are on their way.
 #pragma unroll 1
         for (int it = 0; it < N; ++it) {
           const int side = it / (N / 2), nn = it % (N / 2);
@@ -854,14 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             *reinterpret_cast<Raw*>(w4[i]) = ahead[i];
-            d2[i] = sc_ahead[i];
+            d2[i] = there[i] ? sc_ahead[i] : __ushort_as_half(0);
           }
           if (it + 1 < N) {
-            fetch((it + 1) % (N / 2), c, (it + 1) / (N / 2));
+            fetch(it + 1, c);
           } else if (tile + 1 < total) {
             alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
             if (!alive) break;
-            fetch(0, bar->info[(tile + 1) % kInfo], 0);
+            fetch(0, bar->info[(tile + 1) % kInfo]);
           }
           const bool mixed = side == 1 && (c.flags & kMixed);
 #pragma unroll
@@ -925,95 +949,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 12) {
       constexpr uint32_t kQK = tc::idesc_f16_f32(128, 128);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
-      const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
-      uint32_t seen0 = 0, seen1 = 0, units0 = 0, units1 = 0;  // tiles, units of a row tile
+      const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring)), v_desc = desc_mn(smem_u32(ring));
       const long long mine = bar->mine;
+      uint32_t turn = 0;  // parities: bits 0, 1 tiles of a row tile, bits 2, 3 its units, bit 4 the ring
+      uint32_t slot = 0;  // ring unit of the next K or V
       bool alive = true;
-      auto at_unit = [&](uint32_t u) { return ring_at + (u % NU) * G::UNIT; };
-      auto filled = [&](uint32_t u) { return wait(&bar->full[u % NU], (u / NU) & 1u); };
+      auto filled = [&]() { return wait(&bar->full[slot], (turn >> 4) & 1u); };
+      auto advance = [&]() {
+        if (++slot == NU) {
+          slot = 0;
+          turn ^= 16u;
+        }
+      };
       // Order: PV of a row tile, then its next QK, while the other's softmax
       // runs. MMAs of one thread run in order, so that QK may overwrite the P
       // that the PV before it reads. Between units both PVs come first: the
       // next queries are written when both row tiles are done.
-      uint32_t flags = 0;
+      uint32_t flags = 0, vslot = 0, kslot = 0;
 #pragma unroll 1
       for (long long tile = -1; tile < mine && mine > 0 && alive; ++tile) {
-        const uint32_t v = static_cast<uint32_t>(2 * tile + 1), k = v + 1;  // ring units of this tile's V and the next one's K
         const bool more = tile + 1 < mine;
         uint32_t next = 0;
-        if (tile >= 0) alive = filled(v);
-        if (tile < 0 && alive) {
-          alive = filled(k);
-          next = bar->info[0].flags;
+        bool have = false;
+        if (tile >= 0) {
+          alive = filled();
+          if (!alive) break;
+          vslot = slot;
+          advance();
         }
-        bool have = tile < 0;
 #pragma unroll 1
-        for (int s = 0; s < 4 && alive; ++s) {
+        for (int s = tile < 0 ? 1 : 0; s < 4; ++s) {
           // 0 PV of row tile 0, 1 its QK, 2 PV of row tile 1, 3 its QK; between units 0, 2, 1, 3
-          if (s == 1 && more && !have) {
-            alive = filled(k);
+          if (more && !have && s > 0) {
+            alive = filled();
             if (!alive) break;
+            kslot = slot;
+            advance();
             next = bar->info[(tile + 1) % kInfo].flags;
             have = true;
           }
-          int op = s;
-          if ((next & kFirst) && (s == 1 || s == 2)) op = 3 - s;
+          const int op = (next & kFirst) && (s == 1 || s == 2) ? 3 - s : s;
           const int q = op >> 1;
           if ((op & 1) == 0) {  // O = P V
             if (tile < 0) continue;
             const bool does = q == 0 || (flags & kTwo);
             if (does) {
-              alive = wait(&bar->p_ready[q], (q ? seen1 : seen0) & 1u);
+              alive = wait(&bar->p_ready[q], (turn >> q) & 1u);
               if (!alive) break;
-              if (q) ++seen1; else ++seen0;
+              turn ^= 1u << q;
               tc::fence_after_sync();
             }
             if (elect_one()) {
               if (does) {
-                const uint64_t b0 = desc_mn(at_unit(v));
+                const uint32_t b = v_desc + vslot * (G::UNIT >> 4);
                 const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
                 constexpr int KS = KT / 16;
                 // p_lo v_hi, (quantised) p_hi v_lo, p_hi v_hi: the small ones first
-#pragma unroll 1
-                for (int part = 0; part < 3; ++part) {
-                  if (!QUANT && part == 1) continue;
-                  const uint32_t pa = p + (part == 0 ? 8 : 0);
-                  const uint64_t b = b0 + (part == 1 ? KS * 128 : 0);
-#pragma unroll 4
-                  for (int c = 0; c < KS; ++c) tc::mma_f16_ts(o, pa + 16 * c, b + c * 128, kPV, part == 0 && c == 0 ? 0u : 1u);
+                mma_ts<false>(o, p + 8, b, kPV);
+#pragma unroll
+                for (int c = 1; c < KS; ++c) mma_ts<true>(o, p + 16 * c + 8, b + c * 128, kPV);
+                if constexpr (QUANT) {
+#pragma unroll
+                  for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + (KS + c) * 128, kPV);
                 }
+#pragma unroll
+                for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + c * 128, kPV);
                 tc::commit(&bar->o_full[q]);
                 mbar_arrive(&bar->o_full[q]);
               }
-              if (q == 1) tc::commit(&bar->empty[v % NU]);  // the last reader of V
+              if (q == 1) tc::commit(&bar->empty[vslot]);  // the last reader of V
             }
             __syncwarp();
           } else if (more) {  // S = Q K^T of the next tile
             const bool does = q == 0 || (next & kTwo);
             if (does) {
               if (next & kFirst) {
-                alive = wait(&bar->q_ready[q], (q ? units1 : units0) & 1u);
+                alive = wait(&bar->q_ready[q], (turn >> (2 + q)) & 1u);
                 if (!alive) break;
-                if (q) ++units1; else ++units0;
+                turn ^= 4u << q;
               }
               tc::fence_after_sync();
             }
             if (elect_one()) {
               if (does) {
-                const uint64_t b0 = tc::desc_sw128_kmajor(at_unit(k));
-                const uint64_t a0 = tc::desc_sw128_kmajor(q_at + q * 2 * G::QPART);
-#pragma unroll 1
-                for (int part = 1; part >= 0; --part) {  // low parts first
-#pragma unroll 4
-                  for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t off = (c >> 2) * G::GROUP + (c & 3) * 32;
-                    tc::mma_bf16(tmem + q * 128, a0 + ((part * G::QPART + off) >> 4), b0 + (off >> 4), kQK, part == 1 && c == 0 ? 0u : 1u);
-                  }
-                }
+                const uint32_t b = k_desc + kslot * (G::UNIT >> 4), d = tmem + q * 128;
+                const uint32_t hi = q_desc + q * (2 * G::QPART >> 4), lo = hi + (G::QPART >> 4);
+                mma_ss<false>(d, lo, b, kQK);  // low parts first
+#pragma unroll
+                for (int c = 1; c < D / 16; ++c) mma_ss<true>(d, lo + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), b + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), kQK);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) mma_ss<true>(d, hi + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), b + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), kQK);
                 tc::commit(&bar->s_full[q]);
                 mbar_arrive(&bar->s_full[q]);
               }
-              if (q == 1) tc::commit(&bar->empty[k % NU]);  // the last reader of K
+              if (q == 1) tc::commit(&bar->empty[kslot]);  // the last reader of K
             }
             __syncwarp();
           }
@@ -1133,6 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (!in_time && lane == 0) record_error(kDevErrTimeout);
   pdl_launch_dependents();
   __syncwarp();
   tc::fence_before_sync();
@@ -1214,8 +1244,11 @@ lq_status launch_attn_tile(const AttnArgs& a, int fmt, int small_rows, void* wor
   p.small_rows = small_rows;
   p.vec_q = a.ldq % 4 == 0 && aligned_to(a.Q, 16);
   p.vec_o = a.ldo % 4 == 0 && aligned_to(a.O, 16);
-  p.wait_ns = wait_limit_ns();
-  p.wait_iters = wait_limit_iters();
+  // the default limit of 2 s as cycles of a fast clock; a debugging limit below
+  // one millisecond gives up at the first poll that fails
+  const unsigned long long ns = wait_limit_ns();
+  p.wait_hint = ns < 1000000ull ? 0u : 10000000u;
+  p.wait_clocks = ns < 1000000ull ? 0u : static_cast<unsigned>(std::min(ns * 2, 4200000000ull));
   const int ctas = std::max(1, std::min(device_info().sm_count, kAttnMaxCtas));
   switch (fmt) {
     case LQ_FMT_F16: return pick<LQ_FMT_F16>(p, ctas, stream);
