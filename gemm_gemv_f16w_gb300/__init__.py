@@ -325,6 +325,7 @@ class KVCache:
         self.struct = KVCacheStruct(code, int(page_size), int(kv_heads), int(head_dim), int(num_pages),
                                     _ptr(self.k), _ptr(self.v))
         self.ref = ctypes.byref(self.struct)
+        self.head_dim, self.width = int(head_dim), int(kv_heads) * int(head_dim)
 
 
 class KVBatch:
@@ -342,34 +343,56 @@ class KVBatch:
         self.ref = ctypes.byref(self.struct)
 
 
-def _rows(x, batch, width, what):
+def _rows(x, tokens, width, what):
     """(address, leading dimension) of f32 rows [tokens, heads, head_dim] or
     [tokens, heads * head_dim]; a raw address is taken as tightly packed."""
     if x is None or isinstance(x, int):
         return x or 0, width
     shape, strides = x.shape, x.stride()
-    per_row = x.numel() // shape[0] if shape[0] else width
-    if str(x.dtype) != "torch.float32" or len(shape) not in (2, 3) or shape[0] < batch.tokens or per_row != width:
-        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 [tokens, heads, head_dim] wanted, got {tuple(shape)} {x.dtype}")
-    if strides[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and strides[1] != shape[2]):
-        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: heads and dims have to be contiguous")
-    return x.data_ptr(), strides[0] if shape[0] > 1 else width
+    rank, rows = len(shape), shape[0]
+    ok = rows >= tokens and strides[-1] == 1 and x.dtype.itemsize == 4 and x.is_floating_point()
+    if rank == 3:
+        ok = ok and shape[1] * shape[2] == width and (strides[1] == shape[2] or shape[1] == 1)
+    else:
+        ok = ok and rank == 2 and shape[1] == width
+    if not ok:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 [tokens, heads, head_dim] with contiguous heads and dims wanted, "
+                                          f"got {tuple(shape)} {x.dtype}, strides {strides}")
+    return x.data_ptr(), strides[0] if rows > 1 else width
+
+
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The handle of torch's current stream, by the quickest way there is."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.current_stream()  # initialises CUDA
+        _raw_stream = (lambda: get(device())) if get and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def lq_kv_write(cache, batch, K, V, stream=None) -> None:
     """Stores the batch's tokens in the cache; K, V: float32 [tokens,
     kv_heads, head_dim] (token-strided slices allowed). See include/lq.h."""
-    c = cache.struct
-    (k, ldk), (v, ldv) = (_rows(x, batch, c.kv_heads * c.head_dim, "lq_kv_write") for x in (K, V))
-    _check(lib().lq_kv_write(cache.ref, batch.ref, k, ldk, v, ldv, _stream(stream)), "lq_kv_write")
+    k, ldk = _rows(K, batch.tokens, cache.width, "lq_kv_write")
+    v, ldv = _rows(V, batch.tokens, cache.width, "lq_kv_write")
+    st = (_lib or lib()).lq_kv_write(cache.ref, batch.ref, k, ldk, v, ldv, _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_kv_write")
 
 
 def lq_kv_read(cache, batch, K, V, stream=None) -> None:
     """Reads the batch's tokens back as float32 into K and V (either may be
     None). See include/lq.h."""
-    c = cache.struct
-    (k, ldk), (v, ldv) = (_rows(x, batch, c.kv_heads * c.head_dim, "lq_kv_read") for x in (K, V))
-    _check(lib().lq_kv_read(cache.ref, batch.ref, k, ldk, v, ldv, _stream(stream)), "lq_kv_read")
+    k, ldk = _rows(K, batch.tokens, cache.width, "lq_kv_read")
+    v, ldv = _rows(V, batch.tokens, cache.width, "lq_kv_read")
+    st = (_lib or lib()).lq_kv_read(cache.ref, batch.ref, k, ldk, v, ldv, _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_kv_read")
 
 
 def attn_work(cache, batch, heads, device=None):
@@ -387,19 +410,21 @@ def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=N
     sinks; lse: float32 [tokens, heads] or None; work: attn_work(...), which a
     program keeps (None makes one for this call). ``heads`` is needed where Q
     is not a three-dimensional tensor. See include/lq.h."""
-    D = cache.struct.head_dim
+    D = cache.head_dim
     if heads is None:
         heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // D
     if work is None:
         if stream is not None:
             raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: a call on a stream of its own brings its work buffer")
         work = attn_work(cache, batch, heads)
-    q, ldq = _rows(Q, batch, heads * D, "lq_attn_paged")
-    o, ldo = _rows(O, batch, heads * D, "lq_attn_paged")
+    q, ldq = _rows(Q, batch.tokens, heads * D, "lq_attn_paged")
+    o, ldo = _rows(O, batch.tokens, heads * D, "lq_attn_paged")
     if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()):
         raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: lse is a contiguous float32 [tokens, heads]")
-    _check(lib().lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, _ptr(lse), heads, scale, window, sinks, _ptr(work),
-                               _stream(stream)), "lq_attn_paged")
+    st = (_lib or lib()).lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, _ptr(lse), heads, scale, window, sinks, _ptr(work),
+                                       _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_attn_paged")
 
 
 def attn_route(route: int) -> None:

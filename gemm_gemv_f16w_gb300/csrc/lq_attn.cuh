@@ -25,7 +25,8 @@ lq_status launch_attn_generic(const AttnArgs& a, int fmt, cudaStream_t stream);
 
 // The work buffer: arrival counters (zero between calls), then partial results.
 constexpr int kAttnMaxCtas = 256;
-constexpr size_t kAttnCounterBytes = 4096;
+constexpr size_t kAttnCounterBytes = 4096;  // counters by CTA, and by slot (two a CTA)
+static_assert(3 * kAttnMaxCtas * sizeof(int) <= kAttnCounterBytes);
 
 // Rows of 8 on warp-level MMAs (lq_attn_warp.cu); `rows`: the most rows
 // (tokens * group) a sequence is expected to have, small_rows: sequences with

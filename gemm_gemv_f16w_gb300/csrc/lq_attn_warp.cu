@@ -46,7 +46,8 @@ __device__ unsigned g_attnw_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnw_err, 0u, code); }
 
 constexpr int kTile = 16;            // keys of a tile: never crosses a page
-constexpr int kMinTiles = 32;        // tiles worth a CTA
+constexpr int kMinTiles = 16;        // tiles worth a CTA
+constexpr int kJoin = 8;              // partial results that one CTA joins at once
 constexpr float kNoMax = -1e30f;     // M before the first key
 constexpr float kLift = 11.0f;       // how far M stays below the maximum
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,7 +65,7 @@ struct WarpParams {
 template <int FMT, int D, int NR>
 struct Geo {
   static constexpr int W = FMT == LQ_FMT_F16 && D == 256 ? 4 : 8;  // warps
-  static constexpr int TPS = (FMT == LQ_FMT_Q4_0 && D <= 128) || D == 64 ? 2 : 1;  // tiles a step
+  static constexpr int TPS = (FMT != LQ_FMT_F16 && D == 128) || D == 64 ? 2 : 1;  // tiles a step
   static constexpr int ROW = FMT == LQ_FMT_F16 ? 2 * D : (FMT == LQ_FMT_Q8_0 ? D : D / 2);
   // pitches: the eight rows (or 4 x 32, 8 x 16 bytes) of a fragment load fall
   // into different banks
@@ -135,12 +136,36 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
-// (x, y) as two f16 pairs, high parts and what they leave.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
+// A pair as two f16 pairs, high parts and what they leave.
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  const float2 r = ffma2(__half22float2(h), make_float2(-1.0f, -1.0f), x);
   hi = h2(h);
-  lo = h2(__floats2half2_rn(x - f.x, y - f.y));
+  lo = h2(__floats2half2_rn(r.x, r.y));
+}
+// N words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4);
+  if constexpr (N == 1) {
+    w[0] = lds32(at);
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(at);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    const uint4 v = lds128(at);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+}
+// f16 number i of packed words.
+template <int N>
+__device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i) {
+  const __half2 h = as_h2(w[i >> 1]);
+  return (i & 1) ? __high2float(h) : __low2float(h);
 }
 
 // Four int8 codes (a word) as two f16 pairs: (code + 128) in the mantissa of
@@ -244,15 +269,34 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     if (rows == 0 || (P.small_rows && rows > P.small_rows)) return 0;
     return static_cast<long long>((rows + R - 1) / R) * H * tiles_of(s, a.window, a.sinks).n;
   };
-  long long total = 0;
-  for (int i = tid; i < a.b.batch; i += W * 32) total += cost(i);
+  // inclusive sums over the block's threads, and the block's total in scan[W]
+  auto block_scan = [&](long long mine, long long& all) {
+    long long incl = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) scan[warp] = total;
-  __syncthreads();
-  total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();  // scan[] is free
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    all = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) total += scan[w];
+    for (int w = 0; w < W; ++w) {
+      if (w == warp) incl += all;
+      all += scan[w];
+    }
+    return incl;
+  };
+  long long first_cost = cost(tid), first_all, total;
+  const long long first_incl = block_scan(first_cost, first_all);
+  total = first_all;
+#pragma unroll 1
+  for (int base = W * 32; base < a.b.batch; base += W * 32) {  // batches beyond the block's threads
+    long long all;
+    block_scan(cost(base + tid), all);
+    total += all;
+  }
   const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
   long long x0 = per * blockIdx.x;
   const long long x1 = min(x0 + per, total);
@@ -262,33 +306,23 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   }
   // the sequence that x0 falls into
   long long before = 0;
+#pragma unroll 1
   for (int base = 0;; base += W * 32) {
-    __syncthreads();  // scan[] is free
-    const long long mine = cost(base + tid);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+    long long mine = first_cost, all = first_all, incl = first_incl;
+    if (base > 0) {
+      mine = cost(base + tid);
+      incl = block_scan(mine, all);
     }
-    if (lane == 31) scan[warp] = incl;
-    if (tid == 0) scan[W] = -1;
-    __syncthreads();
-    long long at = before, sum = before;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) at += scan[w];
-      sum += scan[w];
-    }
-    incl += at;
-    if (x0 >= incl - mine && x0 < incl) {
+    incl += before;
+    const bool here = x0 < before + all;
+    if (here && x0 >= incl - mine && x0 < incl) {
       scan[W] = base + tid;
       scan[W + 1] = x0 - (incl - mine);
     }
-    __syncthreads();
-    if (scan[W] >= 0) break;
-    before = sum;
+    if (here) break;
+    before += all;
   }
+  __syncthreads();
   Piece pc;
   auto enter = [&](int i) {  // the first sequence from i on that has work here
     for (;; ++i) {
@@ -312,16 +346,21 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   // ---- a warp's steps of a piece ---------------------------------------------
   const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * S * G::STAGE);
   unsigned char* const ring_ptr = smem + warp * S * G::STAGE;
-  int ids = -1, ids_next = -1;  // pages of 32 tiles: lane -> (step lane / TPS, tile lane % TPS)
+  // 32 of the warp's tiles, lane -> (step lane / TPS, tile lane % TPS): where its
+  // codes and scales begin, its first key and the keys that some row sees
+  long long code_at = 0, scale_at = 0;
+  int first_key = 0;
+  uint32_t seen = 0;
   constexpr int IDS = 32 / TPS;
-  auto tile_at = [&](const Piece& q, int k) { return (k < q.t.sink_tiles ? k : q.t.first + (k - q.t.sink_tiles)) * kTile; };
-  auto look_up = [&](int m) {  // pages of the warp's steps m .. m + IDS - 1
+  auto look_up = [&](int m) {  // the warp's steps m .. m + IDS - 1
     const int k = pc.k0 + (warp + W * (m + lane / TPS)) * TPS + lane % TPS;
-    return k < pc.k1 ? kv::page_of(a.c, a.b, pc.i, tile_at(pc, k)) : -1;
-  };
-  // keys of the tile at j0 that some row of the sequence sees
-  auto seen_by_any = [&](int j0) -> uint32_t {
-    const int p0 = pc.s.len - pc.s.rows;
+    first_key = (k < pc.t.sink_tiles ? k : pc.t.first + (k - pc.t.sink_tiles)) * kTile;
+    const int page = k < pc.k1 ? kv::page_of(a.c, a.b, pc.i, first_key) : -1;
+    const int slot = first_key % page_size;
+    const long long head = max(page, 0) * a.c.page_bytes + pc.h * a.c.head_bytes;
+    code_at = head + static_cast<long long>(slot) * G::ROW;
+    scale_at = head + static_cast<long long>(page_size) * G::ROW + slot * (NB * 2);
+    const int p0 = pc.s.len - pc.s.rows, j0 = first_key;
     const kv::Visible v = kv::visible(max(p0, 0), a.window, a.sinks);
     uint32_t mask = 0xFFFFu;
     if (pc.s.len - j0 < kTile) mask = pc.s.len > j0 ? (1u << (pc.s.len - j0)) - 1u : 0u;
@@ -330,44 +369,47 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       const uint32_t sink = v.sink_end - j0 >= kTile ? 0xFFFFu : (v.sink_end > j0 ? (1u << (v.sink_end - j0)) - 1u : 0u);
       mask &= in | sink;
     }
-    return mask;
+    seen = page >= 0 && LQ_IN_BOUNDS(page < a.c.num_pages && slot + kTile <= page_size && pc.h < H) ? mask : 0u;
   };
+  constexpr int CH = G::ROW / 16;     // 16-byte chunks of a row
+  constexpr int CN = kTile * CH / 32; // chunks a lane
+  static_assert(CN >= 1);
+  const int row0 = lane / CH, col0 = lane % CH;  // the lane's first chunk; the others are 32 / CH rows on
   auto load = [&](int m) {  // the copies of step m (a group even if empty)
-    if (m % IDS == 0) {
-      ids = m == 0 ? look_up(0) : ids_next;
-      ids_next = look_up(m + IDS);
-    }
-    const int k = pc.k0 + (warp + W * m) * TPS;
-    if (k < pc.k1) {
+    if (m % IDS == 0) look_up(m);
+    if (pc.k0 + (warp + W * m) * TPS < pc.k1) {
       const uint32_t stage = ring + static_cast<uint32_t>(m % S) * G::STAGE;
 #pragma unroll
       for (int t = 0; t < TPS; ++t) {
-        const int page = __shfl_sync(0xffffffffu, ids, (m % IDS) * TPS + t);
-        const int j0 = tile_at(pc, k + t);
-        const uint32_t mask = page >= 0 && k + t < pc.k1 ? seen_by_any(j0) : 0u;
-        const int slot = j0 % page_size;
-        const long long at = max(page, 0) * a.c.page_bytes + pc.h * a.c.head_bytes;
-        const bool in = LQ_IN_BOUNDS(page < a.c.num_pages && slot + kTile <= page_size && pc.h < H);
+        const int from = (m % IDS) * TPS + t;
+        const long long at = __shfl_sync(0xffffffffu, code_at, from);
+        const uint32_t mask = __shfl_sync(0xffffffffu, seen, from);
+        const int j0 = __shfl_sync(0xffffffffu, first_key, from);
         const uint32_t dst = stage + G::HEAD + t * G::TILE;
-        const unsigned char* ks = a.c.k + at + slot * G::ROW;
-        const unsigned char* vs = a.c.v + at + slot * G::ROW;
-        constexpr int CH = G::ROW / 16;               // 16-byte chunks of a row
-        constexpr int N = kTile * CH / 32;            // chunks a lane
-        static_assert(N >= 1);
+        const uint32_t kd = dst + row0 * G::KP + col0 * 16, vd = dst + kTile * G::KP + row0 * G::VP + col0 * 16;
+        const unsigned char* ks = a.c.k + at + lane * 16;
+        const unsigned char* vs = a.c.v + at + lane * 16;
+        if (mask == 0xFFFFu) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int id = n * 32 + lane, row = id / CH, col = id % CH;
-          const bool there = in && ((mask >> row) & 1u);
-          copy16(dst + row * G::KP + col * 16, ks + row * G::ROW + col * 16, there);
-          copy16(dst + kTile * G::KP + row * G::VP + col * 16, vs + row * G::ROW + col * 16, there);
+          for (int n = 0; n < CN; ++n) {
+            cp_async16(kd + n * (32 / CH) * G::KP, ks + n * 512);
+            cp_async16(vd + n * (32 / CH) * G::VP, vs + n * 512);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < CN; ++n) {
+            const bool there = (mask >> (row0 + n * (32 / CH))) & 1u;
+            copy16(kd + n * (32 / CH) * G::KP, ks + n * 512, there);
+            copy16(vd + n * (32 / CH) * G::VP, vs + n * 512, there);
+          }
         }
         if constexpr (FMT != LQ_FMT_F16) {
-          const long long sat = at + static_cast<long long>(page_size) * G::ROW + slot * (NB * 2);
+          const long long sat = __shfl_sync(0xffffffffu, scale_at, from);
           constexpr int SC = G::SB / 16;  // chunks of a side's scales
           const int side = lane / SC;
           if (side < 2)
             copy16(dst + kTile * (G::KP + G::VP) + side * G::SB + (lane % SC) * 16,
-                   (side ? a.c.v : a.c.k) + sat + (lane % SC) * 16, in && page >= 0);
+                   (side ? a.c.v : a.c.k) + sat + (lane % SC) * 16, mask != 0u);
         }
         if (lane == 0)
           *reinterpret_cast<int2*>(ring_ptr + (m % S) * G::STAGE + t * 8) = make_int2(j0, static_cast<int>(mask));
@@ -424,16 +466,17 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         qr[i][3] = v.w;
       }
     }
-    float f[NR], M[NR], l[NR], om[NR][D / 8][2];
+    float f[NR], M[NR];
+    float2 l[NR], om[NR][D / 8];
     int pos[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       f[n] = row_f[n * 8 + g];
       M[n] = kNoMax;
-      l[n] = 0.0f;
+      l[n] = make_float2(0.0f, 0.0f);
       pos[n] = pc.s.len - pc.s.rows + min(rho0 + n * 8 + g, rows_all - 1) / group;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) om[n][i][0] = om[n][i][1] = 0.0f;
+      for (int i = 0; i < D / 8; ++i) om[n][i] = make_float2(0.0f, 0.0f);
     }
     const int p_first = pc.s.len - pc.s.rows + rho0 / group;
     const int p_last = pc.s.len - pc.s.rows + min(rho0 + R - 1, rows_all - 1) / group;
@@ -459,44 +502,67 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         mixed = mixed || (!clear && pc.s.rows > 1);
       }
       // ---- logits ---------------------------------------------------------------
-      float x[NR][TPS * 2][2];
+      constexpr int NT = TPS * 2;  // n-tiles of 8 keys
+      float2 x[NR][NT];
+      auto query = [&](int n, int i, uint32_t (&q4)[4]) {  // MMA i of a row tile's query
+        if constexpr (G::QREG) {
 #pragma unroll
-      for (int nt = 0; nt < TPS * 2; ++nt) {
-        const uint32_t tk = t0 + (nt >> 1) * G::TILE;
-        float s[NR][2];
-        if constexpr (FMT == LQ_FMT_F16) {
-          float acc[NR][4] = {};
-          const uint32_t at = tk + ((nt & 1) * 8 + (lane & 7)) * G::KP + (lane >> 3) * 16;
+          for (int j = 0; j < 4; ++j) q4[j] = qr[n * NB * 2 + i][j];
+        } else {
+          const uint4 v = lds128(qf + (n * NB * 2 + i) * 512 + lane * 16);
+          q4[0] = v.x;
+          q4[1] = v.y;
+          q4[2] = v.z;
+          q4[3] = v.w;
+        }
+      };
+      if constexpr (FMT == LQ_FMT_F16) {
+        float acc[NR][NT][4] = {};
+        const uint32_t at = t0 + (lane & 7) * G::KP + (lane >> 3) * 16;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < NB; ++b) {
+          uint32_t q4[NR][2][4];
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) query(n, 2 * b + h, q4[n][h]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
             uint32_t kf[4];
-            ldmatrix4(kf, at + b * 64);
+            ldmatrix4(kf, at + (nt >> 1) * G::TILE + (nt & 1) * 8 * G::KP + b * 64);
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if constexpr (G::QREG) {
-                  mma_f16(acc[n], qr[(n * NB + b) * 2 + h], kf[2 * h], kf[2 * h + 1]);
-                } else {
-                  const uint4 v = lds128(qf + ((n * NB + b) * 2 + h) * 512 + lane * 16);
-                  const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
-                  mma_f16(acc[n], q4, kf[2 * h], kf[2 * h + 1]);
-                }
-              }
+              mma_f16(acc[n][nt], q4[n][0], kf[0], kf[1]);
+              mma_f16(acc[n][nt], q4[n][1], kf[2], kf[3]);
             }
           }
+        }
 #pragma unroll
-          for (int n = 0; n < NR; ++n) {
-            s[n][0] = acc[n][0] + acc[n][2];
-            s[n][1] = acc[n][1] + acc[n][3];
-          }
-        } else {
-          const uint32_t row = tk + ((nt & 1) * 8 + g) * G::KP;
-          const uint32_t sc = tk + kTile * (G::KP + G::VP) + ((nt & 1) * 8 + 2 * c) * (NB * 2);
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = 0.0f;
+          for (int nt = 0; nt < NT; ++nt)
+            x[n][nt] = fmul2(fadd2(make_float2(acc[n][nt][0], acc[n][nt][1]), make_float2(acc[n][nt][2], acc[n][nt][3])), make_float2(f[n], f[n]));
+      } else {
+        uint32_t kd[NT][2][NB / 2];  // scales of the keys 2c, 2c + 1 of each 8
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            lds_words(t0 + (nt >> 1) * G::TILE + kTile * (G::KP + G::VP) + ((nt & 1) * 8 + 2 * c + j) * (NB * 2), kd[nt][j]);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[n][nt] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t q4[NR][2][4];
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) query(n, 2 * b + h, q4[n][h]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t row = t0 + (nt >> 1) * G::TILE + ((nt & 1) * 8 + g) * G::KP;
             uint32_t kf[4];
             if constexpr (FMT == LQ_FMT_Q8_0) {
               const uint2 w = lds64(row + b * 32 + c * 8);
@@ -509,31 +575,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
               kf[2] = nibbles_hi(w);
               kf[3] = nibbles_hi(w8);
             }
-            const float d0 = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(sc + b * 2))));
-            const float d1 = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(sc + NB * 2 + b * 2))));
+            const float2 d = make_float2(half_at(kd[nt][0], b), half_at(kd[nt][1], b));
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
               float acc[4] = {};
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if constexpr (G::QREG) {
-                  mma_f16(acc, qr[(n * NB + b) * 2 + h], kf[2 * h], kf[2 * h + 1]);
-                } else {
-                  const uint4 v = lds128(qf + ((n * NB + b) * 2 + h) * 512 + lane * 16);
-                  const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
-                  mma_f16(acc, q4, kf[2 * h], kf[2 * h + 1]);
-                }
-              }
-              s[n][0] = fmaf(d0, acc[0] + acc[2], s[n][0]);
-              s[n][1] = fmaf(d1, acc[1] + acc[3], s[n][1]);
+              mma_f16(acc, q4[n][0], kf[0], kf[1]);
+              mma_f16(acc, q4[n][1], kf[2], kf[3]);
+              x[n][nt] = ffma2(d, fadd2(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3])), x[n][nt]);
             }
           }
         }
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          x[n][nt][0] = s[n][0] * f[n];
-          x[n][nt][1] = s[n][1] * f[n];
-        }
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[n][nt] = fmul2(x[n][nt], make_float2(f[n], f[n]));
       }
       // ---- masks: bit 2 nt + j of vis[n] is key 8 nt + 2c + j for the lane's row --
       uint32_t vis[NR];
@@ -551,53 +606,53 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
                                (a.window == 0 || key > pos[n] - a.window || key < a.sinks);
               if (!see) {
                 vis[n] &= ~(1u << (2 * nt + j));
-                x[n][nt][j] = -INFINITY;
+                if (j == 0) x[n][nt].x = -INFINITY; else x[n][nt].y = -INFINITY;
               }
             }
         }
       }
       // ---- values' scales: thread's keys 2c, 2c + 1 of each 8 --------------------
-      float ld[TPS * 2][2];  // log2 of the largest |d| of a key
+      uint32_t vd[FMT == LQ_FMT_F16 ? 1 : NT][2][FMT == LQ_FMT_F16 ? 1 : NB / 2];
+      float2 ld[NT];  // log2 of the largest |d| of a key
       if constexpr (FMT != LQ_FMT_F16) {
 #pragma unroll
-        for (int nt = 0; nt < TPS * 2; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t sc = t0 + (nt >> 1) * G::TILE + kTile * (G::KP + G::VP) + G::SB + ((nt & 1) * 8 + 2 * c + j) * (NB * 2);
-            __half2 top = as_h2(lds32(sc) & 0x7FFF7FFFu);
+            lds_words(t0 + (nt >> 1) * G::TILE + kTile * (G::KP + G::VP) + G::SB + ((nt & 1) * 8 + 2 * c + j) * (NB * 2), vd[nt][j]);
+            __half2 top = as_h2(vd[nt][j][0] & 0x7FFF7FFFu);
 #pragma unroll
-            for (int b = 2; b < NB; b += 2) top = __hmax2(top, as_h2(lds32(sc + b * 2) & 0x7FFF7FFFu));
-            ld[nt][j] = fmaxf(lg2(fmaxf(__low2float(top), __high2float(top))), -24.0f);
+            for (int w = 1; w < NB / 2; ++w) top = __hmax2(top, as_h2(vd[nt][j][w] & 0x7FFF7FFFu));
+            const float e = fmaxf(lg2(fmaxf(__low2float(top), __high2float(top))), -24.0f);
+            if (j == 0) ld[nt].x = e; else ld[nt].y = e;
           }
+        }
       }
       // ---- running maximum, weights ----------------------------------------------
-      float p[NR][TPS * 2][2];
+      float2 p[NR][NT];
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         float top = -INFINITY;
 #pragma unroll
-        for (int nt = 0; nt < TPS * 2; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) top = fmaxf(top, FMT == LQ_FMT_F16 ? x[n][nt][j] : x[n][nt][j] + ld[nt][j]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 y = FMT == LQ_FMT_F16 ? x[n][nt] : fadd2(x[n][nt], ld[nt]);
+          top = fmaxf(top, fmaxf(y.x, y.y));
+        }
         if (__any_sync(0xffffffffu, top > M[n] + 15.0f)) {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const float to = fmaxf(M[n], top - kLift), keep = ex2(M[n] - to);
           M[n] = to;
-          l[n] *= keep;
+          l[n] = fmul2(l[n], make_float2(keep, keep));
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            om[n][i][0] *= keep;
-            om[n][i][1] *= keep;
-          }
+          for (int i = 0; i < D / 8; ++i) om[n][i] = fmul2(om[n][i], make_float2(keep, keep));
         }
 #pragma unroll
-        for (int nt = 0; nt < TPS * 2; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p[n][nt][j] = ex2(x[n][nt][j] - M[n]);
-            l[n] += p[n][nt][j];
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 y = fadd2(x[n][nt], make_float2(-M[n], -M[n]));
+          p[n][nt] = make_float2(ex2(y.x), ex2(y.y));
+          l[n] = fadd2(l[n], p[n][nt]);
+        }
       }
       // ---- weighted values ---------------------------------------------------------
       if constexpr (FMT == LQ_FMT_F16) {
@@ -621,8 +676,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int t = 0; t < TPS; ++t) {
-              split2(p[n][2 * t][0], p[n][2 * t][1], pa[n][t][0], pa[n][t][1]);
-              split2(p[n][2 * t + 1][0], p[n][2 * t + 1][1], pa[n][t][2], pa[n][t][3]);
+              split2(p[n][2 * t], pa[n][t][0], pa[n][t][1]);
+              split2(p[n][2 * t + 1], pa[n][t][2], pa[n][t][3]);
             }
           const uint32_t at = t0 + kTile * G::KP + ((lane & 7) + ((lane >> 3) & 1) * 8) * G::VP + (lane >> 4) * 16;
 #pragma unroll
@@ -641,10 +696,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                om[n][2 * d + h][0] += acc[n][h][0] + acc[n][h][2];
-                om[n][2 * d + h][1] += acc[n][h][1] + acc[n][h][3];
-              }
+              for (int h = 0; h < 2; ++h)
+                om[n][2 * d + h] = fadd2(om[n][2 * d + h], fadd2(make_float2(acc[n][h][0], acc[n][h][1]), make_float2(acc[n][h][2], acc[n][h][3])));
           }
         } else {  // key by key, leaving out what a row does not see
 #pragma unroll
@@ -655,15 +708,14 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
               const int from = (lane & ~3) | (kk >> 1);
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
-                const float w0 = __shfl_sync(0xffffffffu, p[n][nt][0], from), w1 = __shfl_sync(0xffffffffu, p[n][nt][1], from);
+                const float w0 = __shfl_sync(0xffffffffu, p[n][nt].x, from), w1 = __shfl_sync(0xffffffffu, p[n][nt].y, from);
                 const uint32_t vv = __shfl_sync(0xffffffffu, vis[n], from);
                 const float w = (kk & 1) ? w1 : w0;
                 if ((vv >> (2 * nt + (kk & 1))) & 1u) {
 #pragma unroll
                   for (int i = 0; i < D / 8; ++i) {
                     const float2 v = __half22float2(as_h2(lds32(row + i * 16 + c * 4)));
-                    om[n][i][0] = fmaf(w, v.x, om[n][i][0]);
-                    om[n][i][1] = fmaf(w, v.y, om[n][i][1]);
+                    om[n][i] = ffma2(make_float2(w, w), v, om[n][i]);
                   }
                 }
               }
@@ -676,26 +728,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
           for (int t = 0; t < TPS; ++t) {
             const uint32_t tv = t0 + t * G::TILE + kTile * G::KP;
-            const uint32_t sc = tv + kTile * G::VP + G::SB + b * 2;
-            float d[2][2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                d[u][j] = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(sc + (u * 8 + 2 * c + j) * (NB * 2)))));
             uint32_t pa[NR][4];
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-              float w[2][2];
+            for (int u = 0; u < 2; ++u) {
+              const int nt = 2 * t + u;
+              const float2 d = make_float2(half_at(vd[nt][0], b), half_at(vd[nt][1], b));
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  w[u][j] = p[n][2 * t + u][j] * d[u][j];
-                  if (edge && !((vis[n] >> (2 * (2 * t + u) + j)) & 1u)) w[u][j] = 0.0f;  // d may be NaN there
+              for (int n = 0; n < NR; ++n) {
+                float2 w = fmul2(p[n][nt], d);
+                if (edge) {  // the scale of a key that the row does not see may be NaN
+                  w.x = (vis[n] >> (2 * nt)) & 1u ? w.x : 0.0f;
+                  w.y = (vis[n] >> (2 * nt + 1)) & 1u ? w.y : 0.0f;
                 }
-              split2(w[0][0], w[0][1], pa[n][0], pa[n][1]);
-              split2(w[1][0], w[1][1], pa[n][2], pa[n][3]);
+                split2(w, pa[n][2 * u], pa[n][2 * u + 1]);
+              }
             }
             uint32_t vf[4][2];  // n-tile, register
 #pragma unroll
@@ -706,7 +752,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
                 codes8(__byte_perm(w0, w1, 0x5140), vf[0][u], vf[1][u]);
                 codes8(__byte_perm(w0, w1, 0x7362), vf[2][u], vf[3][u]);
               } else {
-                const uint32_t w = lds16(row + b * 16 + g * 2) | (lds16(row + G::VP + b * 16 + g * 2) << 16), w8 = w >> 8;
+                const uint32_t w = __byte_perm(lds16(row + b * 16 + g * 2), lds16(row + G::VP + b * 16 + g * 2), 0x5410), w8 = w >> 8;
                 vf[0][u] = nibbles_lo(w);
                 vf[1][u] = nibbles_lo(w8);
                 vf[2][u] = nibbles_hi(w);
@@ -721,10 +767,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
           for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              om[n][4 * b + i][0] += acc[n][i][0] + acc[n][i][2];
-              om[n][4 * b + i][1] += acc[n][i][1] + acc[n][i][3];
-            }
+            for (int i = 0; i < 4; ++i)
+              om[n][4 * b + i] = fadd2(om[n][4 * b + i], fadd2(make_float2(acc[n][i][0], acc[n][i][1]), make_float2(acc[n][i][2], acc[n][i][3])));
         }
       }
       __syncwarp();  // every lane has read the slot that the next copies take
@@ -754,8 +798,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     // ---- join the warps: halves of them, pairwise -----------------------------------
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
-      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+      l[n].x += l[n].y;
+      l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, 1);
+      l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, 2);
     }
 #pragma unroll
     for (int half = W / 2; half >= 1; half >>= 1) {
@@ -765,10 +810,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2) = make_float2(om[n][i][0], om[n][i][1]);
+            *reinterpret_cast<float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2) = om[n][i];
           if (c == 0) {
             at[R * D + n * 8 + g] = M[n];
-            at[R * D + R + n * 8 + g] = l[n];
+            at[R * D + R + n * 8 + g] = l[n].x;
           }
         }
       }
@@ -780,12 +825,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           const float om2 = at[R * D + n * 8 + g], l2 = at[R * D + R + n * 8 + g];
           const float to = fmaxf(M[n], om2), f1 = ex2(M[n] - to), f2 = ex2(om2 - to);
           M[n] = to;
-          l[n] = l[n] * f1 + l2 * f2;
+          l[n].x = l[n].x * f1 + l2 * f2;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
             const float2 o2 = *reinterpret_cast<const float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2);
-            om[n][i][0] = om[n][i][0] * f1 + o2.x * f2;
-            om[n][i][1] = om[n][i][1] * f1 + o2.y * f2;
+            om[n][i] = ffma2(om[n][i], make_float2(f1, f1), fmul2(o2, make_float2(f2, f2)));
           }
         }
       }
@@ -799,10 +843,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) merge[r * D + o_dim<FMT>(i, c, j)] = om[n][i][j];
+          for (int j = 0; j < 2; ++j) merge[r * D + o_dim<FMT>(i, c, j)] = j == 0 ? om[n][i].x : om[n][i].y;
         if (c == 0) {
           row_m[r] = M[n];
-          row_l[r] = l[n];
+          row_l[r] = l[n].x;
         }
       }
     }
@@ -847,36 +891,43 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     } else {
       // partial sums: the unit's CTAs are c0 .. c1, c0's slot 2 c0 + 1, the others' 2 c
       const long long unit_x0 = x0 - done.k1, unit_x1 = unit_x0 + done.t.n - 1;
-      const int c0 = static_cast<int>(unit_x0 / per), c1 = static_cast<int>(unit_x1 / per);
-      float* mine = P.parts + static_cast<long long>(2 * blockIdx.x + (done.k0 == 0 ? 1 : 0)) * G::SLOT;
+      const int c0 = static_cast<int>(unit_x0 / per), parts = static_cast<int>(unit_x1 / per) - c0 + 1;
+      auto slot_of = [&](int q) { return q == 0 ? 2 * c0 + 1 : 2 * (c0 + q); };
+      auto part_at = [&](int slot) { return P.parts + static_cast<long long>(slot) * G::SLOT; };
+      const int me = static_cast<int>(blockIdx.x) - c0;
+      float* mine = part_at(slot_of(me));
       for (int e = tid; e < R * (D / 4); e += W * 32)
         reinterpret_cast<float4*>(mine)[e] = *reinterpret_cast<const float4*>(merge + e * 4);
       if (tid < R) {
         mine[R * D + tid] = row_m[tid];
         mine[R * D + R + tid] = row_l[tid];
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int before_us = atomicAdd(P.counters + c0, 1);
-        *last_flag = before_us == c1 - c0;
-        if (before_us == c1 - c0) P.counters[c0] = 0;
-      }
-      __syncthreads();
-      if (*last_flag) {
+      // Counts this CTA in; true for the last of n, which leaves the counter at zero.
+      auto last_of = [&](int* counter, int n) {
         __threadfence();
-        const int n = c1 - c0 + 1;
-        auto slot_of = [&](int q) { return P.parts + static_cast<long long>(q == 0 ? 2 * c0 + 1 : 2 * (c0 + q)) * G::SLOT; };
-        // M and l of the unit; the parts' factors
+        __syncthreads();
+        if (tid == 0) {
+          const int before_us = atomicAdd(counter, 1);
+          *last_flag = before_us == n - 1;
+          if (before_us == n - 1) *counter = 0;
+        }
+        __syncthreads();
+        const bool last = *last_flag != 0;
+        if (last) __threadfence();
+        return last;
+      };
+      // Joins n parts, the q-th in slot_at(q), in the order of the keys: into the
+      // first's slot, or (into == null) the output.
+      auto combine = [&](auto&& slot_at, int n, float* into) {
         for (int r = warp; r < R; r += W) {
           float top = kNoMax;
-          for (int q = lane; q < n; q += 32) top = fmaxf(top, __ldcg(slot_of(q) + R * D + r));
+          for (int q = lane; q < n; q += 32) top = fmaxf(top, __ldcg(part_at(slot_at(q)) + R * D + r));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           float sum = 0.0f;
           for (int q = lane; q < n; q += 32) {
-            const float w = ex2(__ldcg(slot_of(q) + R * D + r) - top);
-            sum = fmaf(w, __ldcg(slot_of(q) + R * D + R + r), sum);
+            const float w = ex2(__ldcg(part_at(slot_at(q)) + R * D + r) - top);
+            sum = fmaf(w, __ldcg(part_at(slot_at(q)) + R * D + R + r), sum);
           }
           sum = warp_sum(sum);
           if (lane == 0) {
@@ -889,9 +940,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           const int r = e / (D / 4);
           const float top = row_m[r];
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
           for (int q = 0; q < n; ++q) {
-            const float* at = slot_of(q);
+            const float* at = part_at(slot_at(q));
             const float w = ex2(__ldcg(at + R * D + r) - top);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(at) + e);
             o.x = fmaf(w, v.x, o.x);
@@ -899,9 +950,32 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
             o.z = fmaf(w, v.z, o.z);
             o.w = fmaf(w, v.w, o.w);
           }
-          finish(r, e % (D / 4), o, row_l[r]);
+          if (into) {
+            reinterpret_cast<float4*>(into)[e] = o;
+          } else {
+            finish(r, e % (D / 4), o, row_l[r]);
+          }
         }
-        if (tid < d_rows) finish_lse(tid, row_m[tid], row_l[tid]);
+        if (into) {
+          __syncthreads();  // every thread has read the parts' maxima
+          if (tid < R) {
+            into[R * D + tid] = row_m[tid];
+            into[R * D + R + tid] = row_l[tid];
+          }
+        } else if (tid < d_rows) {
+          finish_lse(tid, row_m[tid], row_l[tid]);
+        }
+      };
+      // Up to kJoin parts are joined by the last CTA of them; more in groups of
+      // kJoin first, so that no CTA reads more than a few dozen of them.
+      if (parts <= kJoin) {
+        if (last_of(P.counters + c0, parts)) combine(slot_of, parts, static_cast<float*>(nullptr));
+      } else {
+        const int g0 = me / kJoin * kJoin, groups = (parts + kJoin - 1) / kJoin;
+        if (last_of(P.counters + kAttnMaxCtas + slot_of(g0), min(kJoin, parts - g0))) {
+          combine([&](int q) { return slot_of(g0 + q); }, min(kJoin, parts - g0), part_at(slot_of(g0)));
+          if (last_of(P.counters + c0, groups)) combine([&](int q) { return slot_of(q * kJoin); }, groups, static_cast<float*>(nullptr));
+        }
       }
     }
     if (!more) return;
