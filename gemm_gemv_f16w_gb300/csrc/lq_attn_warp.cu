@@ -64,8 +64,10 @@ struct WarpParams {
 
 template <int FMT, int D, int NR>
 struct Geo {
-  static constexpr int W = FMT == LQ_FMT_F16 && D == 256 ? 4 : 8;  // warps
-  static constexpr int TPS = (FMT != LQ_FMT_F16 && D == 128) || D == 64 ? 2 : 1;  // tiles a step
+  // warps: what registers and stages allow (Q8_0, head dim 128: 12 warps of 168
+  // registers run a step of 64 sequences in 162 us, 8 in 172, 16 in 190)
+  static constexpr int W = FMT == LQ_FMT_F16 && D == 256 ? 4 : (FMT != LQ_FMT_F16 && D <= 128 && NR == 1 ? 12 : 8);
+  static constexpr int TPS = (FMT == LQ_FMT_Q4_0 && D == 128) || D == 64 ? 2 : 1;  // tiles a step
   static constexpr int ROW = FMT == LQ_FMT_F16 ? 2 * D : (FMT == LQ_FMT_Q8_0 ? D : D / 2);
   // pitches: the eight rows (or 4 x 32, 8 x 16 bytes) of a fragment load fall
   // into different banks
@@ -84,7 +86,7 @@ struct Geo {
   static_assert(S >= 2 && STAGE % 16 == 0 && QF % 16 == 0 && MERGE % 16 == 0);
   static constexpr int SMEM = W * S * STAGE + FIXED;
   static constexpr int SLOT = R * (D + 2);  // floats of a partial result
-  static constexpr bool QREG = NR * D <= 128;  // query fragments in registers
+  static constexpr bool QREG = NR * D <= 128 && W <= 8;  // query fragments in registers
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -92,6 +94,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A B: the first of a sum, without registers that hold zeros.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -422,20 +431,29 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   for (int m = 0; m < S - 1; ++m) load(m);
 
   const float qscale = a.scale * kLog2e;
-  for (;;) {
-    // ---- the unit's query rows, as MMA fragments in shared memory -------------
-    const int rho0 = pc.rt * R, rows_all = pc.s.rows * group;
-    for (int r = warp; r < R; r += W) {
-      const int rho = rho0 + r;
-      float v[NB], top = 0.0f;
-      const bool there = rho < rows_all;
-      const int t = pc.s.row0 + (there ? rho / group : 0);
-      const float* src = a.Q + t * a.ldq + static_cast<long long>(pc.h * group + (there ? rho % group : 0)) * D;
+  // the unit's query rows: asked for early, and stored as MMA fragments in
+  // shared memory (two parts, scaled to the top of f16's range) once it is free
+  constexpr int RPW = (R + W - 1) / W;  // rows a warp
+  float qv[RPW][NB];
+  auto ask_queries = [&]() {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        v[b] = there ? src[b * 32 + lane] : 0.0f;
-        top = fmaxf(top, fabsf(v[b]));
-      }
+    for (int i = 0; i < RPW; ++i) {
+      const int rho = pc.rt * R + warp + i * W;
+      const bool there = warp + i * W < R && rho < pc.s.rows * group;
+      const int token = there ? rho / group : 0;
+      const float* src = a.Q + (pc.s.row0 + token) * a.ldq + static_cast<long long>(pc.h * group + (there ? rho - token * group : 0)) * D;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) qv[i][b] = there ? src[b * 32 + lane] : 0.0f;
+    }
+  };
+  auto store_queries = [&]() {
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const int r = warp + i * W;
+      if (r >= R) break;
+      float top = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) top = fmaxf(top, fabsf(qv[i][b]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // sigma: a power of two that takes the largest |q| to [2^14, 2^15)
@@ -445,7 +463,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       if (lane == 0) row_f[r] = qscale / sigma;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float x = v[b] * sigma;
+        const float x = qv[i][b] * sigma;
         const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
         int mma, cc, pair, half;
         q_place<FMT>(lane, mma, cc, pair, half);
@@ -454,6 +472,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         *reinterpret_cast<__half*>(at + 4) = lo;
       }
     }
+  };
+  ask_queries();
+  for (;;) {
+    store_queries();
+    const int rho0 = pc.rt * R, rows_all = pc.s.rows * group;
     __syncthreads();
     uint32_t qr[G::QREG ? NR * NB * 2 : 1][4];
     if constexpr (G::QREG) {
@@ -517,7 +540,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         }
       };
       if constexpr (FMT == LQ_FMT_F16) {
-        float acc[NR][NT][4] = {};
+        float acc[NR][NT][4];
         const uint32_t at = t0 + (lane & 7) * G::KP + (lane >> 3) * 16;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -532,7 +555,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
             ldmatrix4(kf, at + (nt >> 1) * G::TILE + (nt & 1) * 8 * G::KP + b * 64);
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-              mma_f16(acc[n][nt], q4[n][0], kf[0], kf[1]);
+              if (b == 0) {
+                mma_f16_first(acc[n][nt], q4[n][0], kf[0], kf[1]);
+              } else {
+                mma_f16(acc[n][nt], q4[n][0], kf[0], kf[1]);
+              }
               mma_f16(acc[n][nt], q4[n][1], kf[2], kf[3]);
             }
           }
@@ -578,8 +605,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
             const float2 d = make_float2(half_at(kd[nt][0], b), half_at(kd[nt][1], b));
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-              float acc[4] = {};
-              mma_f16(acc, q4[n][0], kf[0], kf[1]);
+              float acc[4];
+              mma_f16_first(acc, q4[n][0], kf[0], kf[1]);
               mma_f16(acc, q4[n][1], kf[2], kf[3]);
               x[n][nt] = ffma2(d, fadd2(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3])), x[n][nt]);
             }
@@ -682,15 +709,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           const uint32_t at = t0 + kTile * G::KP + ((lane & 7) + ((lane >> 3) & 1) * 8) * G::VP + (lane >> 4) * 16;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
-            float acc[NR][2][4] = {};
+            float acc[NR][2][4];
 #pragma unroll
             for (int t = 0; t < TPS; ++t) {
               uint32_t vf[4];
               ldmatrix4_trans(vf, at + t * G::TILE + d * 32);
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
-                mma_f16(acc[n][0], pa[n][t], vf[0], vf[1]);
-                mma_f16(acc[n][1], pa[n][t], vf[2], vf[3]);
+                if (t == 0) {
+                  mma_f16_first(acc[n][0], pa[n][t], vf[0], vf[1]);
+                  mma_f16_first(acc[n][1], pa[n][t], vf[2], vf[3]);
+                } else {
+                  mma_f16(acc[n][0], pa[n][t], vf[0], vf[1]);
+                  mma_f16(acc[n][1], pa[n][t], vf[2], vf[3]);
+                }
               }
             }
 #pragma unroll
@@ -722,9 +754,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
             }
         }
       } else {
+        auto add_values = [&](const bool masked) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          float acc[NR][4][4] = {};
+          float acc[NR][4][4];
 #pragma unroll
           for (int t = 0; t < TPS; ++t) {
             const uint32_t tv = t0 + t * G::TILE + kTile * G::KP;
@@ -736,7 +769,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
                 float2 w = fmul2(p[n][nt], d);
-                if (edge) {  // the scale of a key that the row does not see may be NaN
+                if (masked) {  // the scale of a key that the row does not see may be NaN
                   w.x = (vis[n] >> (2 * nt)) & 1u ? w.x : 0.0f;
                   w.y = (vis[n] >> (2 * nt + 1)) & 1u ? w.y : 0.0f;
                 }
@@ -762,13 +795,25 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_f16(acc[n][i], pa[n], vf[i][0], vf[i][1]);
+              for (int i = 0; i < 4; ++i) {
+                if (t == 0) {
+                  mma_f16_first(acc[n][i], pa[n], vf[i][0], vf[i][1]);
+                } else {
+                  mma_f16(acc[n][i], pa[n], vf[i][0], vf[i][1]);
+                }
+              }
           }
 #pragma unroll
           for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               om[n][4 * b + i] = fadd2(om[n][4 * b + i], fadd2(make_float2(acc[n][i][0], acc[n][i][1]), make_float2(acc[n][i][2], acc[n][i][3])));
+        }
+        };
+        if (!edge) {  // (two copies: merged into one, every tile pays for the masks)
+          add_values(false);
+        } else {
+          add_values(true);
         }
       }
       __syncwarp();  // every lane has read the slot that the next copies take
@@ -791,11 +836,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       pc.k1 = static_cast<int>(min(static_cast<long long>(pc.t.n), x1 - x0));
 #pragma unroll 1
       for (int n = 0; n < S - 1; ++n) load(n);
+      ask_queries();
     } else {
       pdl_launch_dependents();
     }
 
-    // ---- join the warps: halves of them, pairwise -----------------------------------
+    // ---- join the warps, pairwise, half of them at a time -----------------------------------
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       l[n].x += l[n].y;
@@ -803,8 +849,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, 2);
     }
 #pragma unroll
-    for (int half = W / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
+    for (int n_left = W; n_left > 1; n_left = (n_left + 1) / 2) {
+      const int half = (n_left + 1) / 2;
+      if (warp >= half && warp < n_left) {
         float* at = merge + (warp - half) * (R * (D + 2));
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -818,7 +865,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         }
       }
       __syncthreads();
-      if (warp < half) {
+      if (warp < n_left - half) {
         const float* at = merge + warp * (R * (D + 2));
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
