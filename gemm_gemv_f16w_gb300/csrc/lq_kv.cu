@@ -1,16 +1,25 @@
 // Writing tokens into the paged key/value cache and reading them back.
 //
 // One pass over the data: 8 bytes an element come in or go out as f32, and
-// 2 (f16), 1.0625 (Q8_0) or 0.5625 (Q4_0) as codes and scales, so HBM (or,
-// for a decode step, the launch) bounds both kernels. A warp takes 512
+// 2 (f16), 1.0625 (Q8_0) or 0.5625 (Q4_0) as codes and scales: HBM is the
+// floor (for a decode step, the launch), and instruction issue the first
+// bound: a warp has about 40 cycles for 128 elements. A warp takes 1024
 // consecutive elements of one token's heads, four per lane and load, so that
 // a block of 32 is eight neighbouring lanes: its largest magnitude is three
 // shuffles away, four codes of a lane leave as one 4-byte store (Q4_0: the
 // low-nibble lanes fetch their partners' codes with one shuffle), and the
-// loads of all four groups are in flight before the first is used. The eight
+// loads of all groups are in flight before the first is used. The eight
 // warps of a CTA take consecutive tokens, whose rows are neighbours in a page.
-// The rounding rules are those of the host packers (lq_pack.cpp), with the
-// same float32 steps, so the codes are theirs bit for bit.
+//
+// The rounding rules are those of the host packers (lq_pack.cpp), and the
+// codes are theirs bit for bit, without a division an element: the scale
+// top / 127 comes from the rounded reciprocal by Markstein's correction (the
+// remainder top - 127 q is exact, q + remainder / 127 rounds correctly;
+// checked for every mantissa), and x / d from an approximate reciprocal, whose
+// error (3e-5 at most) cannot change a code unless x / d is within 1e-4 of a
+// half. Blocks with such an element (one in 160), with values beyond the
+// cache's range, NaNs or scales near f32's smallest take the exact divisions.
+// (With the divisions for all, 16384 tokens of 8 x 128 took 69 us to write.)
 #include <algorithm>
 
 #include "lq_device.cuh"
@@ -24,9 +33,10 @@ __device__ unsigned g_kv_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_kv_err, 0u, code); }
 
 constexpr int kKvWarps = 8;
-constexpr int kKvGroups = 4;  // 128-element groups of a warp
+constexpr int kKvGroups = 8;  // 128-element groups of a warp
 constexpr unsigned kLimitBits = 0x477FE000u;  // 65504.0f
 constexpr unsigned kInfBits = 0x7F800000u;
+constexpr unsigned kTinyBits = 0x20000000u;   // 2^-63: remainders and reciprocals stay normal above
 
 struct KvArgs {
   kv::Cache c;
@@ -36,12 +46,13 @@ struct KvArgs {
   long long ld[2];
   int width;           // kv_heads * head_dim
   int sides, only;     // 2: K and V; 1: only K (0) or only V (1)
+  unsigned by_dim;     // ceil(2^32 / head_dim): e / head_dim is the high word of e * by_dim (e < 2^24)
 };
 
-// |x| as bits, clamped to the cache's range; NaNs stay above kInfBits.
-__device__ __forceinline__ unsigned magnitude(float x) {
-  const unsigned u = __float_as_uint(x) & 0x7FFFFFFFu;
-  return u > kInfBits ? u : min(u, kLimitBits);
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float clamped(float x) { return fminf(fmaxf(x, -65504.0f), 65504.0f); }
 
@@ -72,44 +83,70 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
     for (int j = 0; j < 4; ++j) h[j] = __float2half_rn(x[j] == x[j] ? clamped(x[j]) : x[j]);
     if (row) store4<VEC>(row + 2 * e, h);
   } else {
-    unsigned top = 0;
+    unsigned u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, magnitude(x[j]));
-    const unsigned mine = top;
+    for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    const unsigned mine = max(max(u[0], u[1]), max(u[2], u[3]));
+    unsigned top = mine;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool bad = top > kInfBits;  // a NaN in the block
-    float d;
-    alignas(4) unsigned char q[4];
-    if constexpr (FMT == LQ_FMT_Q8_0) {
-      d = __fdiv_rn(__uint_as_float(top), 127.0f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int v = 0;
-        if (!bad && d != 0.0f) v = max(-127, min(127, static_cast<int>(roundf(__fdiv_rn(clamped(x[j]), d)))));
-        q[j] = static_cast<unsigned char>(v);
-      }
-      if (row) store4<VEC>(row + e, q);
-    } else {
+    float m = __uint_as_float(top);
+    if constexpr (FMT == LQ_FMT_Q4_0) {
       // the first element of the largest magnitude gives the scale its sign
       const unsigned holders = __ballot_sync(0xffffffffu, mine == top) >> (lane & 24);
       const int first = __ffs(static_cast<int>(holders & 0xFFu)) - 1;
-      float m = x[3];
+      float own = x[3];
 #pragma unroll
-      for (int j = 2; j >= 0; --j) m = magnitude(x[j]) == mine ? x[j] : m;
-      m = __shfl_sync(0xffffffffu, clamped(m), (lane & 24) + first);
-      d = __fdiv_rn(m, -8.0f);
-      unsigned word = 0;
+      for (int j = 2; j >= 0; --j) own = u[j] == mine ? x[j] : own;
+      m = __shfl_sync(0xffffffffu, own, (lane & 24) + first);
+    }
+    // q = m / 127, or m / -8 (exact)
+    constexpr float kBy127 = 1.0f / 127.0f;
+    float d = m * -0.125f;
+    if constexpr (FMT == LQ_FMT_Q8_0) {
+      const float q = m * kBy127;
+      d = __fmaf_rn(__fmaf_rn(-127.0f, q, m), kBy127, q);
+    }
+    const float by_d = top == 0u ? 0.0f : reciprocal(d);
+    constexpr float kMagic = 12582912.0f + (FMT == LQ_FMT_Q4_0 ? 8.0f : 0.0f);  // 1.5 2^23: the sum's low byte is the code
+    unsigned t[4];
+    float off = 0.0f;  // distance to the nearest integer
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float y = x[j] * by_d;
+      if constexpr (FMT == LQ_FMT_Q4_0) y = fminf(y, 7.25f);  // 7.5 .. 8 is code 15 too
+      const float r = y + kMagic;
+      off = fmaxf(off, fabsf((r - kMagic) - y));
+      t[j] = __float_as_uint(r);
+    }
+    bool bad = false;
+    const bool plain = off < 0.4999f && top <= kLimitBits && (top == 0u || top >= kTinyBits);
+    unsigned word = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    if (__any_sync(0xffffffffu, !plain)) {  // by the definition's own divisions
+      const unsigned capped = top > kInfBits ? top : min(top, kLimitBits);
+      bad = capped > kInfBits;  // a NaN in the block
+      m = clamped(m);
+      d = FMT == LQ_FMT_Q8_0 ? __fdiv_rn(__uint_as_float(capped), 127.0f) : __fdiv_rn(m, -8.0f);
+      word = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        int v = 8;
-        if (!bad && d != 0.0f) v = min(15, static_cast<int>(__fadd_rn(__fdiv_rn(clamped(x[j]), d), 8.5f)));
-        word |= static_cast<unsigned>(v) << (8 * j);
+        int v = FMT == LQ_FMT_Q8_0 ? 0 : 8;
+        if (!bad && d != 0.0f) {
+          const float y = __fdiv_rn(clamped(x[j]), d);
+          v = FMT == LQ_FMT_Q8_0 ? max(-127, min(127, static_cast<int>(roundf(y)))) : min(15, static_cast<int>(__fadd_rn(y, 8.5f)));
+        }
+        word |= (static_cast<unsigned>(v) & 0xFFu) << (8 * j);
       }
-      const unsigned high = __shfl_down_sync(0xffffffffu, word, 4);  // elements + 16
-      word |= high << 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = static_cast<unsigned char>(word >> (8 * j));
+    }
+    if constexpr (FMT == LQ_FMT_Q4_0) {
+      word &= 0x0F0F0F0Fu;
+      word |= __shfl_down_sync(0xffffffffu, word, 4) << 4;  // elements + 16
+    }
+    alignas(4) unsigned char q[4];
+    *reinterpret_cast<unsigned*>(q) = word;
+    if constexpr (FMT == LQ_FMT_Q8_0) {
+      if (row) store4<VEC>(row + e, q);
+    } else {
       if (row && (lane & 4) == 0) store4<VEC>(row + (e >> 5) * 16 + (e & 15), q);
     }
     if (row && (lane & 7) == 0) scales[e >> 5] = bad ? __ushort_as_half(0x7E00) : __float2half_rn(d);
@@ -139,13 +176,13 @@ __device__ __forceinline__ float4 get(const unsigned char* row, const __half* sc
     }
     const float d = __half2float(scales[e >> 5]);
     float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned byte = (w >> (8 * j)) & 0xFFu;
-      const int q = FMT == LQ_FMT_Q8_0 ? static_cast<int>(static_cast<signed char>(byte))
-                                       : static_cast<int>((e & 16) ? byte >> 4 : byte & 15u) - 8;
-      v[j] = d * static_cast<float>(q);
+    if constexpr (FMT == LQ_FMT_Q8_0) {
+      w ^= 0x80808080u;
+    } else {
+      w = ((e & 16) ? w >> 4 : w) & 0x0F0F0F0Fu;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = d * (s8_to_magic(w, j) - (FMT == LQ_FMT_Q8_0 ? kMagicS8 : kMagicQ4));
     return make_float4(v[0], v[1], v[2], v[3]);
   }
 }
@@ -193,7 +230,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
     for (int g = 0; g < kKvGroups; ++g) {
       const int e = first + g * 128;
       if (e - lane * 4 >= a.width) break;  // the warp's last group
-      const int h = e / D, r = e - h * D;
+      const int h = static_cast<int>(__umulhi(static_cast<unsigned>(e), a.by_dim)), r = e - h * D;
       unsigned char* row = nullptr;
       __half* scales = nullptr;
       if (page >= 0 && e < a.width && LQ_IN_BOUNDS(page < a.c.num_pages && h < a.c.kv_heads)) {
@@ -222,6 +259,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
 
 template <bool WRITE>
 lq_status launch(int fmt, KvArgs& a, cudaStream_t stream) {
+  a.by_dim = static_cast<unsigned>(((1ull << 32) + a.c.head_dim - 1) / a.c.head_dim);
   a.sides = WRITE || (a.out[0] && a.out[1]) ? 2 : 1;
   a.only = !WRITE && !a.out[0] ? 1 : 0;
   const unsigned segments = static_cast<unsigned>((a.width + kKvGroups * 128 - 1) / (kKvGroups * 128));
