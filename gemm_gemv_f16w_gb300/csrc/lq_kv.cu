@@ -9,7 +9,7 @@
 // shuffles away, four codes of a lane leave as one 4-byte store (Q4_0: the
 // low-nibble lanes fetch their partners' codes with one shuffle), and the
 // loads of all groups are in flight before the first is used. The eight
-// warps of a CTA take consecutive tokens, whose rows are neighbours in a page.
+// warps of a CTA take 16 consecutive tokens, whose rows are neighbours in a page.
 //
 // The rounding rules are those of the host packers (lq_pack.cpp), and the
 // codes are theirs bit for bit, without a division an element: the scale
@@ -33,10 +33,9 @@ __device__ unsigned g_kv_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_kv_err, 0u, code); }
 
 constexpr int kKvWarps = 8;
+constexpr int kKvTokens = 16;  // tokens of a CTA
 constexpr int kKvGroups = 8;  // 128-element groups of a warp
-constexpr unsigned kLimitBits = 0x477FE000u;  // 65504.0f
-constexpr unsigned kInfBits = 0x7F800000u;
-constexpr unsigned kTinyBits = 0x20000000u;   // 2^-63: remainders and reciprocals stay normal above
+constexpr float kTiny = 1.0842021724855044e-19f;  // 2^-63: remainders and reciprocals stay normal above
 
 struct KvArgs {
   kv::Cache c;
@@ -83,21 +82,19 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
     for (int j = 0; j < 4; ++j) h[j] = __float2half_rn(x[j] == x[j] ? clamped(x[j]) : x[j]);
     if (row) store4<VEC>(row + 2 * e, h);
   } else {
-    unsigned u[4];
+    // (a NaN is lost here and found by the test of the quotients)
+    const float mine = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    float top = mine;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(x[j]) & 0x7FFFFFFFu;
-    const unsigned mine = max(max(u[0], u[1]), max(u[2], u[3]));
-    unsigned top = mine;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float m = __uint_as_float(top);
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float m = top;
     if constexpr (FMT == LQ_FMT_Q4_0) {
       // the first element of the largest magnitude gives the scale its sign
       const unsigned holders = __ballot_sync(0xffffffffu, mine == top) >> (lane & 24);
       const int first = __ffs(static_cast<int>(holders & 0xFFu)) - 1;
       float own = x[3];
 #pragma unroll
-      for (int j = 2; j >= 0; --j) own = u[j] == mine ? x[j] : own;
+      for (int j = 2; j >= 0; --j) own = fabsf(x[j]) == mine ? x[j] : own;
       m = __shfl_sync(0xffffffffu, own, (lane & 24) + first);
     }
     // q = m / 127, or m / -8 (exact)
@@ -107,26 +104,24 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
       const float q = m * kBy127;
       d = __fmaf_rn(__fmaf_rn(-127.0f, q, m), kBy127, q);
     }
-    const float by_d = top == 0u ? 0.0f : reciprocal(d);
+    const float by_d = top == 0.0f ? 0.0f : reciprocal(d);
     constexpr float kMagic = 12582912.0f + (FMT == LQ_FMT_Q4_0 ? 8.0f : 0.0f);  // 1.5 2^23: the sum's low byte is the code
     unsigned t[4];
-    float off = 0.0f;  // distance to the nearest integer
+    bool plain = top <= 65504.0f && (top == 0.0f || top >= kTiny);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float y = x[j] * by_d;
-      if constexpr (FMT == LQ_FMT_Q4_0) y = fminf(y, 7.25f);  // 7.5 .. 8 is code 15 too
+      if constexpr (FMT == LQ_FMT_Q4_0) y = y > 7.25f ? 7.25f : y;  // 7.5 .. 8 is code 15 too (a NaN stays)
       const float r = y + kMagic;
-      off = fmaxf(off, fabsf((r - kMagic) - y));
+      plain = plain && fabsf((r - kMagic) - y) < 0.4999f;  // no half near, no NaN
       t[j] = __float_as_uint(r);
     }
     bool bad = false;
-    const bool plain = off < 0.4999f && top <= kLimitBits && (top == 0u || top >= kTinyBits);
     unsigned word = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
     if (__any_sync(0xffffffffu, !plain)) {  // by the definition's own divisions
-      const unsigned capped = top > kInfBits ? top : min(top, kLimitBits);
-      bad = capped > kInfBits;  // a NaN in the block
-      m = clamped(m);
-      d = FMT == LQ_FMT_Q8_0 ? __fdiv_rn(__uint_as_float(capped), 127.0f) : __fdiv_rn(m, -8.0f);
+      // a NaN in the block: of its eight lanes, any
+      bad = ((__ballot_sync(0xffffffffu, x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3]) >> (lane & 24)) & 0xFFu) != 0u;
+      d = FMT == LQ_FMT_Q8_0 ? __fdiv_rn(fminf(top, 65504.0f), 127.0f) : __fdiv_rn(clamped(m), -8.0f);
       word = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -153,50 +148,81 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
   }
 }
 
-// The four elements e .. e + 3 of a stored row.
+// The codes (and scale) of the four elements e .. e + 3 of a stored row, and
+// the values that they stand for.
+struct Four {
+  uint2 codes;
+  unsigned short scale;
+};
 template <int FMT, bool VEC>
-__device__ __forceinline__ float4 get(const unsigned char* row, const __half* scales, int e) {
+__device__ __forceinline__ Four take4(const unsigned char* row, const __half* scales, int e) {
+  Four f;
+  f.codes = make_uint2(0u, 0u);
+  f.scale = 0;
   if constexpr (FMT == LQ_FMT_F16) {
-    __half h[4];
     if constexpr (VEC) {
-      *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(row + 2 * e);
+      f.codes = __ldg(reinterpret_cast<const uint2*>(row + 2 * e));
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = reinterpret_cast<const __half*>(row)[e + j];
+      const unsigned short* at = reinterpret_cast<const unsigned short*>(row) + e;
+      f.codes = make_uint2(at[0] | static_cast<unsigned>(at[1]) << 16, at[2] | static_cast<unsigned>(at[3]) << 16);
     }
-    return make_float4(__half2float(h[0]), __half2float(h[1]), __half2float(h[2]), __half2float(h[3]));
   } else {
     const unsigned char* at = FMT == LQ_FMT_Q8_0 ? row + e : row + (e >> 5) * 16 + (e & 15);
-    unsigned w = 0;
     if constexpr (VEC) {
-      w = *reinterpret_cast<const unsigned*>(at);
+      f.codes.x = __ldg(reinterpret_cast<const unsigned*>(at));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w |= static_cast<unsigned>(at[j]) << (8 * j);
+      for (int j = 0; j < 4; ++j) f.codes.x |= static_cast<unsigned>(at[j]) << (8 * j);
     }
-    const float d = __half2float(scales[e >> 5]);
-    float v[4];
-    if constexpr (FMT == LQ_FMT_Q8_0) {
-      w ^= 0x80808080u;
-    } else {
-      w = ((e & 16) ? w >> 4 : w) & 0x0F0F0F0Fu;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = d * (s8_to_magic(w, j) - (FMT == LQ_FMT_Q8_0 ? kMagicS8 : kMagicQ4));
-    return make_float4(v[0], v[1], v[2], v[3]);
+    f.scale = __ldg(reinterpret_cast<const unsigned short*>(scales) + (e >> 5));
+  }
+  return f;
+}
+template <int FMT>
+__device__ __forceinline__ float4 values4(const Four& f, int e) {
+  if constexpr (FMT == LQ_FMT_F16) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f.codes.x)), y = __half22float2(*reinterpret_cast<const __half2*>(&f.codes.y));
+    return make_float4(x.x, x.y, y.x, y.y);
+  } else {
+    const float d = __half2float(__ushort_as_half(f.scale));
+    const unsigned w = FMT == LQ_FMT_Q8_0 ? f.codes.x ^ 0x80808080u : ((e & 16) ? f.codes.x >> 4 : f.codes.x) & 0x0F0F0F0Fu;
+    constexpr float kBias = FMT == LQ_FMT_Q8_0 ? kMagicS8 : kMagicQ4;
+    return make_float4(d * (s8_to_magic(w, 0) - kBias), d * (s8_to_magic(w, 1) - kBias), d * (s8_to_magic(w, 2) - kBias),
+                       d * (s8_to_magic(w, 3) - kBias));
   }
 }
 
-// grid: x = groups of kKvWarps tokens, y = sides * (512-element segment) + side
+// grid: x = groups of kKvTokens tokens, y = sides * (512-element segment) + side
 template <int FMT, bool VEC, bool WRITE>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = static_cast<int>(blockIdx.x) * kKvWarps + warp;
   const int which = a.sides == 2 ? static_cast<int>(blockIdx.y & 1u) : a.only;
   const int segment = static_cast<int>(a.sides == 2 ? blockIdx.y >> 1 : blockIdx.y);
   const int first = segment * (kKvGroups * 128) + lane * 4;
-  if (t < a.b.tokens) {
+  // where the CTA's tokens are, a lane each (the chain of loads behind that is
+  // paid once for a warp's two tokens); -2: the token is no sequence's
+  const int t0 = static_cast<int>(blockIdx.x) * kKvTokens;
+  int my_page = -2, my_slot = 0;
+  if (lane < kKvTokens && t0 + lane < a.b.tokens) {
+    const int t = t0 + lane;
+    int lo = 0, n = a.b.batch;  // the last sequence that begins at or before t is in [lo, lo + n)
+    while (n > 1) {
+      const int half = n / 2;
+      const bool right = a.b.q_start[lo + half] <= t;
+      lo = right ? lo + half : lo;
+      n = right ? n - half : half;
+    }
+    if (a.b.q_start[lo] <= t && t < a.b.q_start[lo + 1]) {
+      const kv::Seq s = kv::sequence(a.b, a.c.page_size, lo);
+      const int p = s.len - s.rows + (t - s.row0);
+      my_page = p >= 0 ? kv::page_of(a.c, a.b, lo, p) : -1;
+      my_slot = max(p, 0) % a.c.page_size;
+    }
+  }
+#pragma unroll 1
+  for (int tt = warp; tt < kKvTokens && t0 + tt < a.b.tokens; tt += kKvWarps) {
+    const int t = t0 + tt;
     float4 x[kKvGroups];
     if constexpr (WRITE) {
       const float* in = a.in[which] + t * a.ld[which];
@@ -213,36 +239,56 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
         }
       }
     }
-    const int i = kv::find_sequence(a.b, t, lane);
-    int page = -1, slot = 0;
-    if (i >= 0) {
-      const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
-      const int p = s.len - s.rows + (t - s.row0);
-      if (p >= 0) {
-        page = kv::page_of(a.c, a.b, i, p);
-        slot = p % a.c.page_size;
-      }
-    }
-    unsigned char* pool = which ? a.c.v : a.c.k;
+    const int page = __shfl_sync(0xffffffffu, my_page, tt), slot = __shfl_sync(0xffffffffu, my_slot, tt);
     const int D = a.c.head_dim;
-    const long long scale_at = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
-#pragma unroll
-    for (int g = 0; g < kKvGroups; ++g) {
-      const int e = first + g * 128;
-      if (e - lane * 4 >= a.width) break;  // the warp's last group
-      const int h = static_cast<int>(__umulhi(static_cast<unsigned>(e), a.by_dim)), r = e - h * D;
-      unsigned char* row = nullptr;
-      __half* scales = nullptr;
-      if (page >= 0 && e < a.width && LQ_IN_BOUNDS(page < a.c.num_pages && h < a.c.kv_heads)) {
-        unsigned char* head = pool + page * a.c.page_bytes + h * a.c.head_bytes;
-        row = head + static_cast<long long>(slot) * a.c.row_bytes;
-        scales = reinterpret_cast<__half*>(head + scale_at) + slot * (D / 32);
+    const unsigned head_bytes = static_cast<unsigned>(a.c.head_bytes);  // at most 2^16 tokens of 512 bytes
+    // the token's codes and scales of head 0
+    unsigned char* codes = nullptr;
+    __half* scale0 = nullptr;
+    if (page >= 0 && LQ_IN_BOUNDS(page < a.c.num_pages)) {
+      unsigned char* at = (which ? a.c.v : a.c.k) + page * a.c.page_bytes;
+      codes = at + static_cast<long long>(slot) * a.c.row_bytes;
+      scale0 = reinterpret_cast<__half*>(at + static_cast<long long>(a.c.page_size) * a.c.row_bytes) + slot * (D / 32);
+    }
+    auto place = [&](int e, unsigned char*& row, __half*& scales) {  // the head of element e; its element there
+      const unsigned h = __umulhi(static_cast<unsigned>(e), a.by_dim);
+      row = nullptr;
+      scales = nullptr;
+      if (codes && e < a.width && LQ_IN_BOUNDS(h < static_cast<unsigned>(a.c.kv_heads))) {
+        const unsigned long long at = static_cast<unsigned long long>(h) * head_bytes;
+        row = codes + at;
+        scales = reinterpret_cast<__half*>(reinterpret_cast<unsigned char*>(scale0) + at);
       }
-      if constexpr (WRITE) {
+      return e - static_cast<int>(h) * D;
+    };
+    unsigned char* row;
+    __half* scales;
+    if constexpr (WRITE) {
+#pragma unroll
+      for (int g = 0; g < kKvGroups; ++g) {
+        const int e = first + g * 128;
+        if (e - lane * 4 >= a.width) break;  // the warp's last group
+        const int r = place(e, row, scales);
         put<FMT, VEC>(x[g], r, row, scales, lane);
-      } else if (e < a.width && i >= 0) {
-        const float4 v = row ? get<FMT, VEC>(row, scales, r) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float* out = a.out[which] + t * a.ld[which] + e;
+      }
+    } else if (page != -2) {
+      float* const out0 = a.out[which] + t * a.ld[which] + first;
+      Four got[kKvGroups];  // all on their way before the first is used
+#pragma unroll
+      for (int g = 0; g < kKvGroups; ++g) {
+        got[g].codes = make_uint2(0u, 0u);
+        got[g].scale = 0;
+        const int r = place(first + g * 128, row, scales);
+        if (row) got[g] = take4<FMT, VEC>(row, scales, r);
+      }
+#pragma unroll
+      for (int g = 0; g < kKvGroups; ++g) {
+        const int e = first + g * 128;
+        if (e >= a.width) break;
+        const int r = e - static_cast<int>(__umulhi(static_cast<unsigned>(e), a.by_dim)) * D;
+        // (no place: zeros; a 4-bit code of zero stands for -8 d, d is zero too)
+        const float4 v = values4<FMT>(got[g], r);
+        float* out = out0 + g * 128;
         if constexpr (VEC) {
           *reinterpret_cast<float4*>(out) = v;
         } else {
@@ -269,7 +315,7 @@ lq_status launch(int fmt, KvArgs& a, cudaStream_t stream) {
     vec = vec && (!p || (a.ld[i] % 4 == 0 && aligned_to(p, 16)));
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.b.tokens + kKvWarps - 1) / kKvWarps),
+  cfg.gridDim = dim3(static_cast<unsigned>((a.b.tokens + kKvTokens - 1) / kKvTokens),
                      static_cast<unsigned>(a.sides) * segments);
   cfg.blockDim = dim3(kKvWarps * 32);
   cfg.stream = stream;
