@@ -30,14 +30,12 @@ template <int FMT>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
   __shared__ float part[kGWarps][kMaxDim + 2];
   pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = static_cast<int>(blockIdx.x / a.heads), h = static_cast<int>(blockIdx.x % a.heads);
   const int D = a.c.head_dim, blocks = D / 32, hk = h / a.group;
   const int i = kv::find_sequence(a.b, t, lane);
-  if (i < 0) {  // the whole CTA
-    pdl_launch_dependents();
-    return;
-  }
+  if (i < 0) return;  // the whole CTA
   const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
   const int p = s.len - s.rows + (t - s.row0);
   const kv::Visible see = kv::visible(p, a.window, a.sinks);
@@ -95,7 +93,6 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
     for (int b = 0; b < kMaxDim / 32; ++b)
       if (b < blocks) acc[b] = acc[b] * keep + w * v[b];
   }
-  pdl_launch_dependents();
 #pragma unroll
   for (int b = 0; b < kMaxDim / 32; ++b)
     if (b < blocks) part[warp][b * 32 + lane] = acc[b];

@@ -321,7 +321,7 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   all *= a.c.kv_heads;
-  const long long per = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
+  const long long per = max(kv::quotient(all + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
   long long x = per * blockIdx.x;
   const long long mine = min(per, all - x);
   int i = 0, h = 0, rt = 0;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
       }
       x -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    h = static_cast<int>(x / totals[i]);
+    h = static_cast<int>(kv::quotient(x, totals[i]));
     x -= h * totals[i];
     Work w;
     w.s = kv::sequence(a.b, a.c.page_size, i);
@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* const ring = smem + G::Q;
   Bars* const bar = reinterpret_cast<Bars*>(ring + NU * G::UNIT);
   const AttnArgs& a = P.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
+  // (from lane 0 by a shuffle: the compiler then knows that a warp has one role,
+  // and keeps its addresses and descriptors in uniform registers)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), wg = warp >> 2;
 
   if (tid == 0) {
     for (int u = 0; u < NU; ++u) {
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   pdl_wait();
+  pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
   plan<KT>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
   if (warp == 12) {
     tc::tmem_alloc(&bar->tmem, 512);
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = bar->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
 
   bool in_time = true;  // no wait of this warp has run out
   auto wait = [&](uint64_t* b, uint32_t parity) {  // by whole warps
@@ -950,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kQK = tc::idesc_f16_f32(128, 128);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
       const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring)), v_desc = desc_mn(smem_u32(ring));
-      const long long mine = bar->mine;
+      const int mine = __shfl_sync(0xffffffffu, static_cast<int>(min(max(bar->mine, 0ll), 1ll << 30)), 0);
       uint32_t turn = 0;  // parities: bits 0, 1 tiles of a row tile, bits 2, 3 its units, bit 4 the ring
       uint32_t slot = 0;  // ring unit of the next K or V
       bool alive = true;
@@ -967,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // next queries are written when both row tiles are done.
       uint32_t flags = 0, vslot = 0, kslot = 0;
 #pragma unroll 1
-      for (long long tile = -1; tile < mine && mine > 0 && alive; ++tile) {
+      for (int tile = -1; tile < mine && mine > 0 && alive; ++tile) {
         const bool more = tile + 1 < mine;
         uint32_t next = 0;
         bool have = false;
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!alive) break;
             kslot = slot;
             advance();
-            next = bar->info[(tile + 1) % kInfo].flags;
+            next = __shfl_sync(0xffffffffu, bar->info[(tile + 1) % kInfo].flags, 0);
             have = true;
           }
           const int op = (next & kFirst) && (s == 1 || s == 2) ? 3 - s : s;
@@ -1087,8 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.seq = w.i;
             u.kv_head = w.h;
             const bool whole = w.k0 == 0 && w.k1 == w.n;
-            u.c0 = whole ? 0 : static_cast<int>(ux / per);
-            u.c1 = whole ? 0 : static_cast<int>((ux + w.n - 1) / per);
+            u.c0 = whole ? 0 : static_cast<int>(kv::quotient(ux, per));
+            u.c1 = whole ? 0 : static_cast<int>(kv::quotient(ux + w.n - 1, per));
             u.slot = 2 * static_cast<int>(blockIdx.x) + (w.k0 == 0 ? 1 : 0);
             mbar_arrive(&bar->unit[un % kUnits]);
           }
@@ -1163,7 +1166,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (!in_time && lane == 0) record_error(kDevErrTimeout);
-  pdl_launch_dependents();
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();

@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int group = a.group, H = a.c.kv_heads, page_size = a.c.page_size;
   pdl_wait();
+  pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
 
   // ---- this CTA's share of all tiles ----------------------------------------
   auto cost = [&](int i) -> long long {
@@ -306,13 +307,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     block_scan(cost(base + tid), all);
     total += all;
   }
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
+  const long long per = max(kv::quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
   long long x0 = per * blockIdx.x;
   const long long x1 = min(x0 + per, total);
-  if (x0 >= x1) {
-    pdl_launch_dependents();
-    return;
-  }
+  if (x0 >= x1) return;
   // the sequence that x0 falls into
   long long before = 0;
 #pragma unroll 1
@@ -345,10 +343,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   };
   enter(static_cast<int>(scan[W]));
   {
-    const long long off = scan[W + 1], unit = off / pc.t.n;
-    pc.h = static_cast<int>(unit / pc.row_tiles);
-    pc.rt = static_cast<int>(unit % pc.row_tiles);
-    pc.k0 = static_cast<int>(off % pc.t.n);
+    const long long off = scan[W + 1], unit = kv::quotient(off, pc.t.n);
+    pc.h = static_cast<int>(kv::quotient(unit, pc.row_tiles));
+    pc.rt = static_cast<int>(unit - static_cast<long long>(pc.h) * pc.row_tiles);
+    pc.k0 = static_cast<int>(off - unit * pc.t.n);
     pc.k1 = static_cast<int>(min(static_cast<long long>(pc.t.n), pc.k0 + (x1 - x0)));
   }
 
@@ -837,8 +835,6 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll 1
       for (int n = 0; n < S - 1; ++n) load(n);
       ask_queries();
-    } else {
-      pdl_launch_dependents();
     }
 
     // ---- join the warps, pairwise, half of them at a time -----------------------------------
@@ -938,7 +934,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     } else {
       // partial sums: the unit's CTAs are c0 .. c1, c0's slot 2 c0 + 1, the others' 2 c
       const long long unit_x0 = x0 - done.k1, unit_x1 = unit_x0 + done.t.n - 1;
-      const int c0 = static_cast<int>(unit_x0 / per), parts = static_cast<int>(unit_x1 / per) - c0 + 1;
+      const int c0 = static_cast<int>(kv::quotient(unit_x0, per)), parts = static_cast<int>(kv::quotient(unit_x1, per)) - c0 + 1;
       auto slot_of = [&](int q) { return q == 0 ? 2 * c0 + 1 : 2 * (c0 + q); };
       auto part_at = [&](int slot) { return P.parts + static_cast<long long>(slot) * G::SLOT; };
       const int me = static_cast<int>(blockIdx.x) - c0;

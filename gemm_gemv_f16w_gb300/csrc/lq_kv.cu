@@ -196,6 +196,7 @@ __device__ __forceinline__ float4 values4(const Four& f, int e) {
 template <int FMT, bool VEC, bool WRITE>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
   pdl_wait();
+  pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int which = a.sides == 2 ? static_cast<int>(blockIdx.y & 1u) : a.only;
   const int segment = static_cast<int>(a.sides == 2 ? blockIdx.y >> 1 : blockIdx.y);
@@ -300,7 +301,6 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
       }
     }
   }
-  pdl_launch_dependents();
 }
 
 template <bool WRITE>
