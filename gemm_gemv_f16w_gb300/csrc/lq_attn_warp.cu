@@ -78,6 +78,7 @@ struct Geo {
   static constexpr int HEAD = 16;  // per stage: first position and visible keys of each tile
   static constexpr int STAGE = TPS * TILE + HEAD;
   static constexpr int R = 8 * NR;
+  static constexpr int WHOLE = 6 * W;  // tiles up to which a unit is better not split
   static constexpr int QF = NR * (D / 16) * 512;           // fragments of the query rows
   static constexpr int MERGE = (W / 2) * R * (D + 2) * 4;  // partial sums of half the warps
   static constexpr int FIXED = QF + MERGE + 2048;
@@ -272,12 +273,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
 
   // ---- this CTA's share of all tiles ----------------------------------------
-  auto cost = [&](int i) -> long long {
-    if (i >= a.b.batch) return 0;
+  struct Cost {
+    long long tiles;  // of a sequence, all heads and row tiles
+    int units, n;     // its units, and their tiles each
+  };
+  auto cost = [&](int i) {
+    Cost c = {0, 0, 0};
+    if (i >= a.b.batch) return c;
     const kv::Seq s = kv::sequence(a.b, page_size, i);
     const int rows = s.rows * group;
-    if (rows == 0 || (P.small_rows && rows > P.small_rows)) return 0;
-    return static_cast<long long>((rows + R - 1) / R) * H * tiles_of(s, a.window, a.sinks).n;
+    if (rows == 0 || (P.small_rows && rows > P.small_rows)) return c;
+    c.units = (rows + R - 1) / R * H;
+    c.n = tiles_of(s, a.window, a.sinks).n;
+    c.tiles = static_cast<long long>(c.units) * c.n;
+    return c;
   };
   // inclusive sums over the block's threads, and the block's total in scan[W]
   auto block_scan = [&](long long mine, long long& all) {
@@ -298,26 +307,43 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     }
     return incl;
   };
-  long long first_cost = cost(tid), first_all, total;
-  const long long first_incl = block_scan(first_cost, first_all);
-  total = first_all;
+  const Cost first = cost(tid);
+  long long total, units;
+  const long long first_incl = block_scan(first.tiles, total), unit_incl = block_scan(first.units, units);
+  const long long first_all = total;
+  const bool one_pass = a.b.batch <= W * 32;  // every sequence has a thread
+  const bool short_units = !__syncthreads_or(first.n > G::WHOLE);
 #pragma unroll 1
-  for (int base = W * 32; base < a.b.batch; base += W * 32) {  // batches beyond the block's threads
+  for (int base = W * 32; base < a.b.batch; base += W * 32) {
     long long all;
-    block_scan(cost(base + tid), all);
+    block_scan(cost(base + tid).tiles, all);
     total += all;
   }
+  // Few short units: a CTA takes one whole unit (joining parts costs more than
+  // the tiles: one f16 sequence of 513 positions, 8 heads, 9.7 us against 12.9
+  // in parts of 16 tiles). Otherwise all tiles in equal ranges.
+  const bool whole_units = one_pass && short_units && units <= gridDim.x;
   const long long per = max(kv::quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
-  long long x0 = per * blockIdx.x;
-  const long long x1 = min(x0 + per, total);
+  long long x0 = per * blockIdx.x, x1 = min(x0 + per, total);
+  if (whole_units) {
+    if (blockIdx.x >= units) return;
+    if (blockIdx.x >= unit_incl - first.units && blockIdx.x < unit_incl) {
+      const long long within = (blockIdx.x - (unit_incl - first.units)) * first.n;
+      scan[W + 2] = first_incl - first.tiles + within;
+      scan[W + 3] = first.n;
+    }
+    __syncthreads();
+    x0 = scan[W + 2];
+    x1 = x0 + scan[W + 3];
+  }
   if (x0 >= x1) return;
   // the sequence that x0 falls into
   long long before = 0;
 #pragma unroll 1
   for (int base = 0;; base += W * 32) {
-    long long mine = first_cost, all = first_all, incl = first_incl;
+    long long mine = first.tiles, all = first_all, incl = first_incl;
     if (base > 0) {
-      mine = cost(base + tid);
+      mine = cost(base + tid).tiles;
       incl = block_scan(mine, all);
     }
     incl += before;
@@ -962,6 +988,51 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       // Joins n parts, the q-th in slot_at(q), in the order of the keys: into the
       // first's slot, or (into == null) the output.
       auto combine = [&](auto&& slot_at, int n, float* into) {
+        if (n <= kJoin) {  // one round of loads
+          for (int e = tid; e < d_rows * (D / 4); e += W * 32) {
+            const int r = e / (D / 4);
+            float m[kJoin], ls[kJoin];
+            float4 v[kJoin];
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q) {
+              const float* at = part_at(slot_at(min(q, n - 1)));
+              m[q] = __ldcg(at + R * D + r);
+              ls[q] = __ldcg(at + R * D + R + r);
+              v[q] = __ldcg(reinterpret_cast<const float4*>(at) + e);
+            }
+            float top = m[0], sum = 0.0f;
+#pragma unroll
+            for (int q = 1; q < kJoin; ++q) top = fmaxf(top, m[q]);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q) {
+              if (q < n) {
+                const float w = ex2(m[q] - top);
+                sum = fmaf(w, ls[q], sum);
+                o.x = fmaf(w, v[q].x, o.x);
+                o.y = fmaf(w, v[q].y, o.y);
+                o.z = fmaf(w, v[q].z, o.z);
+                o.w = fmaf(w, v[q].w, o.w);
+              }
+            }
+            if (into) {
+              reinterpret_cast<float4*>(into)[e] = o;
+              row_m[r] = top;
+              row_l[r] = sum;
+            } else {
+              finish(r, e % (D / 4), o, sum);
+              if (e % (D / 4) == 0) finish_lse(r, top, sum);
+            }
+          }
+          if (into) {
+            __syncthreads();  // every thread has read the parts' maxima
+            if (tid < R) {
+              into[R * D + tid] = tid < d_rows ? row_m[tid] : kNoMax;
+              into[R * D + R + tid] = tid < d_rows ? row_l[tid] : 0.0f;
+            }
+          }
+          return;
+        }
         for (int r = warp; r < R; r += W) {
           float top = kNoMax;
           for (int q = lane; q < n; q += 32) top = fmaxf(top, __ldcg(part_at(slot_at(q)) + R * D + r));
