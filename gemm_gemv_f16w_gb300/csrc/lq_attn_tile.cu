@@ -193,6 +193,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint32_
   } while (ok == 0u && static_cast<uint32_t>(clock()) - t0 < clocks);
   return ok != 0u;
 }
+__device__ __forceinline__ void arrive_many(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 // One lane of a converged warp, the same every time; the compiler knows that
 // it is one, and keeps the MMAs' descriptors in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -778,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     uint32_t unit = 0, pend = 0;  // ring units filled; f16: unit whose copies are not yet reported, plus one
+    uint32_t boxed = 0;           // f16, bit i: the copy engine fills the i-th unit from the last
     bool pend_screen = false;
     using Raw = typename std::conditional<FMT == LQ_FMT_Q8_0, uint4, uint2>::type;
     Raw ahead[2];
@@ -821,19 +825,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* const e = &bar->empty[unit % NU];
           const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
           uint64_t* const fl = &bar->full[unit % NU];
-          if (pend && !__all_sync(0xffffffffu, mbar_test_wait(e, parity))) {  // about to wait: report what landed
+          // every key is every row's: the copy engine's boxes of 16 keys x 64 dims, all
+          // by one warp (which arrives for the others, so that it can see them land)
+          const bool boxes = P.tma && (c.flags & (kAll | kMixed)) == kAll;
+          if (pend && (boxes || !__all_sync(0xffffffffu, mbar_test_wait(e, parity)))) {  // report what landed before waiting
             wait_copies<0>();
             report();
           }
           alive = wait(e, parity);
           if (!alive) break;
-          if (P.tma && (c.flags & (kAll | kMixed)) == kAll) {  // every key is every row's: the copy engine's boxes of 16 keys x 64 dims
-            if (pend) {
-              wait_copies<0>();
-              report();
-            }
+          boxed = boxed << 1 | (boxes ? 1u : 0u);
+          if (boxes) {
             if (warp == 8) {
-              if (lane == 0) mbar_arrive_expect_tx(fl, G::UNIT);
+              if (lane == 0) {
+                mbar_arrive_expect_tx(fl, G::UNIT);
+                arrive_many(fl, kLoaders - 1);
+              }
               __syncwarp();
               if (lane < KT / 16) {
                 const int r16 = static_cast<int>(c.at[lane]);
@@ -841,10 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < G::HALVES; ++h)
                   tc::tma_load_2d(ring + (unit % NU) * G::UNIT + h * G::GROUP + lane * 2048, side ? &mv : &mk, h * 64, r16, fl);
               }
-              if (lane != 0) mbar_arrive(fl);
               __syncwarp();
-            } else {
-              mbar_arrive(fl);
             }
             continue;
           }
@@ -946,6 +950,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     wait_copies<0>();
     if (pend) report();
+    // a warp that gives up lets the copy engine finish first
+    if (!in_time && warp == 8) {
+      for (uint32_t i = 0; i < NU; ++i) {
+        const uint32_t u = unit - 1 - i;  // the units before `unit` were issued
+        if ((boxed >> i) & 1u) mbar_wait(&bar->full[u % NU], (u / NU) & 1u, kDrainWaitNs);
+      }
+    }
   } else {
     // ================= MMA issue =======================================================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::REG_MMA));
