@@ -67,7 +67,7 @@ struct Geo {
   // warps: what registers and stages allow (Q8_0, head dim 128: 12 warps of 168
   // registers run a step of 64 sequences in 162 us, 8 in 172, 16 in 190)
   static constexpr int W = FMT == LQ_FMT_F16 && D == 256 ? 4 : (FMT != LQ_FMT_F16 && D <= 128 && NR == 1 ? 12 : 8);
-  static constexpr int TPS = (FMT == LQ_FMT_Q4_0 && D == 128) || D == 64 ? 2 : 1;  // tiles a step
+  static constexpr int TPS = FMT != LQ_FMT_F16 && D == 64 ? 2 : 1;  // tiles a step
   static constexpr int ROW = FMT == LQ_FMT_F16 ? 2 * D : (FMT == LQ_FMT_Q8_0 ? D : D / 2);
   // pitches: the eight rows (or 4 x 32, 8 x 16 bytes) of a fragment load fall
   // into different banks
