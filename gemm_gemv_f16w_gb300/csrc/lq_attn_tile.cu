@@ -59,7 +59,9 @@ __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnt
 constexpr int kThreads = 512;
 constexpr int kRows = 256;          // query rows of a unit: two tiles of 128
 constexpr int kLoaders = 128;       // loader threads
-constexpr int kMinTiles = 4;        // key tiles worth a CTA
+// Key tiles worth a CTA: one f16 sequence, 512 of 1000 | 500 of 500 tokens, 32 heads over 8
+// of 128: 2: 54.7 | 48.5 us, 4: 48.7 | 54.8, 8: 72.0 | 93.4.
+constexpr int kMinTiles = 4;
 constexpr int kInfo = 8;            // tiles of bookkeeping kept
 constexpr int kUnits = 8;           // units of bookkeeping kept
 constexpr int kMaxBatch = 4096;     // sequences whose totals fit in shared memory
@@ -90,8 +92,14 @@ struct Geo {
   static constexpr int Q = 4 * QPART;                      // [row tile][hi, lo]
   static constexpr int SMEM = Q + NU * UNIT + 1024 + 2048;  // alignment, barriers
   static constexpr int SLOT = kRows * (D + 2);             // floats of a partial result
-  // registers a thread of the warpgroups: together the launch's 4 * 128
-  static constexpr int REG_SOFTMAX = D == 128 ? 200 : 168, REG_LOAD = D == 128 ? 72 : 128, REG_MMA = D == 128 ? 40 : 48;
+  // Quantised tiles: their loaders convert, and at 72 registers they wait on their own
+  // chains. 2048 tokens over 16384 positions, 32 query heads over 8 of 128, Q8_0: 1652 us
+  // with (200, 72), 1529 with (192, 88), 1740 with (176, 120). In f16 the loaders only
+  // issue copies: 3 prompts of 4001 take 594 us with (200, 72), 602 with (192, 88).
+  static constexpr bool QUANT = FMT != LQ_FMT_F16;
+  // registers a thread of the warpgroups: together no more than the launch's 4 * 128
+  static constexpr int REG_SOFTMAX = D == 128 ? (QUANT ? 192 : 200) : 168, REG_LOAD = D == 128 ? (QUANT ? 88 : 72) : 128,
+                       REG_MMA = D == 128 ? 40 : 48;
   static_assert(2 * REG_SOFTMAX + REG_LOAD + REG_MMA <= 512);
 };
 
@@ -895,47 +903,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             fetch(0, bar->info[(tile + 1) % kInfo]);
           }
           const bool mixed = side == 1 && (c.flags & kMixed);
+          // step by step for both passes at once: one chain after the other would
+          // leave this warp waiting for its own results
+          uint32_t hi[2][8], lo[2][8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (mixed && !(fabsf(__half2float(d2[i])) <= 65504.0f)) {
+              const int row = row0 + (2 * nn + i) * PASS;
+              d2[i] = __ushort_as_half(0);
+              atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
+            }
+            if constexpr (FMT == LQ_FMT_Q8_0) {
+#pragma unroll
+              for (int n = 0; n < 4; ++n) codes8(w4[i][n], hi[i][2 * n], hi[i][2 * n + 1]);
+            } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
+#pragma unroll
+              for (int n = 0; n < 2; ++n) codes4(w4[i][n], hi[i][2 * n], hi[i][2 * n + 1], hi[i][4 + 2 * n], hi[i][4 + 2 * n + 1]);
+            }
+          }
+          constexpr float kTop = FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f;
+          if (!(fabsf(__half2float(d2[0])) >= kTop) && !(fabsf(__half2float(d2[1])) >= kTop)) {
+            // code * d in f16, and what it leaves: exact by the fused multiply-add
+            const __half2 da = __half2half2(d2[0]), db = __half2half2(d2[1]);
+            __half2 prod[2][8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              prod[0][n] = __hmul2_rn(as_h2(hi[0][n]), da);
+              prod[1][n] = __hmul2_rn(as_h2(hi[1][n]), db);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              lo[0][n] = h2(__hfma2(as_h2(hi[0][n]), da, __hneg2(prod[0][n])));
+              lo[1][n] = h2(__hfma2(as_h2(hi[1][n]), db, __hneg2(prod[1][n])));
+              hi[0][n] = h2(prod[0][n]);
+              hi[1][n] = h2(prod[1][n]);
+            }
+          } else {  // the top of f16's range: rounded toward zero, through f32
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float df = __half2float(d2[i]);
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                const float2 c2 = __half22float2(as_h2(hi[i][n]));
+                split2_rz(c2.x * df, c2.y * df, hi[i][n], lo[i][n]);
+              }
+            }
+          }
+          // 16-byte chunks of the rows: the second column group's threads start with their second
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int row = row0 + (2 * nn + i) * PASS;
-            __half d = d2[i];
-            if (mixed && !(fabsf(__half2float(d)) <= 65504.0f)) {
-              d = __ushort_as_half(0);
-              atomicOr(&bar->bad[tile % kInfo][row >> 5], 1u << (row & 31));
-            }
-            uint32_t hi[8], lo[8];
-            if constexpr (FMT == LQ_FMT_Q8_0) {
-#pragma unroll
-              for (int n = 0; n < 4; ++n) codes8(w4[i][n], hi[2 * n], hi[2 * n + 1]);
-            } else {  // pairs (0, 1), (2, 3), ... of the low nibbles, then of the high ones
-#pragma unroll
-              for (int n = 0; n < 2; ++n) codes4(w4[i][n], hi[2 * n], hi[2 * n + 1], hi[4 + 2 * n], hi[4 + 2 * n + 1]);
-            }
-            if (!(fabsf(__half2float(d)) >= (FMT == LQ_FMT_Q8_0 ? 515.5f : 8188.0f))) {
-              // code * d in f16, and what it leaves: exact by the fused multiply-add
-              const __half2 dd = __half2half2(d);
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const __half2 c2 = as_h2(hi[n]), prod = __hmul2_rn(c2, dd);
-                hi[n] = h2(prod);
-                lo[n] = h2(__hfma2(c2, dd, __hneg2(prod)));
-              }
-            } else {  // the top of f16's range: rounded toward zero, through f32
-              const float df = __half2float(d);
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const float2 c2 = __half22float2(as_h2(hi[n]));
-                split2_rz(c2.x * df, c2.y * df, hi[n], lo[n]);
-              }
-            }
-            // 16-byte chunks of the row: the second column group's threads start with their second
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               const int part = s ^ ((ch >> 2) & 1);
               const int c16 = FMT == LQ_FMT_Q8_0 ? 2 * ch + part : (ch >> 1) * 4 + (ch & 1) + 2 * part;
               unsigned char* const to = dst + (c16 >> 3) * G::GROUP + tc::sw128_offset(row, c16 & 7);
-              *reinterpret_cast<uint4*>(to) = part ? make_uint4(hi[4], hi[5], hi[6], hi[7]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(to + 64 * 128) = part ? make_uint4(lo[4], lo[5], lo[6], lo[7]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(to) = part ? make_uint4(hi[i][4], hi[i][5], hi[i][6], hi[i][7]) : make_uint4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
+              *reinterpret_cast<uint4*>(to + 64 * 128) = part ? make_uint4(lo[i][4], lo[i][5], lo[i][6], lo[i][7]) : make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
             }
           }
           if (nn == N / 2 - 1) {
