@@ -7,7 +7,10 @@
 // maximum and sum (softmax in one pass over the keys) rescale the output when
 // the maximum grows. The warps' partial results are joined through shared
 // memory. It is bound by its serial chain of loads and shuffles per key and
-// reads a shared head's keys once per query head.
+// reads a shared head's keys once per query head: one f16 sequence of 513
+// positions, 32 heads over 8 of 128, takes 66 us (the warp-level kernel 10),
+// 64 sequences of 8192 take 5.1 ms (0.34; with heads of 96, which only this
+// kernel takes, 4.5).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -24,7 +27,17 @@ std::atomic<int> g_attn_route{0};
 
 constexpr int kGWarps = 8;
 constexpr int kMaxDim = 256;
-constexpr int kAttnFewRows = 32;  // rows of a sequence up to which the warp-level kernel runs
+// Rows (tokens x query heads a key/value head) of a sequence up to which the
+// warp-level kernel runs: it reads the keys once for every 16 rows, and its
+// time grows with the rows; the tile kernel's is that of 256 rows. 32 heads
+// over 8, 16 sequences of 4096 | one of 32768, us, warp-level / tile:
+//   rows           32               48               64               128
+//   f16, 64    42/70 | 33/54    51/71 | 40/60    65/72 | 48/55    106/75 | 81/57
+//   f16, 128   68/109 | 64/85   83/110 | 84/95   110/111 | 105/86  172/116 | 190/88
+//   Q8_0, 64   48/94 | 37/72    59/94 | 45/77    74/89 | 55/73    117/91 | 94/74
+//   Q8_0, 128  65/169 | 58/148  82/174 | 75/159  105/177 | 95/152  180/184 | 173/158
+//   Q4_0, 128  65/155 | 57/135  81/156 | 75/144  105/147 | 95/135  178/156 | 175/138
+int few_rows(int fmt) { return fmt == LQ_FMT_F16 ? 48 : 80; }
 
 template <int FMT>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
@@ -198,9 +211,9 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   if (route == 2) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   if (route == 3) return launch_attn_tile(a, cache->fmt, 0, work, s);
   if (!attn_warp_eligible(a)) return launch_attn_generic(a, cache->fmt, s);
-  if (rows <= kAttnFewRows || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
+  if (rows <= few_rows(cache->fmt) || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   // one sequence: all of it is one kernel's; else each kernel takes its own
-  const int split = a.b.batch > 1 ? kAttnFewRows : 0;
+  const int split = a.b.batch > 1 ? few_rows(cache->fmt) : 0;
   if (split) {
     st = launch_attn_warp(a, cache->fmt, split, split, work, s);
     if (st != LQ_OK) return st;

@@ -46,7 +46,9 @@ __device__ unsigned g_attnw_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnw_err, 0u, code); }
 
 constexpr int kTile = 16;            // keys of a tile: never crosses a page
-constexpr int kMinTiles = 16;        // tiles worth a CTA
+// Tiles worth a CTA: fewer make more partial results to join. One f16 sequence of 1600 | 3000
+// positions, 8 heads of 128: 8: 16.2 | 15.6 us, 16: 12.8 | 16.5, 32: 14.8 | 15.5.
+constexpr int kMinTiles = 16;
 constexpr int kJoin = 8;              // partial results that one CTA joins at once
 constexpr float kNoMax = -1e30f;     // M before the first key
 constexpr float kLift = 11.0f;       // how far M stays below the maximum
@@ -64,10 +66,13 @@ struct WarpParams {
 
 template <int FMT, int D, int NR>
 struct Geo {
-  // warps: what registers and stages allow (Q8_0, head dim 128: 12 warps of 168
-  // registers run a step of 64 sequences in 162 us, 8 in 172, 16 in 190)
+  // warps: what registers and stages allow. A step of 64 sequences of up to 8192, Q8_0, heads
+  // of 128: 12 warps of 168 registers 162 us, 8 warps 172, 16 warps 190 (with one tile a step);
+  // Q4_0, heads of 64: 12 warps 100 us, 8 warps 108.
   static constexpr int W = FMT == LQ_FMT_F16 && D == 256 ? 4 : (FMT != LQ_FMT_F16 && D <= 128 && NR == 1 ? 12 : 8);
-  static constexpr int TPS = FMT != LQ_FMT_F16 && D == 64 ? 2 : 1;  // tiles a step
+  // tiles a step: two where a tile's work does not cover the step's own. The same step in us
+  // with two | one: Q8_0 of 64 104 | 110, Q4_0 of 64 100 | 105, f16 of 64 117 | 112, Q4_0 of 128 157 | 148
+  static constexpr int TPS = FMT != LQ_FMT_F16 && D == 64 ? 2 : 1;
   static constexpr int ROW = FMT == LQ_FMT_F16 ? 2 * D : (FMT == LQ_FMT_Q8_0 ? D : D / 2);
   // pitches: the eight rows (or 4 x 32, 8 x 16 bytes) of a fragment load fall
   // into different banks
@@ -78,7 +83,9 @@ struct Geo {
   static constexpr int HEAD = 16;  // per stage: first position and visible keys of each tile
   static constexpr int STAGE = TPS * TILE + HEAD;
   static constexpr int R = 8 * NR;
-  static constexpr int WHOLE = 6 * W;  // tiles up to which a unit is better not split
+  // tiles up to which few units are better not split (8 heads of f16, 513 positions: 9.8 us,
+  // split 12.5; 1100 positions: 13.4 and 12.9)
+  static constexpr int WHOLE = 6 * W;
   static constexpr int QF = NR * (D / 16) * 512;           // fragments of the query rows
   static constexpr int MERGE = (W / 2) * R * (D + 2) * 4;  // partial sums of half the warps
   static constexpr int FIXED = QF + MERGE + 2048;
