@@ -1,6 +1,10 @@
 """lq_attn_paged against the float64 formula (oracle/attention.py), on caches
 whose bytes the oracle's packer made. Tolerances are the oracle's: derived
 from the rounding of the kernels' steps, per element."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -267,3 +271,13 @@ def test_layer_of_a_decoder(lq, cuda_dev):
     y = np.concatenate([s[2] for s in out])
     ref, tol = O.reference("q8_0", o, O.pack("q8_0", Wo.numpy()), E, heads * d, tensor_core=True)
     compare(y, ref + X.numpy()[:23], tol + 1e-6)
+
+
+@pytest.mark.parametrize("args", [["--batch", "3", "--prompt", "90", "--steps", "4", "--embed", "512", "--heads", "8", "--kv-heads", "2"],
+                                  ["--fmt", "q4_0", "--cache", "f16", "--batch", "1", "--prompt", "40", "--steps", "3", "--embed",
+                                   "256", "--heads", "4", "--kv-heads", "4", "--head-dim", "64", "--window", "16", "--sinks", "2"]])
+def test_example_of_an_attention_block(args):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "attention_block.py"), *args], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
