@@ -346,11 +346,7 @@ lq_status lq_matmul_swiglu(int fmt, const float* A, const void* W, float* H,
  *     their elements (pools: 2 bytes), else LQ_ERR_INVALID_ARG; head_dim
  *     > 256, LQ_FMT_Q4_0I or max_pages * page_size > 2^30 ->
  *     LQ_ERR_UNSUPPORTED. batch == 0 or tokens == 0:
- *     LQ_OK, nothing is launched.
- * (The pages keep an f32 or f16 cache beside their attention kernels:
- * kv_cache_append_f32 and flash_attn_decode_paged_f32, ferrum-kernels
- * src/attention/metal/pipelines.rs; decode_attention and prefill_attention_
- * batched, lattice-inference src/forward/metal_qwen35.rs.) */
+ *     LQ_OK, nothing is launched. */
 typedef struct {
   int32_t fmt;       /* LQ_FMT_F16, LQ_FMT_Q8_0 or LQ_FMT_Q4_0 */
   int32_t page_size; /* tokens a page */
