@@ -37,7 +37,14 @@ constexpr int kMaxDim = 256;
 //   Q8_0, 64   48/94 | 37/72    59/94 | 45/77    74/89 | 55/73    117/91 | 94/74
 //   Q8_0, 128  65/169 | 58/148  82/174 | 75/159  105/177 | 95/152  180/184 | 173/158
 //   Q4_0, 128  65/155 | 57/135  81/156 | 75/144  105/147 | 95/135  178/156 | 175/138
-int few_rows(int fmt) { return fmt == LQ_FMT_F16 ? 48 : 80; }
+// 16 sequences of 4096, 2 | 4 heads of 256:
+//   rows           64                80                96                128
+//   f16, 256   62/81 | 123/118   72/91 | 151/127   87/91 | 179/129   118/86 | 233/126
+//   Q8_0, 256  58/110 | 115/199  68/109 | 144/206  82/112 | 171/208  110/114 | 219/216
+int few_rows(int fmt, int head_dim) {
+  if (head_dim == 256) return fmt == LQ_FMT_F16 ? 64 : 128;
+  return fmt == LQ_FMT_F16 ? 48 : 80;
+}
 
 template <int FMT>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
@@ -211,9 +218,10 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   if (route == 2) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   if (route == 3) return launch_attn_tile(a, cache->fmt, 0, work, s);
   if (!attn_warp_eligible(a)) return launch_attn_generic(a, cache->fmt, s);
-  if (rows <= few_rows(cache->fmt) || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
+  const int few = few_rows(cache->fmt, cache->head_dim);
+  if (rows <= few || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   // one sequence: all of it is one kernel's; else each kernel takes its own
-  const int split = a.b.batch > 1 ? few_rows(cache->fmt) : 0;
+  const int split = a.b.batch > 1 ? few : 0;
   if (split) {
     st = launch_attn_warp(a, cache->fmt, split, split, work, s);
     if (st != LQ_OK) return st;

@@ -13,7 +13,7 @@
 // 2 * 65504 in range) and lo hold them exactly.
 //
 // A unit is (sequence, key/value head, 256 query rows (token, head of the
-// group)): two row tiles of 128 share every key tile. Key tiles are 128 "rows
+// group)): two row tiles of 128 share every key tile (heads of 256: below). Key tiles are 128 "rows
 // of shared memory": 128 keys (f16), or 64 keys, hi parts and then lo parts
 // (quantised), so that both run the same MMAs: S[128 x 128] = Q K^T with K as
 // it lies (K-major), and O[128 x D] = P V with P from tensor memory and V as
@@ -23,6 +23,13 @@
 // O starts from zero in every tile and is added to the f32 sums that the
 // softmax threads keep in registers (thread = row, D sums): the tensor core's
 // own accumulation truncates, which over thousands of keys would show.
+//
+// Heads of 256: O of one row tile fills half of the tensor memory, its queries 128
+// KB of shared memory, so a unit is 128 rows and a key tile 64 rows. Both
+// softmax groups work on that row tile: each takes the maximum over all keys (the
+// same bits in both), weighs its half of the keys (P has columns of its own) and
+// sums its half of O's dims. 3 prompts of up to 2001 tokens, 16 heads over 2, take
+// 512 us in f16 and 679 in Q8_0 (2892 and 1845 on warp-level MMAs).
 //
 // Roles (four warpgroups, registers moved between them): two softmax groups,
 // one per row tile; four loader warps (16-byte asynchronous copies for f16;
@@ -68,7 +75,6 @@ __device__ unsigned g_attnt_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnt_err, 0u, code); }
 
 constexpr int kThreads = 512;
-constexpr int kRows = 256;          // query rows of a unit: two tiles of 128
 constexpr int kLoaders = 128;       // loader threads
 // Key tiles worth a CTA: one f16 sequence, 512 of 1000 | 500 of 500 tokens, 32 heads over 8
 // of 128: 2: 54.7 | 48.5 us, 4: 48.7 | 54.8, 8: 72.0 | 93.4.
@@ -93,24 +99,29 @@ struct TileParams {
 
 template <int FMT, int D>
 struct Geo {
-  static constexpr int KT = FMT == LQ_FMT_F16 ? 128 : 64;  // keys of a tile
+  static constexpr bool ONE = D == 256;                    // one row tile a unit, shared by both softmax groups
+  static constexpr int ROWS = ONE ? 128 : 256;             // query rows of a unit
+  static constexpr int KROWS = ONE ? 64 : 128;             // rows of a key tile in shared memory
+  static constexpr int KT = FMT == LQ_FMT_F16 ? KROWS : KROWS / 2;  // keys of a tile
+  static constexpr int DO = ONE ? 128 : D;                 // output dims of a softmax thread
   static constexpr int ROW = FMT == LQ_FMT_F16 ? 2 * D : (FMT == LQ_FMT_Q8_0 ? D : D / 2);
   static constexpr int HALVES = D / 64;                    // 64-dim column groups
-  static constexpr int GROUP = 128 * 128;                  // bytes of a group: 128 rows of 128 bytes
-  static constexpr int UNIT = HALVES * GROUP;              // K or V of a tile
-  static constexpr int NU = D == 128 ? 3 : 6;              // ring of units
+  static constexpr int GROUP = 128 * 128;                  // bytes of a group of queries: 128 rows of 128 bytes
+  static constexpr int KGROUP = KROWS * 128;               // of keys or values
+  static constexpr int UNIT = HALVES * KGROUP;             // K or V of a tile
+  static constexpr int NU = D == 64 ? 6 : 3;               // ring of units
   static constexpr int QPART = HALVES * GROUP;             // hi or lo of a row tile
-  static constexpr int Q = 4 * QPART;                      // [row tile][hi, lo]
+  static constexpr int Q = ROWS / 64 * QPART;              // [row tile][hi, lo]
   static constexpr int SMEM = Q + NU * UNIT + 1024 + 2048;  // alignment, barriers
-  static constexpr int SLOT = kRows * (D + 2);             // floats of a partial result
+  static constexpr int SLOT = ROWS * (D + 2);              // floats of a partial result
   // Quantised tiles: their loaders convert, and at 72 registers they wait on their own
   // chains. 2048 tokens over 16384 positions, 32 query heads over 8 of 128, Q8_0: 1652 us
   // with (200, 72), 1529 with (192, 88), 1740 with (176, 120). In f16 the loaders only
   // issue copies: 3 prompts of 4001 take 594 us with (200, 72), 602 with (192, 88).
   static constexpr bool QUANT = FMT != LQ_FMT_F16;
   // registers a thread of the warpgroups: together no more than the launch's 4 * 128
-  static constexpr int REG_SOFTMAX = D == 128 ? (QUANT ? 192 : 200) : 168, REG_LOAD = D == 128 ? (QUANT ? 88 : 72) : 128,
-                       REG_MMA = D == 128 ? 40 : 48;
+  static constexpr int REG_SOFTMAX = D != 64 ? (QUANT ? 192 : 200) : 168, REG_LOAD = D != 64 ? (QUANT ? 88 : 72) : 128,
+                       REG_MMA = D != 64 ? 40 : 48;
   static_assert(2 * REG_SOFTMAX + REG_LOAD + REG_MMA <= 512);
 };
 
@@ -162,10 +173,13 @@ constexpr uint32_t kAll = 1u << 11;    // every key is there and seen by some ro
 // Shared-memory matrix descriptors, 128-byte swizzle, as words: the low one has
 // the address (>> 4) and the leading byte offset, the high one the stride
 // (1024: groups of 8 rows) and the mode. Queries and keys are K-major (leading
-// offset unused); values are MN-major: 64-dim groups 128 rows apart, 8-key groups.
+// offset unused); values are MN-major: 64-dim groups a key tile's rows apart, 8-key groups.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_k(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t desc_mn(uint32_t at) { return ((at & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16); }
+template <int GROUP_BYTES>
+__device__ __forceinline__ uint32_t desc_mn(uint32_t at) {
+  return ((at & 0x3FFFFu) >> 4) | ((static_cast<uint32_t>(GROUP_BYTES) >> 4) << 16);
+}
 // D[tmem] = A B or (ADD) D + A B, f16, A from shared memory or from tensor memory.
 template <bool ADD>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -189,6 +203,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_st1(uint32_t at, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(r) : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t at) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(at));
+  return r;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -277,11 +299,11 @@ struct Work {
   int begin, sink_end;       // keys that its rows see: [begin, p1] and [0, sink_end)
 };
 
-template <int KT>
+template <int KT, int ROWS>
 __device__ __forceinline__ void unit_tiles(Work& w, const AttnArgs& a) {
-  const int rows = w.s.rows * a.group, rho0 = w.rt * kRows;
+  const int rows = w.s.rows * a.group, rho0 = w.rt * ROWS;
   w.p0 = w.s.len - w.s.rows + rho0 / a.group;
-  w.p1 = w.s.len - w.s.rows + min(rho0 + kRows - 1, rows - 1) / a.group;
+  w.p1 = w.s.len - w.s.rows + min(rho0 + ROWS - 1, rows - 1) / a.group;
   const kv::Visible v = kv::visible(max(w.p0, 0), a.window, a.sinks);
   w.begin = v.begin;
   w.sink_end = v.sink_end;
@@ -295,13 +317,14 @@ __device__ __forceinline__ bool takes(const kv::Seq& s, const TileParams& P) {
 }
 
 // The first sequence from i on that has work here.
+template <int ROWS>
 __device__ __forceinline__ void enter(Work& w, const TileParams& P, int i) {
   for (;; ++i) {
     w.s = kv::sequence(P.a.b, P.a.c.page_size, i);
     if (takes(w.s, P)) break;
   }
   w.i = i;
-  w.row_tiles = (w.s.rows * P.a.group + kRows - 1) / kRows;
+  w.row_tiles = (w.s.rows * P.a.group + ROWS - 1) / ROWS;
 }
 
 __device__ __forceinline__ long long scan32(long long mine, int lane) {
@@ -315,7 +338,7 @@ __device__ __forceinline__ long long scan32(long long mine, int lane) {
 
 // This CTA's range of all units' tiles, in the order (sequence, key/value
 // head, row tile, key tile): its first unit and its length, into `bar`.
-template <int KT>
+template <int KT, int ROWS>
 __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* totals, int warp, int lane) {
   const AttnArgs& a = P.a;
 #pragma unroll 1
@@ -324,10 +347,10 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
     w.s = kv::sequence(a.b, a.c.page_size, i);
     long long sum = 0;
     if (takes(w.s, P)) {
-      const int rts = (w.s.rows * a.group + kRows - 1) / kRows;
+      const int rts = (w.s.rows * a.group + ROWS - 1) / ROWS;
 #pragma unroll 1
       for (w.rt = lane; w.rt < rts; w.rt += 32) {
-        unit_tiles<KT>(w, a);
+        unit_tiles<KT, ROWS>(w, a);
         sum += w.n;
       }
     }
@@ -367,8 +390,8 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
 #pragma unroll 1
     for (int base = 0;; base += 32) {  // the row tile
       w.rt = base + lane;
-      unit_tiles<KT>(w, a);
-      const long long here = w.rt * kRows < w.s.rows * a.group ? w.n : 0, incl = scan32(here, lane);
+      unit_tiles<KT, ROWS>(w, a);
+      const long long here = w.rt * ROWS < w.s.rows * a.group ? w.n : 0, incl = scan32(here, lane);
       const unsigned past = __ballot_sync(0xffffffffu, x < incl);
       if (past) {
         const int at = __ffs(static_cast<int>(past)) - 1;
@@ -393,7 +416,8 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ TileParams P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using G = Geo<FMT, D>;
-  constexpr int KT = G::KT, NU = G::NU;
+  constexpr int KT = G::KT, NU = G::NU, ROWS = G::ROWS, DO = G::DO;
+  constexpr bool ONE = G::ONE;
   constexpr bool QUANT = FMT != LQ_FMT_F16;
   extern __shared__ unsigned char raw_smem[];
   unsigned char* const smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -410,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->empty[u], 1);
     }
     for (int q = 0; q < 2; ++q) {
-      mbar_init(&bar->q_ready[q], 128);
+      mbar_init(&bar->q_ready[q], ONE ? 256 : 128);
       mbar_init(&bar->s_full[q], 2);  // the MMAs, and the issuing thread (what the loaders wrote)
-      mbar_init(&bar->p_ready[q], 128);
+      mbar_init(&bar->p_ready[q], ONE ? 256 : 128);
       mbar_init(&bar->o_full[q], 2);
     }
     for (int u = 0; u < kUnits; ++u) {
@@ -430,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
-  plan<KT>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
+  plan<KT, ROWS>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
   if (warp == 12) {
     tc::tmem_alloc(&bar->tmem, 512);
     tc::tmem_relinquish();
@@ -449,12 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (wg < 2) {
     // ================= softmax: thread = query row =================================
+    // One row tile: both groups look at every key for the maximum, each weighs its
+    // half of the keys and sums its half of the output's dims.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::REG_SOFTMAX));
-    const int q = wg, r = tid & 127;
+    const int q = wg, r = tid & 127, half = q;
+    const int rq = ONE ? 0 : q, row_at = rq * 128 + r, dim0 = ONE ? half * DO : 0;  // row tile, row of the unit, first dim
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + q * 128, o_at = tmem + lanes + 256 + q * D;
-    unsigned char* const q_hi = smem + q * 2 * G::QPART;
+    const uint32_t s_at = tmem + lanes + rq * 128, p_at = ONE ? s_at + 128 : s_at, o_at = tmem + lanes + 256 + q * DO;
+    unsigned char* const q_hi = smem + rq * 2 * G::QPART;
     unsigned char* const q_lo = q_hi + G::QPART;
+    unsigned char* const stage = smem + q * 2 * (DO / 64) * G::GROUP;  // where the group's rows go out from
     uint32_t tile = 0, tiles_q = 0, joins = 0;  // tiles done by the CTA, by this row tile
 #pragma unroll 1
     for (uint32_t un = 0;; ++un) {
@@ -462,40 +490,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const UnitInfo& w = bar->units[un % kUnits];
       const int tiles = w.tiles;
       if (tiles == 0) break;
-      const int rho = w.rho0 + q * 128 + r;
-      const bool active = w.rho0 + q * 128 < w.rows;  // the row tile has rows
+      const int rho = w.rho0 + row_at;
+      const bool active = w.rho0 + rq * 128 < w.rows;  // the row tile has rows
       const bool row = rho < w.rows;
       const int token = min(rho, w.rows - 1) / a.group;
       const int t = w.row0 + token, head = w.head0 + (min(rho, w.rows - 1) - token * a.group), pos = w.pos0 + token;
-      float om[D], M = kNoMax, l = 0.0f, f = 0.0f;
+      float om[DO], M = kNoMax, l = 0.0f, f = 0.0f;
       if (active) {
-        // the warp's 32 query rows, one or two at a time: scaled to the top of
-        // f16's range, in two parts
-        constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes a row, rows at a time
+        // the warp's 32 query rows, one or two at a time: scaled to the top of f16's
+        // range, in two parts (one row tile: the first group lays the high parts, the
+        // second the low ones, where its rows will go out later)
+        constexpr int NB = D > 128 ? 2 : 1;                  // 16-byte loads a lane and row
+        constexpr int LPR = D / 4 / NB, RPI = 32 / LPR;      // lanes a row, rows at a time
+        constexpr int STEP = 16 / NB, BOTH = STEP / RPI;
         const int l4 = lane % LPR;
         const long long off = t * a.ldq + static_cast<long long>(head) * D;
         const uint32_t live = __ballot_sync(0xffffffffu, row);
         const uint32_t col = (l4 >> 4) * G::GROUP + (l4 & 1) * 8;  // column group, half of a 16-byte chunk
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += 16) {
-          float4 v[16 / RPI];
+        for (int r0 = 0; r0 < 32; r0 += STEP) {
+          float4 v[BOTH][NB];
 #pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
+          for (int i = 0; i < BOTH; ++i) {
             const int rr = r0 + i * RPI + lane / LPR;
             const float* src = a.Q + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
-            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if ((live >> rr) & 1u) {
-              if (P.vec_q) {
-                v[i] = ldg128f(src);
-              } else {
-                v[i] = make_float4(src[0], src[1], src[2], src[3]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              v[i][b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if ((live >> rr) & 1u) {
+                if (P.vec_q) {
+                  v[i][b] = ldg128f(src + b * 128);
+                } else {
+                  v[i][b] = make_float4(src[b * 128], src[b * 128 + 1], src[b * 128 + 2], src[b * 128 + 3]);
+                }
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
+          for (int i = 0; i < BOTH; ++i) {
             const int rr = r0 + i * RPI + lane / LPR;
-            float top = fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+            float top = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i][b].x), fabsf(v[i][b].y)), fmaxf(fabsf(v[i][b].z), fabsf(v[i][b].w))));
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const int ex = static_cast<int>(__float_as_uint(top) >> 23);
@@ -506,25 +543,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float fr = __shfl_sync(0xffffffffu, back, (lane % RPI) * LPR);
             if (lane / RPI == (r0 + i * RPI) / RPI) f = fr;
             const float sg = a.scale < 0.0f ? -sigma : sigma;
-            uint2 hi, lo;
-            split2(v[i].x * sg, v[i].y * sg, hi.x, lo.x);
-            split2(v[i].z * sg, v[i].w * sg, hi.y, lo.y);
-            const uint32_t at = col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
-            *reinterpret_cast<uint2*>(q_hi + at) = hi;
-            *reinterpret_cast<uint2*>(q_lo + at) = lo;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              uint2 hi, lo;
+              split2(v[i][b].x * sg, v[i][b].y * sg, hi.x, lo.x);
+              split2(v[i][b].z * sg, v[i][b].w * sg, hi.y, lo.y);
+              const uint32_t at = b * 2 * G::GROUP + col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
+              if (!ONE || half == 0) *reinterpret_cast<uint2*>(q_hi + at) = hi;
+              if (!ONE || half == 1) *reinterpret_cast<uint2*>(q_lo + at) = lo;
+            }
           }
         }
         f *= fabsf(a.scale) * kLog2e;
         fence_proxy_async_smem();
-        mbar_arrive(&bar->q_ready[q]);
+        mbar_arrive(&bar->q_ready[rq]);
 #pragma unroll
-        for (int d = 0; d < D; ++d) om[d] = 0.0f;
+        for (int d = 0; d < DO; ++d) om[d] = 0.0f;
       }
       bool ok = true;
       if (!active) tile += tiles;
 #pragma unroll 1
       for (int k = 0; k < (active ? tiles : 0); ++k, ++tile, ++tiles_q) {
-        ok = wait(&bar->s_full[q], tiles_q & 1u);
+        ok = wait(&bar->s_full[rq], tiles_q & 1u);
         if (!ok) break;
         tc::fence_after_sync();
         const int j0 = bar->info[tile % kInfo].j0;
@@ -544,17 +584,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t pg = pages >> (j >> 4);
           return m & ((pg & 1u ? 0xFFFFu : 0u) | (pg & 2u ? 0xFFFF0000u : 0u));
         };
-        // Over the raw sums of all keys of the tile, 16 at a time. (Asking for the
+        // Over the raw sums of the tile's keys from `from` on, 16 at a time. (Asking for the
         // next 16 ahead of time costs more in register moves than it hides.)
-        auto each = [&](auto&& what, bool masked) {
+        auto each = [&](auto&& what, bool masked, int from, int to) {
 #pragma unroll 1
-          for (int j = 0; j < KT; j += 16) {
+          for (int j = from; j < to; j += 16) {
             uint32_t s[16];
             tmem_ld16(s_at + j, s);
             const uint32_t vis = masked ? vis32(j) : 0u;
             if constexpr (QUANT) {
               uint32_t low[16];
-              tmem_ld16(s_at + 64 + j, low);
+              tmem_ld16(s_at + KT + j, low);
               tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
@@ -575,12 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           each([&](int, uint32_t (&s)[16], uint32_t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(s[i]));
-          }, false);
+          }, false, 0, KT);
         } else {
           each([&](int, uint32_t (&s)[16], uint32_t vis) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, (vis >> i) & 1u ? __uint_as_float(s[i]) : -INFINITY);
-          }, true);
+          }, true, 0, KT);
         }
         top = top == -INFINITY ? top : top * f;
         float keep = 1.0f;
@@ -609,18 +649,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             w16[i / 2] = h2(h);
             w16[8 + i / 2] = h2(__floats2half2_rn(r2.x, r2.y));
           }
-          tmem_st16(s_at + j, w16);
+          tmem_st16(p_at + j, w16);
         };
+        const int from = ONE ? half * (KT / 2) : 0, to = ONE ? from + KT / 2 : KT;
         if (!edge) {
-          each([&](int j, uint32_t (&s)[16], uint32_t) { weights(j, s, 0u, false); }, false);
+          each([&](int j, uint32_t (&s)[16], uint32_t) { weights(j, s, 0u, false); }, false, from, to);
         } else {
-          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true); }, true);
+          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true); }, true, from, to);
         }
         l += l2.x + l2.y;
         tc::wait_st();
         tc::fence_before_sync();
-        mbar_arrive(&bar->p_ready[q]);
-        ok = wait(&bar->o_full[q], tiles_q & 1u);
+        mbar_arrive(&bar->p_ready[rq]);
+        ok = wait(&bar->o_full[rq], tiles_q & 1u);
         if (!ok) break;
         tc::fence_after_sync();
         const uint4 bad = *reinterpret_cast<const uint4*>(bar->bad[tile % kInfo]);
@@ -638,19 +679,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           tmem_ld16(o_at, sa);
 #pragma unroll
-          for (int d = 0; d < D; d += 32) {
+          for (int d = 0; d < DO; d += 32) {
             tc::wait_ld();
             tmem_ld16(o_at + d + 16, sb);
             add(d, sa);
             tc::wait_ld();
-            if (d + 32 < D) tmem_ld16(o_at + d + 32, sa);
+            if (d + 32 < DO) tmem_ld16(o_at + d + 32, sa);
             add(d + 16, sb);
           }
           if (pass == 1 || (bad.x | bad.y | bad.z | bad.w) == 0u) break;
           // values that are not finite were kept out of the MMA: once more, with
           // their sums over the keys that each row sees in O's place
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
+          for (int d = 0; d < DO; d += 16) {
             float o[16] = {};
 #pragma unroll 1
             for (int j = 0; j < KT; ++j) {
@@ -660,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (page < 0) continue;
               const int slot = (j0 + j) % a.c.page_size;
               const unsigned char* at = a.c.v + page * a.c.page_bytes + w.kv_head * a.c.head_bytes;
-              const __half* h16 = QUANT ? reinterpret_cast<const __half*>(at + static_cast<long long>(a.c.page_size) * G::ROW) + slot * (D / 32) + d / 32
-                                        : reinterpret_cast<const __half*>(at) + static_cast<long long>(slot) * D + d;
+              const __half* h16 = QUANT ? reinterpret_cast<const __half*>(at + static_cast<long long>(a.c.page_size) * G::ROW) + slot * (D / 32) + (dim0 + d) / 32
+                                        : reinterpret_cast<const __half*>(at) + static_cast<long long>(slot) * D + dim0 + d;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float v = __half2float(h16[QUANT ? 0 : i]);
@@ -682,14 +723,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the unit's result, or its part -----------------------------------------
       bool writes = active;
+      if constexpr (ONE) {  // the groups' sums of weights, by tensor memory that held P
+        tmem_st1(p_at + half, __float_as_uint(l));
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&bar->join);
+        if (!wait(&bar->join, joins++ & 1u)) break;
+        tc::fence_after_sync();
+        const uint32_t other = tmem_ld1(p_at + (half ^ 1));
+        tc::wait_ld();
+        l = half == 0 ? l + __uint_as_float(other) : __uint_as_float(other) + l;
+        tc::fence_before_sync();
+      }
       if (w.c0 != w.c1) {
-        auto slot_of = [&](int c) { return P.parts + static_cast<long long>(c == w.c0 ? 2 * c + 1 : 2 * c) * G::SLOT + (q * 128 + r) * 4; };
+        auto slot_of = [&](int slot) { return P.parts + static_cast<long long>(slot) * G::SLOT; };  // [dim / 4][row][4], then M and l
+        constexpr int kSums = D * ROWS;
         if (row) {
-          float* to = P.parts + static_cast<long long>(w.slot) * G::SLOT + (q * 128 + r) * 4;
+          float* to = slot_of(w.slot);
 #pragma unroll
-          for (int d = 0; d < D; d += 4)
-            *reinterpret_cast<float4*>(to + d * kRows) = make_float4(om[d], om[d + 1], om[d + 2], om[d + 3]);
-          *reinterpret_cast<float2*>(to + D * kRows - (q * 128 + r) * 2) = make_float2(M, l);
+          for (int d = 0; d < DO; d += 4)
+            *reinterpret_cast<float4*>(to + (dim0 + d) * ROWS + row_at * 4) = make_float4(om[d], om[d + 1], om[d + 2], om[d + 3]);
+          if (!ONE || half == 0) *reinterpret_cast<float2*>(to + kSums + row_at * 2) = make_float2(M, l);
         }
         __threadfence();
         mbar_arrive(&bar->join);
@@ -707,17 +761,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           M = kNoMax;
           l = 0.0f;
 #pragma unroll
-          for (int d = 0; d < D; ++d) om[d] = 0.0f;
+          for (int d = 0; d < DO; ++d) om[d] = 0.0f;
 #pragma unroll 1
           for (int c = w.c0; c <= w.c1; ++c) {
-            const float* from = slot_of(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D * kRows - (q * 128 + r) * 2));
+            const float* from = slot_of(c == w.c0 ? 2 * c + 1 : 2 * c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + kSums + row_at * 2));
             const float to = fmaxf(M, ml.x), f1 = ex2(M - to), f2 = ex2(ml.x - to);
             M = to;
             l = l * f1 + ml.y * f2;
 #pragma unroll
-            for (int d = 0; d < D; d += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + d * kRows));
+            for (int d = 0; d < DO; d += 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + (dim0 + d) * ROWS + row_at * 4));
               om[d] = om[d] * f1 + v.x * f2;
               om[d + 1] = om[d + 1] * f1 + v.y * f2;
               om[d + 2] = om[d + 2] * f1 + v.z * f2;
@@ -732,19 +786,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: the row sees nothing; NaN stays
         __syncwarp();
 #pragma unroll
-        for (int d = 0; d < D; d += 4)
-          *reinterpret_cast<float4*>(q_hi + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
+        for (int d = 0; d < DO; d += 4)
+          *reinterpret_cast<float4*>(stage + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
               make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
         __syncwarp();
-        constexpr int LPR = D / 4, RPI = 32 / LPR;
+        constexpr int LPR = DO / 4, RPI = 32 / LPR;
         const int l4 = lane % LPR;
         const uint32_t live = __ballot_sync(0xffffffffu, row && LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads));
-        const long long off = t * a.ldo + static_cast<long long>(head) * D;
+        const long long off = t * a.ldo + static_cast<long long>(head) * D + dim0;
 #pragma unroll 4
         for (int r0 = 0; r0 < 32; r0 += RPI) {
           const int rr = r0 + lane / LPR;
           float* out = a.O + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
-          const float4 v = *reinterpret_cast<const float4*>(q_hi + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
+          const float4 v = *reinterpret_cast<const float4*>(stage + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
           if ((live >> rr) & 1u) {
             if (P.vec_o) {
               *reinterpret_cast<float4*>(out) = v;
@@ -756,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (row && a.lse) a.lse[static_cast<long long>(t) * a.heads + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+        if (row && a.lse && (!ONE || half == 0)) a.lse[static_cast<long long>(t) * a.heads + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
         __syncwarp();
       }
       mbar_arrive(&bar->unit_free[un % kUnits]);
@@ -777,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int n = 0; n < N; ++n) {
         const int row = row0 + n * PASS;
-        unsigned char* at = ring + at_unit + (ch >> 3) * G::GROUP + tc::sw128_offset(row, ch & 7);
+        unsigned char* at = ring + at_unit + (ch >> 3) * G::KGROUP + tc::sw128_offset(row, ch & 7);
         uint4 v = *reinterpret_cast<uint4*>(at);
         uint32_t w4[4] = {v.x, v.y, v.z, v.w};
         bool bad = false;
@@ -865,20 +919,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r16 = static_cast<int>(c.at[lane]);
 #pragma unroll
                 for (int h = 0; h < G::HALVES; ++h)
-                  tc::tma_load_2d(ring + (unit % NU) * G::UNIT + h * G::GROUP + lane * 2048, side ? &mv : &mk, h * 64, r16, fl);
+                  tc::tma_load_2d(ring + (unit % NU) * G::UNIT + h * G::KGROUP + lane * 2048, side ? &mv : &mk, h * 64, r16, fl);
               }
               __syncwarp();
             }
             continue;
           }
-          const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::GROUP + tc::sw128_offset(row0, ch & 7);
+          // (passes of eight rows and more stay at the same place of a swizzle atom)
+          const uint32_t dst = smem_u32(ring) + (unit % NU) * G::UNIT + (ch >> 3) * G::KGROUP + (PASS % 8 == 0 ? tc::sw128_offset(row0, ch & 7) : 0);
           const unsigned char* const src = (side ? a.c.v : a.c.k) + row0 * G::ROW + ch * 16;
 #pragma unroll 4
-          for (int n = 0; n < N; ++n) {  // rows row0 + n PASS: the same place in a swizzle atom, one group of 16 a pass
+          for (int n = 0; n < N; ++n) {  // rows row0 + n PASS: one group of 16 a pass
             const long long at = c.at[n * PASS / 16];
             const int key = c.j0 + row0 + n * PASS;
             const bool there = at >= 0 && key <= c.p1 && (key >= c.begin || key < c.sink_end);
-            copy16(dst + n * PASS * 128, src + max(at, 0ll) * G::ROW + (n * PASS % 16) * G::ROW, there);
+            copy16(PASS % 8 == 0 ? dst + n * PASS * 128 : dst + (n * PASS / 8) * 1024 + tc::sw128_offset(row0 + n * PASS % 8, ch & 7), src + max(at, 0ll) * G::ROW + (n * PASS % 16) * G::ROW, there);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (pend) {
@@ -968,9 +1023,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < 2; ++s) {
               const int part = s ^ ((ch >> 2) & 1);
               const int c16 = FMT == LQ_FMT_Q8_0 ? 2 * ch + part : (ch >> 1) * 4 + (ch & 1) + 2 * part;
-              unsigned char* const to = dst + (c16 >> 3) * G::GROUP + tc::sw128_offset(row, c16 & 7);
+              unsigned char* const to = dst + (c16 >> 3) * G::KGROUP + tc::sw128_offset(row, c16 & 7);
               *reinterpret_cast<uint4*>(to) = part ? make_uint4(hi[i][4], hi[i][5], hi[i][6], hi[i][7]) : make_uint4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
-              *reinterpret_cast<uint4*>(to + 64 * 128) = part ? make_uint4(lo[i][4], lo[i][5], lo[i][6], lo[i][7]) : make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
+              *reinterpret_cast<uint4*>(to + KT * 128) = part ? make_uint4(lo[i][4], lo[i][5], lo[i][6], lo[i][7]) : make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
             }
           }
           if (nn == N / 2 - 1) {
@@ -996,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= MMA issue =======================================================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::REG_MMA));
     if (warp == 12) {
-      constexpr uint32_t kQK = tc::idesc_f16_f32(128, 128);
+      constexpr uint32_t kQK = tc::idesc_f16_f32(128, G::KROWS);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
-      const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring)), v_desc = desc_mn(smem_u32(ring));
+      const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring)), v_desc = desc_mn<G::KGROUP>(smem_u32(ring));
       const int mine = __shfl_sync(0xffffffffu, static_cast<int>(min(max(bar->mine, 0ll), 1ll << 30)), 0);
       uint32_t turn = 0;  // parities: bits 0, 1 tiles of a row tile, bits 2, 3 its units, bit 4 the ring
       uint32_t slot = 0;  // ring unit of the next K or V
@@ -1010,13 +1065,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           turn ^= 16u;
         }
       };
+      // S = Q K^T for row tile q, its low parts first; O = P V: p_lo v_hi, (quantised)
+      // p_hi v_lo, p_hi v_hi, the small ones first
+      auto issue_qk = [&](int q, uint32_t kslot) {
+        const uint32_t b = k_desc + kslot * (G::UNIT >> 4), d = tmem + q * 128;
+        const uint32_t hi = q_desc + q * (2 * G::QPART >> 4), lo = hi + (G::QPART >> 4);
+        auto at = [](int c, int group) -> uint32_t { return ((c >> 2) * group + (c & 3) * 32) >> 4; };
+        mma_ss<false>(d, lo, b, kQK);
+#pragma unroll
+        for (int c = 1; c < D / 16; ++c) mma_ss<true>(d, lo + at(c, G::GROUP), b + at(c, G::KGROUP), kQK);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) mma_ss<true>(d, hi + at(c, G::GROUP), b + at(c, G::KGROUP), kQK);
+        tc::commit(&bar->s_full[q]);
+        mbar_arrive(&bar->s_full[q]);
+      };
+      auto issue_pv = [&](int q, uint32_t vslot) {
+        const uint32_t b = v_desc + vslot * (G::UNIT >> 4);
+        const uint32_t p = tmem + q * 128 + (ONE ? 128 : 0), o = tmem + 256 + q * D;
+        constexpr int KS = KT / 16;
+        mma_ts<false>(o, p + 8, b, kPV);
+#pragma unroll
+        for (int c = 1; c < KS; ++c) mma_ts<true>(o, p + 16 * c + 8, b + c * 128, kPV);
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + (KS + c) * 128, kPV);
+        }
+#pragma unroll
+        for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + c * 128, kPV);
+        tc::commit(&bar->o_full[q]);
+        mbar_arrive(&bar->o_full[q]);
+      };
+      if constexpr (ONE) {  // QK, PV, QK, ...: O is added up while the next QK runs
+#pragma unroll 1
+        for (int tile = 0; tile < mine; ++tile) {
+          alive = filled();
+          if (!alive) break;
+          if (__shfl_sync(0xffffffffu, bar->info[tile % kInfo].flags, 0) & kFirst) {
+            alive = wait(&bar->q_ready[0], (turn >> 2) & 1u);
+            if (!alive) break;
+            turn ^= 4u;
+          }
+          tc::fence_after_sync();
+          if (elect_one()) {
+            issue_qk(0, slot);
+            tc::commit(&bar->empty[slot]);
+          }
+          __syncwarp();
+          advance();
+          alive = filled() && wait(&bar->p_ready[0], turn & 1u);
+          if (!alive) break;
+          turn ^= 1u;
+          tc::fence_after_sync();
+          if (elect_one()) {
+            issue_pv(0, slot);
+            tc::commit(&bar->empty[slot]);
+          }
+          __syncwarp();
+          advance();
+        }
+      }
       // Order: PV of a row tile, then its next QK, while the other's softmax
       // runs. MMAs of one thread run in order, so that QK may overwrite the P
       // that the PV before it reads. Between units both PVs come first: the
       // next queries are written when both row tiles are done.
       uint32_t flags = 0, vslot = 0, kslot = 0;
 #pragma unroll 1
-      for (int tile = -1; tile < mine && mine > 0 && alive; ++tile) {
+      for (int tile = ONE ? mine : -1; tile < mine && mine > 0 && alive; ++tile) {
         const bool more = tile + 1 < mine;
         uint32_t next = 0;
         bool have = false;
@@ -1050,21 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (elect_one()) {
               if (does) {
-                const uint32_t b = v_desc + vslot * (G::UNIT >> 4);
-                const uint32_t p = tmem + q * 128, o = tmem + 256 + q * D;
-                constexpr int KS = KT / 16;
-                // p_lo v_hi, (quantised) p_hi v_lo, p_hi v_hi: the small ones first
-                mma_ts<false>(o, p + 8, b, kPV);
-#pragma unroll
-                for (int c = 1; c < KS; ++c) mma_ts<true>(o, p + 16 * c + 8, b + c * 128, kPV);
-                if constexpr (QUANT) {
-#pragma unroll
-                  for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + (KS + c) * 128, kPV);
-                }
-#pragma unroll
-                for (int c = 0; c < KS; ++c) mma_ts<true>(o, p + 16 * c, b + c * 128, kPV);
-                tc::commit(&bar->o_full[q]);
-                mbar_arrive(&bar->o_full[q]);
+                issue_pv(q, vslot);
               }
               if (q == 1) tc::commit(&bar->empty[vslot]);  // the last reader of V
             }
@@ -1081,15 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (elect_one()) {
               if (does) {
-                const uint32_t b = k_desc + kslot * (G::UNIT >> 4), d = tmem + q * 128;
-                const uint32_t hi = q_desc + q * (2 * G::QPART >> 4), lo = hi + (G::QPART >> 4);
-                mma_ss<false>(d, lo, b, kQK);  // low parts first
-#pragma unroll
-                for (int c = 1; c < D / 16; ++c) mma_ss<true>(d, lo + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), b + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), kQK);
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) mma_ss<true>(d, hi + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), b + (((c >> 2) * G::GROUP + (c & 3) * 32) >> 4), kQK);
-                tc::commit(&bar->s_full[q]);
-                mbar_arrive(&bar->s_full[q]);
+                issue_qk(q, kslot);
               }
               if (q == 1) tc::commit(&bar->empty[kslot]);  // the last reader of K
             }
@@ -1112,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true, first = true;
       Work w;
       if (total > 0) {
-        enter(w, P, bar->start_i);
+        enter<ROWS>(w, P, bar->start_i);
         w.h = bar->start_h;
         w.rt = bar->start_rt;
         w.k0 = bar->start_k;
@@ -1120,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (uint32_t tile = 0; left > 0; ++tile, --left) {
         if (first) {  // a unit
-          unit_tiles<KT>(w, a);
+          unit_tiles<KT, ROWS>(w, a);
           w.k1 = static_cast<int>(min(static_cast<long long>(w.n), w.k0 + left));
           if (un >= kUnits) alive = wait(&bar->unit_free[un % kUnits], ((un / kUnits) & 1u) ^ 1u);
           if (!alive) break;
@@ -1128,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long ux = per * blockIdx.x + (total - left) - w.k0;  // its first tile among all
             UnitInfo& u = bar->units[un % kUnits];
             u.tiles = w.k1 - w.k0;
-            u.rho0 = w.rt * kRows;
+            u.rho0 = w.rt * ROWS;
             u.rows = w.s.rows * a.group;
             u.row0 = w.s.row0;
             u.pos0 = w.s.len - w.s.rows;
@@ -1144,8 +1236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (un > 0) {  // its queries, towards the softmax threads
 #pragma unroll 1
-            for (int r = lane; r < kRows; r += 32) {
-              const int rho = w.rt * kRows + r, token = rho / a.group;
+            for (int r = lane; r < ROWS; r += 32) {
+              const int rho = w.rt * ROWS + r, token = rho / a.group;
               const float* src = a.Q + (w.s.row0 + token) * a.ldq + static_cast<long long>(w.h * a.group + rho - token * a.group) * D;
               if (P.vec_q && rho < w.s.rows * a.group) bulk_prefetch_l2(src, D * 4);
             }
@@ -1179,7 +1271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const bool every = a.window == 0 || j0 > w.p1 - a.window || j0 + KT <= a.sinks;
           uint32_t flags = pages;
-          if (w.rt * kRows + 128 < w.s.rows * a.group) flags |= kTwo;
+          if (w.rt * ROWS + 128 < w.s.rows * a.group) flags |= kTwo;
           if (first) flags |= kFirst;
           if (w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && every)) flags |= kMixed;
           if (pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= w.p1 && (j0 >= w.begin || j0 + KT <= w.sink_end)) flags |= kAll;
@@ -1198,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.rt = 0;
             if (++w.h == a.c.kv_heads) {
               w.h = 0;
-              enter(w, P, w.i + 1);
+              enter<ROWS>(w, P, w.i + 1);
             }
           }
           w.k0 = 0;
@@ -1267,20 +1359,27 @@ lq_status run(const TileParams& p, int ctas, cudaStream_t stream) {
 
 template <int FMT>
 lq_status pick(const TileParams& p, int ctas, cudaStream_t stream) {
-  return p.a.c.head_dim == 64 ? run<FMT, 64>(p, ctas, stream) : run<FMT, 128>(p, ctas, stream);
+  switch (p.a.c.head_dim) {
+    case 64: return run<FMT, 64>(p, ctas, stream);
+    case 128: return run<FMT, 128>(p, ctas, stream);
+    default: return run<FMT, 256>(p, ctas, stream);
+  }
 }
 
 }  // namespace
 
 size_t attn_tile_work_bytes(int head_dim) {
   const int ctas = std::min(std::max(device_info().sm_count, 152), kAttnMaxCtas);
-  if (head_dim != 64 && head_dim != 128) return 0;
-  return kAttnCounterBytes + static_cast<size_t>(ctas) * 2 * kRows * (head_dim + 2) * 4;
+  const int slot = head_dim == 64    ? Geo<LQ_FMT_F16, 64>::SLOT
+                   : head_dim == 128 ? Geo<LQ_FMT_F16, 128>::SLOT
+                   : head_dim == 256 ? Geo<LQ_FMT_F16, 256>::SLOT
+                                     : 0;
+  return slot == 0 ? 0 : kAttnCounterBytes + static_cast<size_t>(ctas) * 2 * slot * 4;
 }
 
 bool attn_tile_eligible(const AttnArgs& a) {
   const int d = a.c.head_dim;
-  return (d == 64 || d == 128) && a.c.page_size % 16 == 0 && aligned_to(a.c.k, 16) && aligned_to(a.c.v, 16) && a.b.batch <= kMaxBatch;
+  return (d == 64 || d == 128 || d == 256) && a.c.page_size % 16 == 0 && aligned_to(a.c.k, 16) && aligned_to(a.c.v, 16) && a.b.batch <= kMaxBatch;
 }
 
 lq_status launch_attn_tile(const AttnArgs& a, int fmt, int small_rows, void* work, cudaStream_t stream) {

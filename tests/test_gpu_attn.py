@@ -273,6 +273,39 @@ def test_layer_of_a_decoder(lq, cuda_dev):
     compare(y, ref + X.numpy()[:23], tol + 1e-6)
 
 
+@pytest.mark.parametrize("route", (WARP, TILE))
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("news,totals,heads,kv_heads,page,window,sinks", [
+    ([300], [300], 2, 2, 16, 0, 0), ([129, 1, 64], [700, 50, 64], 4, 1, 32, 0, 0), ([128], [1000], 1, 1, 64, 0, 0),
+    ([200, 3], [900, 33], 2, 1, 16, 150, 5), ([33], [2000], 8, 2, 128, 0, 0), ([100] * 5, [100, 163, 64, 99, 65], 3, 3, 16, 31, 33)])
+def test_chunks_of_wide_heads(lq, cuda_dev, route, fmt, news, totals, heads, kv_heads, page, window, sinks):
+    """Heads of 256: whole and partial units, units across CTAs, windows."""
+    P = Paged(lq, fmt, news, totals, heads, kv_heads, 256, page, cuda_dev, seed=len(news) + page)
+    _check(lq, P, route=route, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wide_heads_missing_keys_and_values_of_no_size(lq, cuda_dev, fmt):
+    """Heads of 256 in tiles: pages that are not there, rows before position 0,
+    and values that are not finite where only later rows see them."""
+    P = Paged(lq, fmt, [20, 140, 90], [9, 400, 100], 2, 1, 256, 16, cuda_dev, seed=4)
+    table = P.table.copy()
+    table[1, 3] = -1
+    table[2, :2] = -1
+    _check(lq, P, route=TILE, table=table)
+    pool, slot = P.pools[1, P.table[1, 390 // 16], 0], 390 % 16  # dim 200 of position 390, or its block's scale: NaN
+    at = slot * P.row + 400 if fmt == "f16" else 16 * P.row + slot * 16 + 200 // 32 * 2
+    pool[at:at + 2] = (0, 0x7E)
+    o, _ = _run(lq, P, route=TILE)
+    o = o[P.q_start[1]:P.q_start[2]]
+    late = np.arange(140) + 260 >= 390
+    block = np.zeros(256, dtype=bool)  # what the cache loses with it
+    block[slice(200, 201) if fmt == "f16" else slice(192, 224)] = True
+    assert np.isfinite(o[~late]).all() and np.isfinite(o[late][:, :, ~block]).all()
+    assert np.isnan(o[late][:, :, block]).all()
+    assert lq.last_device_error() == lq.LQ_OK
+
+
 @pytest.mark.parametrize("args", [["--batch", "3", "--prompt", "90", "--steps", "4", "--embed", "512", "--heads", "8", "--kv-heads", "2"],
                                   ["--fmt", "q4_0", "--cache", "f16", "--batch", "1", "--prompt", "40", "--steps", "3", "--embed",
                                    "256", "--heads", "4", "--kv-heads", "4", "--head-dim", "64", "--window", "16", "--sinks", "2"]])

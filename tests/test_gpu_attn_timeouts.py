@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("fmt,news,totals,d", [("f16", [300], [2000], 128), ("f16", [70, 5], [900, 300], 64),
-                                               ("q8_0", [200], [1500], 128), ("q4_0", [90], [700], 64)])
+                                               ("q8_0", [200], [1500], 128), ("q4_0", [90], [700], 64),
+                                               ("f16", [150], [900], 256), ("q8_0", [140, 70], [900, 100], 256)])
 def test_tile_kernel_timeout(lq, cuda_dev, fmt, news, totals, d):
     P = Paged(lq, fmt, news, totals, 4, 2, d, 16, cuda_dev, seed=3)
     cache, batch = P.cache(), P.batch()
