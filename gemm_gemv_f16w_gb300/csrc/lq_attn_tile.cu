@@ -113,6 +113,11 @@ struct Geo {
   static constexpr int QPART = HALVES * GROUP;             // hi or lo of a row tile
   static constexpr int Q = ROWS / 64 * QPART;              // [row tile][hi, lo]
   static constexpr int SMEM = Q + NU * UNIT + 1024 + 2048;  // alignment, barriers
+  // Key tiles that a unit's start and end cost. One prompt of 4096 tokens with 0 | 2 | 4 | 6 |
+  // 9, us: f16, heads of 64 244 | 196 | 184 | 188 | 197, of 128 364 | 294 | 243 | 245 | 255, of
+  // 256 833 | 614 | 510 | 414 | 388; Q8_0 318 | 273 | 253 | 261 | 267, 506 | 453 | 441 | 448 |
+  // 454, 1192 | 995 | 872 | 865 | 870
+  static constexpr int START = D != 256 ? 4 : (FMT == LQ_FMT_F16 ? 10 : 5);
   static constexpr int SLOT = ROWS * (D + 2);              // floats of a partial result
   // Quantised tiles: their loaders convert, and at 72 registers they wait on their own
   // chains. 2048 tokens over 16384 positions, 32 query heads over 8 of 128, Q8_0: 1652 us
@@ -157,7 +162,7 @@ struct Bars {
   uint32_t tmem;
   int last;
   int start_i, start_h, start_rt, start_k;
-  long long per, mine;
+  long long per, start_x, ends[2];  // tiles a CTA; the place of the first unit; tiles before the range's ends
   uint64_t told[kInfo], done[kInfo];   // a tile is described / its units are filled
   alignas(16) TileInfo info[kInfo];
   alignas(16) uint32_t bad[kInfo][4];  // keys whose values are not finite (kept out of the MMA)
@@ -336,30 +341,35 @@ __device__ __forceinline__ long long scan32(long long mine, int lane) {
   return mine;
 }
 
-// This CTA's range of all units' tiles, in the order (sequence, key/value
-// head, row tile, key tile): its first unit and its length, into `bar`.
-template <int KT, int ROWS>
+// This CTA's range of all units' tiles, in the order (sequence, key/value head, row
+// tile, key tile). A unit counts as START tiles more than it has, ahead of its own:
+// its start costs about that much, and without it the CTAs that get the many short
+// units of a prompt's beginning are the last to end. Warps 0 and 1 look for the
+// range's two ends: the tiles before each, and where the first one is.
+template <int KT, int ROWS, int START>
 __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* totals, int warp, int lane) {
   const AttnArgs& a = P.a;
+  int* const units = reinterpret_cast<int*>(totals + kMaxBatch);
 #pragma unroll 1
   for (int i = warp; i < a.b.batch; i += kThreads / 32) {
     Work w;
     w.s = kv::sequence(a.b, a.c.page_size, i);
     long long sum = 0;
-    if (takes(w.s, P)) {
-      const int rts = (w.s.rows * a.group + ROWS - 1) / ROWS;
+    const int rts = takes(w.s, P) ? (w.s.rows * a.group + ROWS - 1) / ROWS : 0;
 #pragma unroll 1
-      for (w.rt = lane; w.rt < rts; w.rt += 32) {
-        unit_tiles<KT, ROWS>(w, a);
-        sum += w.n;
-      }
+    for (w.rt = lane; w.rt < rts; w.rt += 32) {
+      unit_tiles<KT, ROWS>(w, a);
+      sum += w.n + START;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) totals[i] = sum;
+    if (lane == 0) {
+      totals[i] = sum;  // of one head
+      units[i] = rts;
+    }
   }
   __syncthreads();
-  if (warp != 0) return;
+  if (warp > 1) return;
   long long all = 0;
 #pragma unroll 1
   for (int i = lane; i < a.b.batch; i += 32) all += totals[i];
@@ -367,22 +377,26 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   all *= a.c.kv_heads;
   const long long per = max(kv::quotient(all + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
-  long long x = per * blockIdx.x;
-  const long long mine = min(per, all - x);
+  const long long end = min(per * (blockIdx.x + warp), all);
+  long long x = end, before = 0;  // place in the unit in the end; units before it
   int i = 0, h = 0, rt = 0;
-  if (mine > 0) {
 #pragma unroll 1
-    for (int base = 0;; base += 32) {  // the sequence
-      const long long here = base + lane < a.b.batch ? totals[base + lane] * a.c.kv_heads : 0, incl = scan32(here, lane);
-      const unsigned past = __ballot_sync(0xffffffffu, x < incl);
-      if (past) {
-        const int at = __ffs(static_cast<int>(past)) - 1;
-        i = base + at;
-        x -= __shfl_sync(0xffffffffu, incl - here, at);
-        break;
-      }
-      x -= __shfl_sync(0xffffffffu, incl, 31);
+  for (int base = 0; base < a.b.batch; base += 32) {  // the sequence
+    const bool is = base + lane < a.b.batch;
+    const long long here = is ? totals[base + lane] * a.c.kv_heads : 0, incl = scan32(here, lane);
+    const long long us = scan32(is ? static_cast<long long>(units[base + lane]) * a.c.kv_heads : 0, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, x < incl);
+    const int at = past ? __ffs(static_cast<int>(past)) - 1 : 31;
+    const long long skip = __shfl_sync(0xffffffffu, incl - (past ? here : 0), at);
+    x -= skip;
+    if (past) {
+      i = base + at;
+      before += __shfl_sync(0xffffffffu, us, at) - static_cast<long long>(units[i]) * a.c.kv_heads;
+      break;
     }
+    before += __shfl_sync(0xffffffffu, us, 31);
+  }
+  if (end < all) {
     h = static_cast<int>(kv::quotient(x, totals[i]));
     x -= h * totals[i];
     Work w;
@@ -391,7 +405,7 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
     for (int base = 0;; base += 32) {  // the row tile
       w.rt = base + lane;
       unit_tiles<KT, ROWS>(w, a);
-      const long long here = w.rt * ROWS < w.s.rows * a.group ? w.n : 0, incl = scan32(here, lane);
+      const long long here = w.rt < units[i] ? w.n + START : 0, incl = scan32(here, lane);
       const unsigned past = __ballot_sync(0xffffffffu, x < incl);
       if (past) {
         const int at = __ffs(static_cast<int>(past)) - 1;
@@ -401,14 +415,19 @@ __device__ __forceinline__ void plan(const TileParams& P, Bars* bar, long long* 
       }
       x -= __shfl_sync(0xffffffffu, incl, 31);
     }
+    before += static_cast<long long>(h) * units[i] + rt;
   }
   if (lane == 0) {
-    bar->per = per;
-    bar->mine = mine;
-    bar->start_i = i;
-    bar->start_h = h;
-    bar->start_rt = rt;
-    bar->start_k = static_cast<int>(x);
+    // tiles before the end: its place less the starts before it
+    bar->ends[warp] = end - x - START * before + max(x - START, 0ll);
+    if (warp == 0) {
+      bar->per = per;
+      bar->start_i = i;
+      bar->start_h = h;
+      bar->start_rt = rt;
+      bar->start_k = static_cast<int>(max(x - START, 0ll));
+      bar->start_x = end - x;
+    }
   }
 }
 
@@ -454,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
-  plan<KT, ROWS>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
+  plan<KT, ROWS, G::START>(P, bar, reinterpret_cast<long long*>(ring), warp, lane);
   if (warp == 12) {
     tc::tmem_alloc(&bar->tmem, 512);
     tc::tmem_relinquish();
@@ -464,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
+  const int mine = __shfl_sync(0xffffffffu, static_cast<int>(min(bar->ends[1] - bar->ends[0], 1ll << 30)), 0);  // key tiles here
 
   bool in_time = true;  // no wait of this warp has run out
   auto wait = [&](uint64_t* b, uint32_t parity) {  // by whole warps
@@ -822,7 +842,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CPR = QUANT ? D / 16 : D / 8;          // chunks a row: 16 codes, or 16 bytes of f16
     constexpr int PASS = kLoaders / CPR, N = KT / PASS;  // rows a pass, passes
     const int row0 = tl / CPR, ch = tl % CPR;
-    const long long total = bar->mine;
     bool alive = true;
 
     // the values of a unit's chunks that this thread copied: those that are not
@@ -885,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pend = 0;
     };
 #pragma unroll 1
-    for (uint32_t tile = 0; tile < total && alive; ++tile) {  // loader
+    for (uint32_t tile = 0; tile < static_cast<uint32_t>(mine) && alive; ++tile) {  // loader
       const TileInfo& c = bar->info[tile % kInfo];
       if (!QUANT || tile == 0) {
         alive = wait(&bar->told[tile % kInfo], (tile / kInfo) & 1u);
@@ -963,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (it + 1 < N) {
             fetch(it + 1, c);
-          } else if (tile + 1 < total) {
+          } else if (tile + 1 < static_cast<uint32_t>(mine)) {
             alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
             if (!alive) break;
             fetch(0, bar->info[(tile + 1) % kInfo]);
@@ -1054,7 +1073,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kQK = tc::idesc_f16_f32(128, G::KROWS);
       constexpr uint32_t kPV = tc::idesc_f16_f32(128, D) | (1u << 16);  // B is MN-major
       const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring)), v_desc = desc_mn<G::KGROUP>(smem_u32(ring));
-      const int mine = __shfl_sync(0xffffffffu, static_cast<int>(min(max(bar->mine, 0ll), 1ll << 30)), 0);
       uint32_t turn = 0;  // parities: bits 0, 1 tiles of a row tile, bits 2, 3 its units, bit 4 the ring
       uint32_t slot = 0;  // ring unit of the next K or V
       bool alive = true;
@@ -1197,13 +1215,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&bar->drain, 0, kDrainWaitNs);
     } else if (warp == 13) {
       // ---- walks the CTA's tiles a few ahead of the loaders ----------------------------
-      const long long total = bar->mine, per = bar->per;
-      long long left = total;  // tiles from the walk's on
+      const long long per = bar->per;
+      long long ux = bar->start_x;  // the unit's place among all tiles and starts
+      int left = mine;              // tiles from the walk's on
       uint32_t un = 0;
       int k = 0;
       bool alive = true, first = true;
       Work w;
-      if (total > 0) {
+      if (mine > 0) {
         enter<ROWS>(w, P, bar->start_i);
         w.h = bar->start_h;
         w.rt = bar->start_rt;
@@ -1213,11 +1232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t tile = 0; left > 0; ++tile, --left) {
         if (first) {  // a unit
           unit_tiles<KT, ROWS>(w, a);
-          w.k1 = static_cast<int>(min(static_cast<long long>(w.n), w.k0 + left));
+          w.k1 = min(w.n, w.k0 + left);
           if (un >= kUnits) alive = wait(&bar->unit_free[un % kUnits], ((un / kUnits) & 1u) ^ 1u);
           if (!alive) break;
           if (lane == 0) {
-            const long long ux = per * blockIdx.x + (total - left) - w.k0;  // its first tile among all
             UnitInfo& u = bar->units[un % kUnits];
             u.tiles = w.k1 - w.k0;
             u.rho0 = w.rt * ROWS;
@@ -1228,8 +1246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.seq = w.i;
             u.kv_head = w.h;
             const bool whole = w.k0 == 0 && w.k1 == w.n;
-            u.c0 = whole ? 0 : static_cast<int>(kv::quotient(ux, per));
-            u.c1 = whole ? 0 : static_cast<int>(kv::quotient(ux + w.n - 1, per));
+            u.c0 = whole ? 0 : static_cast<int>(kv::quotient(ux + G::START, per));
+            u.c1 = whole ? 0 : static_cast<int>(kv::quotient(ux + G::START + w.n - 1, per));
             u.slot = 2 * static_cast<int>(blockIdx.x) + (w.k0 == 0 ? 1 : 0);
             mbar_arrive(&bar->unit[un % kUnits]);
           }
@@ -1286,6 +1304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar->told[tile % kInfo]);
         first = ++k == w.k1 && left > 1;
         if (first) {
+          ux += G::START + w.n;
           if (++w.rt == w.row_tiles) {
             w.rt = 0;
             if (++w.h == a.c.kv_heads) {
