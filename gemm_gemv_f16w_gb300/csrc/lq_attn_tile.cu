@@ -502,7 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lanes + rq * 128, p_at = ONE ? s_at + 128 : s_at, o_at = tmem + lanes + 256 + q * DO;
     unsigned char* const q_hi = smem + rq * 2 * G::QPART;
     unsigned char* const q_lo = q_hi + G::QPART;
-    unsigned char* const stage = smem + q * 2 * (DO / 64) * G::GROUP;  // where the group's rows go out from
+    // the column groups of the queries' two parts that are this softmax group's own:
+    // its rows come and go through them, 32 floats a group
+    auto own = [&](int s) { return q_hi + (ONE ? (s >> 1) * 4 + 2 * half + (s & 1) : s) * G::GROUP; };
     uint32_t tile = 0, tiles_q = 0, joins = 0;  // tiles done by the CTA, by this row tile
 #pragma unroll 1
     for (uint32_t un = 0;; ++un) {
@@ -517,64 +519,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = w.row0 + token, head = w.head0 + (min(rho, w.rows - 1) - token * a.group), pos = w.pos0 + token;
       float om[DO], M = kNoMax, l = 0.0f, f = 0.0f;
       if (active) {
-        // the warp's 32 query rows, one or two at a time: scaled to the top of f16's
-        // range, in two parts (one row tile: the first group lays the high parts, the
-        // second the low ones, where its rows will go out later)
-        constexpr int NB = D > 128 ? 2 : 1;                  // 16-byte loads a lane and row
-        constexpr int LPR = D / 4 / NB, RPI = 32 / LPR;      // lanes a row, rows at a time
-        constexpr int STEP = 16 / NB, BOTH = STEP / RPI;
+        // The warp's 32 query rows come as f32 into the very bytes of shared memory
+        // that their two f16 parts will take (rows of 128 bytes in the group's own
+        // column groups), and each thread turns its row: no other thread's bytes.
+        constexpr int LPR = DO / 4, RPI = 32 / LPR;  // lanes a row, rows at a time
         const int l4 = lane % LPR;
-        const long long off = t * a.ldq + static_cast<long long>(head) * D;
+        const long long off = t * a.ldq + static_cast<long long>(head) * D + dim0;
         const uint32_t live = __ballot_sync(0xffffffffu, row);
-        const uint32_t col = (l4 >> 4) * G::GROUP + (l4 & 1) * 8;  // column group, half of a 16-byte chunk
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += STEP) {
-          float4 v[BOTH][NB];
-#pragma unroll
-          for (int i = 0; i < BOTH; ++i) {
-            const int rr = r0 + i * RPI + lane / LPR;
-            const float* src = a.Q + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              v[i][b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if ((live >> rr) & 1u) {
-                if (P.vec_q) {
-                  v[i][b] = ldg128f(src + b * 128);
-                } else {
-                  v[i][b] = make_float4(src[b * 128], src[b * 128 + 1], src[b * 128 + 2], src[b * 128 + 3]);
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < BOTH; ++i) {
-            const int rr = r0 + i * RPI + lane / LPR;
-            float top = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i][b].x), fabsf(v[i][b].y)), fmaxf(fabsf(v[i][b].z), fabsf(v[i][b].w))));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-            const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
-            const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
-            // the row's own lane keeps the factor that takes S back to base-2 logits
-            const float back = __uint_as_float(static_cast<unsigned>(254 - es) << 23);
-            const float fr = __shfl_sync(0xffffffffu, back, (lane % RPI) * LPR);
-            if (lane / RPI == (r0 + i * RPI) / RPI) f = fr;
-            const float sg = a.scale < 0.0f ? -sigma : sigma;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              uint2 hi, lo;
-              split2(v[i][b].x * sg, v[i][b].y * sg, hi.x, lo.x);
-              split2(v[i][b].z * sg, v[i][b].w * sg, hi.y, lo.y);
-              const uint32_t at = b * 2 * G::GROUP + col + tc::sw128_offset((warp & 3) * 32 + rr, (l4 >> 1) & 7);
-              if (!ONE || half == 0) *reinterpret_cast<uint2*>(q_hi + at) = hi;
-              if (!ONE || half == 1) *reinterpret_cast<uint2*>(q_lo + at) = lo;
-            }
+        unsigned char* const land = own(l4 >> 3) + (warp & 3) * 32 * 128 + (l4 & 7) * 16;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int rr = r0 + lane / LPR;
+          const float* src = a.Q + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
+          const bool there = (live >> rr) & 1u;
+          if (P.vec_q) {
+            copy16(smem_u32(land + rr * 128), there ? src : a.Q, there);
+          } else {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (there) v = make_float4(src[0], src[1], src[2], src[3]);
+            *reinterpret_cast<float4*>(land + rr * 128) = v;
           }
         }
-        f *= fabsf(a.scale) * kLog2e;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        wait_copies<0>();
+        __syncwarp();
+        // 16-byte chunks in an order of the row's own, so that eight rows hit all banks
+        float4 v[DO / 4];
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < DO / 4; ++j) {
+          v[j] = *reinterpret_cast<const float4*>(own(j >> 3) + r * 128 + (((j ^ r) & 7) << 4));
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w))));
+        }
+        if constexpr (ONE) {  // the other half's
+          tmem_st1(p_at + 2 + half, __float_as_uint(top));
+          tc::wait_st();
+          tc::fence_before_sync();
+          mbar_arrive(&bar->join);
+          if (!wait(&bar->join, joins++ & 1u)) break;
+          tc::fence_after_sync();
+          const uint32_t other = tmem_ld1(p_at + 2 + (half ^ 1));
+          tc::wait_ld();
+          tc::fence_before_sync();
+          top = fmaxf(top, __uint_as_float(other));
+        }
+        // scaled to the top of f16's range by a power of two; f takes S back to base-2 logits
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+        const int es = ex == 0 || ex == 255 ? 127 : min(max(127 + 127 + 14 - ex, 1), 253);
+        const float sigma = __uint_as_float(static_cast<unsigned>(es) << 23);
+        f = __uint_as_float(static_cast<unsigned>(254 - es) << 23) * fabsf(a.scale) * kLog2e;
+        const float sg = a.scale < 0.0f ? -sigma : sigma;
+        const bool odd = r & 1;
+#pragma unroll
+        for (int j = 0; j < DO / 4; j += 2) {
+          const float4 x = odd ? v[j + 1] : v[j], y = odd ? v[j] : v[j + 1];  // dims in order
+          uint4 hi, lo;
+          split2(x.x * sg, x.y * sg, hi.x, lo.x);
+          split2(x.z * sg, x.w * sg, hi.y, lo.y);
+          split2(y.x * sg, y.y * sg, hi.z, lo.z);
+          split2(y.z * sg, y.w * sg, hi.w, lo.w);
+          const int c8 = (j >> 3 & 1) * 4 + (((j >> 1) ^ (r >> 1)) & 3);  // 16-byte chunk of the 64-dim group
+          const uint32_t at = (ONE ? 2 * half + (j >> 4) : j >> 4) * G::GROUP + r * 128 + ((c8 ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(q_hi + at) = hi;
+          *reinterpret_cast<uint4*>(q_lo + at) = lo;
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bar->q_ready[rq]);
 #pragma unroll
@@ -807,18 +815,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int d = 0; d < DO; d += 4)
-          *reinterpret_cast<float4*>(stage + (d / 32) * G::GROUP + tc::sw128_offset(r, (d / 4) & 7)) =
+          *reinterpret_cast<float4*>(own(d / 32) + tc::sw128_offset(r, (d / 4) & 7)) =
               make_float4(om[d] * inv, om[d + 1] * inv, om[d + 2] * inv, om[d + 3] * inv);
         __syncwarp();
         constexpr int LPR = DO / 4, RPI = 32 / LPR;
         const int l4 = lane % LPR;
         const uint32_t live = __ballot_sync(0xffffffffu, row && LQ_IN_BOUNDS(t < a.b.tokens && head < a.heads));
         const long long off = t * a.ldo + static_cast<long long>(head) * D + dim0;
-#pragma unroll 4
+        const unsigned char* const from = own(l4 >> 3);
+#pragma unroll 8
         for (int r0 = 0; r0 < 32; r0 += RPI) {
           const int rr = r0 + lane / LPR;
           float* out = a.O + __shfl_sync(0xffffffffu, off, rr) + l4 * 4;
-          const float4 v = *reinterpret_cast<const float4*>(stage + (l4 >> 3) * G::GROUP + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
+          const float4 v = *reinterpret_cast<const float4*>(from + tc::sw128_offset((warp & 3) * 32 + rr, l4 & 7));
           if ((live >> rr) & 1u) {
             if (P.vec_o) {
               *reinterpret_cast<float4*>(out) = v;
