@@ -28,8 +28,9 @@
 // KB of shared memory, so a unit is 128 rows and a key tile 64 rows. Both
 // softmax groups work on that row tile: each takes the maximum over all keys (the
 // same bits in both), weighs its half of the keys (P has columns of its own) and
-// sums its half of O's dims. 3 prompts of up to 2001 tokens, 16 heads over 2, take
-// 512 us in f16 and 679 in Q8_0 (2892 and 1845 on warp-level MMAs).
+// sums its half of O's dims; QK of the next tile (S in two places in turn) runs
+// under the softmax. 2048 tokens over 16384 positions, 16 heads over 2, run at
+// 591 TFLOP/s of the plain formula in f16, 198 in Q8_0 (tiles of 32 keys only).
 //
 // Roles (four warpgroups, registers moved between them): two softmax groups,
 // one per row tile; four loader warps (16-byte asynchronous copies for f16;
@@ -43,16 +44,18 @@
 //
 // What bounds it. The floor are the tensor cores at two (f16) or 3.5 (quantised:
 // 2 x 2 products for S, 3 for O) MMAs a product of the plain formula; they are
-// busy for 51 % of the cycles. The rest is each row tile's own chain: S has to
+// busy for half of the cycles. The rest is each row tile's own chain: S has to
 // be read, the weights of 128 keys a thread computed and written, and O
 // added before that tile's next MMAs, and the other tile's work covers half of it;
 // without the weights' arithmetic, or without either product, the time stays
-// within 10 %. 3 prompts of up to 4001 tokens, 32 heads over 8 of 128, f16:
-// 595 us (433 TFLOP/s of the plain formula); 2048 tokens over 16384 positions,
-// Q8_0: 1530 us (337 TFLOP/s), here the loaders' conversions (two parts of every
-// element for every CTA that reads it) take as long as the MMAs. A prompt of
-// 8192 under a window of 1024, heads of 64: 280 us; its units have nine tiles,
-// and each unit's start (its queries' two parts) is not covered.
+// within 10 %. 1024 tokens over 16384 positions, 32 heads over 8 of 128, f16: 357 us
+// (746 TFLOP/s of the plain formula, two MMAs a product); 2048 over 16384, Q8_0:
+// 1397 us (369 TFLOP/s), where the loaders' conversions (two parts of every element
+// for every CTA that reads it) take as long as the MMAs. A unit's start and end add
+// 10 us: 128 KB of queries come in and as much goes out at about 20 bytes a cycle an
+// SM, and asking for the queries a tile earlier changed nothing. So 3 prompts of up
+// to 4001 tokens, f16, take 459 us (562 TFLOP/s), and a prompt of 8192 under a window
+// of 1024, 32 heads over 8 of 64, whose units have nine tiles, 235.
 // Every wait is bounded; on timeout the kernel records LQ_ERR_DEVICE_TIMEOUT,
 // lets its copies and MMAs finish, frees TMEM and returns.
 #include <cuda.h>
@@ -114,9 +117,9 @@ struct Geo {
   static constexpr int Q = ROWS / 64 * QPART;              // [row tile][hi, lo]
   static constexpr int SMEM = Q + NU * UNIT + 1024 + 2048;  // alignment, barriers
   // Key tiles that a unit's start and end cost. One prompt of 4096 tokens with 0 | 2 | 4 | 6 |
-  // 9, us: f16, heads of 64 244 | 196 | 184 | 188 | 197, of 128 364 | 294 | 243 | 245 | 255, of
-  // 256 833 | 614 | 510 | 414 | 388; Q8_0 318 | 273 | 253 | 261 | 267, 506 | 453 | 441 | 448 |
-  // 454, 1192 | 995 | 872 | 865 | 870
+  // 9, us: f16, heads of 64 244 | 196 | 184 | 188 | 197, of 128 364 | 294 | 243 | 245 | 255;
+  // Q8_0 318 | 273 | 253 | 261 | 267, 506 | 453 | 441 | 448 | 454. Heads of 256: f16 with 7 |
+  // 10 | 13 318 | 308 | 316, Q8_0 with 4 | 5 | 7 767 | 761 | 768.
   static constexpr int START = D != 256 ? 4 : (FMT == LQ_FMT_F16 ? 10 : 5);
   static constexpr int SLOT = ROWS * (D + 2);              // floats of a partial result
   // Quantised tiles: their loaders convert, and at 72 registers they wait on their own
@@ -592,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!active) tile += tiles;
 #pragma unroll 1
       for (int k = 0; k < (active ? tiles : 0); ++k, ++tile, ++tiles_q) {
-        ok = wait(&bar->s_full[rq], tiles_q & 1u);
+        // (one row tile: S of the next tile comes while this one's lies here, in turn)
+        const uint32_t s_now = s_at + (ONE ? (tiles_q & 1u) * 64 : 0);
+        ok = ONE ? wait(&bar->s_full[tiles_q & 1u], (tiles_q >> 1) & 1u) : wait(&bar->s_full[rq], tiles_q & 1u);
         if (!ok) break;
         tc::fence_after_sync();
         const int j0 = bar->info[tile % kInfo].j0;
@@ -618,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int j = from; j < to; j += 16) {
             uint32_t s[16];
-            tmem_ld16(s_at + j, s);
+            tmem_ld16(s_now + j, s);
             const uint32_t vis = masked ? vis32(j) : 0u;
             if constexpr (QUANT) {
               uint32_t low[16];
-              tmem_ld16(s_at + KT + j, low);
+              tmem_ld16(s_now + KT + j, low);
               tc::wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
@@ -882,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     uint32_t unit = 0, pend = 0;  // ring units filled; f16: unit whose copies are not yet reported, plus one
+    uint32_t pend_tile = 0;       // its tile
     uint32_t boxed = 0;           // f16, bit i: the copy engine fills the i-th unit from the last
     bool pend_screen = false;
     using Raw = typename std::conditional<FMT == LQ_FMT_Q8_0, uint4, uint2>::type;
@@ -907,22 +913,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto report = [&]() {  // f16: the pending unit has landed
       const uint32_t u = pend - 1;
-      if (pend_screen) screen((u % NU) * G::UNIT, u / 2);
+      if (pend_screen) screen((u % NU) * G::UNIT, pend_tile);
       fence_proxy_async_smem();
       mbar_arrive(&bar->full[u % NU]);
       pend = 0;
     };
+    // Units go in the order of their use. One row tile: the next tile's K before this
+    // one's V, so a step is K of its tile and V of the tile before.
+    const uint32_t tiles = static_cast<uint32_t>(max(mine, 0)), steps = tiles > 0 ? tiles + (ONE ? 1 : 0) : 0;
 #pragma unroll 1
-    for (uint32_t tile = 0; tile < static_cast<uint32_t>(mine) && alive; ++tile) {  // loader
-      const TileInfo& c = bar->info[tile % kInfo];
-      if (!QUANT || tile == 0) {
-        alive = wait(&bar->told[tile % kInfo], (tile / kInfo) & 1u);
+    for (uint32_t step = 0; step < steps && alive; ++step) {  // loader
+      const int first = ONE && step == tiles ? 1 : 0, last = ONE && step == 0 ? 1 : 2;  // sides
+      if ((!QUANT || step == 0) && step < tiles) {
+        alive = wait(&bar->told[step % kInfo], (step / kInfo) & 1u);
         if (!alive) break;
-        if constexpr (QUANT) fetch(0, c);
+        if constexpr (QUANT) fetch(0, bar->info[step % kInfo]);
       }
       if constexpr (!QUANT) {
 #pragma unroll 1
-        for (int side = 0; side < 2; ++side, ++unit) {
+        for (int side = first; side < last; ++side, ++unit) {
+          const TileInfo& c = bar->info[(step - (ONE ? side : 0)) % kInfo];
           uint64_t* const e = &bar->empty[unit % NU];
           const uint32_t parity = ((unit / NU) & 1u) ^ 1u;
           uint64_t* const fl = &bar->full[unit % NU];
@@ -970,12 +980,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pend = unit + 1;
           pend_screen = side == 1 && (c.flags & kMixed);
+          pend_tile = step - (ONE ? side : 0);
         }
       } else {
         // Two passes at a time, K's and then V's, in a small loop (straight code for
         // all passes is bound by instruction fetches); two are on their way.
 #pragma unroll 1
-        for (int it = 0; it < N; ++it) {
+        for (int it = first * (N / 2); it < last * (N / 2); ++it) {
           const int side = it / (N / 2), nn = it % (N / 2);
           if (nn == 0) {
             alive = wait(&bar->empty[unit % NU], ((unit / NU) & 1u) ^ 1u);
@@ -989,14 +1000,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<Raw*>(w4[i]) = ahead[i];
             d2[i] = there[i] ? sc_ahead[i] : __ushort_as_half(0);
           }
-          if (it + 1 < N) {
-            fetch(it + 1, c);
-          } else if (tile + 1 < static_cast<uint32_t>(mine)) {
-            alive = wait(&bar->told[(tile + 1) % kInfo], ((tile + 1) / kInfo) & 1u);
+          const uint32_t tile = step - (ONE ? side : 0);
+          if (it + 1 < last * (N / 2)) {
+            fetch(it + 1, bar->info[(step - (ONE ? (it + 1) / (N / 2) : 0)) % kInfo]);
+          } else if (step + 1 < tiles) {
+            alive = wait(&bar->told[(step + 1) % kInfo], ((step + 1) / kInfo) & 1u);
             if (!alive) break;
-            fetch(0, bar->info[(tile + 1) % kInfo]);
+            fetch(0, bar->info[(step + 1) % kInfo]);
+          } else if (ONE && step + 1 < steps) {
+            fetch(N / 2, bar->info[step % kInfo]);
           }
-          const bool mixed = side == 1 && (c.flags & kMixed);
+          const bool mixed = side == 1 && (bar->info[tile % kInfo].flags & kMixed);
           // step by step for both passes at once: one chain after the other would
           // leave this warp waiting for its own results
           uint32_t hi[2][8], lo[2][8];
@@ -1064,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!alive) break;
-      mbar_arrive(&bar->done[tile % kInfo]);
+      if (!ONE || step > 0) mbar_arrive(&bar->done[(step - (ONE ? 1 : 0)) % kInfo]);
     }
     wait_copies<0>();
     if (pend) report();
@@ -1094,8 +1108,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // S = Q K^T for row tile q, its low parts first; O = P V: p_lo v_hi, (quantised)
       // p_hi v_lo, p_hi v_hi, the small ones first
-      auto issue_qk = [&](int q, uint32_t kslot) {
-        const uint32_t b = k_desc + kslot * (G::UNIT >> 4), d = tmem + q * 128;
+      auto issue_qk = [&](int q, uint32_t kslot, int buf) {
+        const uint32_t b = k_desc + kslot * (G::UNIT >> 4), d = tmem + q * 128 + buf * 64;
         const uint32_t hi = q_desc + q * (2 * G::QPART >> 4), lo = hi + (G::QPART >> 4);
         auto at = [](int c, int group) -> uint32_t { return ((c >> 2) * group + (c & 3) * 32) >> 4; };
         mma_ss<false>(d, lo, b, kQK);
@@ -1103,8 +1117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 1; c < D / 16; ++c) mma_ss<true>(d, lo + at(c, G::GROUP), b + at(c, G::KGROUP), kQK);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) mma_ss<true>(d, hi + at(c, G::GROUP), b + at(c, G::KGROUP), kQK);
-        tc::commit(&bar->s_full[q]);
-        mbar_arrive(&bar->s_full[q]);
+        tc::commit(&bar->s_full[q + buf]);
+        mbar_arrive(&bar->s_full[q + buf]);
       };
       auto issue_pv = [&](int q, uint32_t vslot) {
         const uint32_t b = v_desc + vslot * (G::UNIT >> 4);
@@ -1122,23 +1136,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::commit(&bar->o_full[q]);
         mbar_arrive(&bar->o_full[q]);
       };
-      if constexpr (ONE) {  // QK, PV, QK, ...: O is added up while the next QK runs
-#pragma unroll 1
-        for (int tile = 0; tile < mine; ++tile) {
-          alive = filled();
-          if (!alive) break;
-          if (__shfl_sync(0xffffffffu, bar->info[tile % kInfo].flags, 0) & kFirst) {
-            alive = wait(&bar->q_ready[0], (turn >> 2) & 1u);
-            if (!alive) break;
-            turn ^= 4u;
-          }
+      if constexpr (ONE) {
+        // QK of a tile, then PV of the tile before, whose softmax ran meanwhile; between
+        // units PV first, as the next queries are written after it
+        auto qk = [&](uint32_t kslot, int tile) {
           tc::fence_after_sync();
           if (elect_one()) {
-            issue_qk(0, slot);
-            tc::commit(&bar->empty[slot]);
+            issue_qk(0, kslot, tile & 1);
+            tc::commit(&bar->empty[kslot]);
           }
           __syncwarp();
-          advance();
+        };
+        auto queries = [&]() {
+          const bool there = wait(&bar->q_ready[0], (turn >> 2) & 1u);
+          turn ^= 4u;
+          return there;
+        };
+        if (mine > 0) {
+          alive = filled() && queries();
+          if (alive) {
+            qk(slot, 0);
+            advance();
+          }
+        }
+#pragma unroll 1
+        for (int tile = 0; tile < mine && alive; ++tile) {
+          const bool more = tile + 1 < mine;
+          bool fresh = false;  // the next tile is a unit's first
+          uint32_t kslot = 0;
+          if (more) {
+            alive = filled();
+            if (!alive) break;
+            kslot = slot;
+            advance();
+            fresh = __shfl_sync(0xffffffffu, bar->info[(tile + 1) % kInfo].flags, 0) & kFirst;
+            if (!fresh) qk(kslot, tile + 1);
+          }
           alive = filled() && wait(&bar->p_ready[0], turn & 1u);
           if (!alive) break;
           turn ^= 1u;
@@ -1149,6 +1182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           advance();
+          if (fresh) {
+            alive = queries();
+            if (alive) qk(kslot, tile + 1);
+          }
         }
       }
       // Order: PV of a row tile, then its next QK, while the other's softmax
@@ -1208,7 +1245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (elect_one()) {
               if (does) {
-                issue_qk(q, kslot);
+                issue_qk(q, kslot, 0);
               }
               if (q == 1) tc::commit(&bar->empty[kslot]);  // the last reader of K
             }
