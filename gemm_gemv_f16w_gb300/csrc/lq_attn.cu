@@ -29,7 +29,7 @@ constexpr int kGWarps = 8;
 constexpr int kMaxDim = 256;
 // Rows (tokens x query heads a key/value head) of a sequence up to which the
 // warp-level kernel runs: it reads the keys once for every 16 rows, and its
-// time grows with the rows; the tile kernel's is that of 256 rows. 32 heads
+// time grows with the rows; the tile kernel's is that of 256 (heads of 256: 128) rows. 32 heads
 // over 8, 16 sequences of 4096 | one of 32768, us, warp-level / tile:
 //   rows           32               48               64               128
 //   f16, 64    42/70 | 33/54    51/71 | 40/60    65/72 | 48/55    106/75 | 81/57
@@ -38,13 +38,10 @@ constexpr int kMaxDim = 256;
 //   Q8_0, 128  65/169 | 58/148  82/174 | 75/159  105/177 | 95/152  180/184 | 173/158
 //   Q4_0, 128  65/155 | 57/135  81/156 | 75/144  105/147 | 95/135  178/156 | 175/138
 // 16 sequences of 4096, 2 | 4 heads of 256:
-//   rows           64                80                96                128
-//   f16, 256   62/81 | 123/118   72/91 | 151/127   87/91 | 179/129   118/86 | 233/126
-//   Q8_0, 256  58/110 | 115/199  68/109 | 144/206  82/112 | 171/208  110/114 | 219/216
-int few_rows(int fmt, int head_dim) {
-  if (head_dim == 256) return fmt == LQ_FMT_F16 ? 64 : 128;
-  return fmt == LQ_FMT_F16 ? 48 : 80;
-}
+//   rows           32               48              80                96
+//   f16, 256   42/57 | 73/77    52/57 | 95/77   72/59 | 150/77    86/60 | 180/79
+//   Q8_0, 256  39/88 | 70/171   49/88 | 91/176  68/90 | 143/185   82/91 | 171/189
+int few_rows(int fmt, int head_dim) { return fmt == LQ_FMT_F16 ? 48 : (head_dim == 256 ? 96 : 80); }
 
 template <int FMT>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
