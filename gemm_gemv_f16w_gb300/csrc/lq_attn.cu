@@ -32,15 +32,15 @@ constexpr int kMaxDim = 256;
 // time grows with the rows; the tile kernel's is that of 256 (heads of 256: 128) rows. 32 heads
 // over 8, 16 sequences of 4096 | one of 32768, us, warp-level / tile:
 //   rows           32               48               64               128
-//   f16, 64    42/70 | 33/54    51/71 | 40/60    65/72 | 48/55    106/75 | 81/57
-//   f16, 128   68/109 | 64/85   83/110 | 84/95   110/111 | 105/86  172/116 | 190/88
-//   Q8_0, 64   48/94 | 37/72    59/94 | 45/77    74/89 | 55/73    117/91 | 94/74
-//   Q8_0, 128  65/169 | 58/148  82/174 | 75/159  105/177 | 95/152  180/184 | 173/158
-//   Q4_0, 128  65/155 | 57/135  81/156 | 75/144  105/147 | 95/135  178/156 | 175/138
+//   f16, 64    31/59 | 32/50    38/59 | 38/55    47/59 | 46/50    79/59 | 80/51
+//   f16, 128   54/82 | 61/75    67/81 | 81/84    89/82 | 102/76   147/83 | 188/78
+//   Q8_0, 64   35/83 | 35/72    42/83 | 43/76    52/83 | 53/72    89/83 | 94/72
+//   Q8_0, 128  53/165 | 55/138  67/167 | 72/150  85/172 | 91/142  147/185 | 169/149
+//   Q4_0, 128  54/140 | 54/128  68/141 | 73/137  86/141 | 93/127  150/149 | 175/128
 // 16 sequences of 4096, 2 | 4 heads of 256:
 //   rows           32               48              80                96
-//   f16, 256   42/57 | 73/77    52/57 | 95/77   72/59 | 150/77    86/60 | 180/79
-//   Q8_0, 256  39/88 | 70/171   49/88 | 91/176  68/90 | 143/185   82/91 | 171/189
+//   f16, 256   33/57 | 62/77    45/57 | 84/76   69/58 | 128/78    79/60 | 152/79
+//   Q8_0, 256  31/89 | 58/170   42/88 | 79/175  62/90 | 120/184   73/91 | 141/189
 int few_rows(int fmt, int head_dim) { return fmt == LQ_FMT_F16 ? 48 : (head_dim == 256 ? 96 : 80); }
 
 template <int FMT>

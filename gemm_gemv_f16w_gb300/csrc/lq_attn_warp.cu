@@ -29,19 +29,20 @@
 // barrier between warps until a unit ends, 150 to 200 KB in flight an SM; a
 // page is looked up 16 keys at a time, 32 tiles ahead. The tiles of all units
 // are dealt in equal contiguous ranges to one CTA an SM, whatever the batch's
-// lengths: a CTA whose range covers a whole unit writes its rows, others leave
-// partial sums (M, l, o), and the last one to arrive joins them in the order
-// of the keys.
+// lengths (a unit's start counted as tiles): a CTA whose range covers a whole
+// unit writes its rows, others leave partial sums (M, l, o), and the last one
+// to arrive joins them in the order of the keys.
 //
 // What bounds it. Every key and value is read once for all rows that share it,
 // so HBM is the floor. f16: 64 sequences of 8192 positions, 8 heads of 128,
-// take 196 us (5.84 TB/s, 87 % of a copy); one of 131071, 2 heads of 256, 61 us
+// take 340 us (6.33 TB/s, 94 % of a copy); one of 131071, 2 heads of 256, 61 us
 // (4.43 TB/s: 27 tiles a warp, of whose time a fifth is start and join). Q8_0:
-// the same batch with mixed lengths 152 us (4.01 TB/s), bound by issue: 57 % of
-// the schedulers' cycles, waiting on the MMAs' and conversions' fixed latency
-// for the rest, at the 12 warps that registers and stages allow. Q4_0 has half
-// the bytes and the same work: 148 us. One token over 513 positions takes 9.6
-// us: launch, page lookup, one round of loads, the join of the warps.
+// the same batch with mixed lengths up to 8192 131 us (4.65 TB/s, 69 %), bound
+// by issue: the MMAs' and conversions' instructions and their fixed latency, at
+// the 12 warps that registers and stages allow. Q4_0 has half the bytes and the
+// same work: 131 us. Four tokens of 16 sequences of up to 6000, Q4_0: 50 us. One
+// token over 513 positions takes 9.6 us: launch, page lookup, one round of
+// loads, the join of the warps.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -103,6 +104,11 @@ struct Geo {
   static_assert(S >= 2 && STAGE % 16 == 0 && QF % 16 == 0 && MERGE % 16 == 0);
   static constexpr int SMEM = W * S * STAGE + FIXED;
   static constexpr int SLOT = R * (D + 2);  // floats of a partial result
+  // Tiles that a unit counts for besides its own where the tiles are dealt: its start and its
+  // join. With 0 | 8 | 16 | 32 | 48 | 64, us: the step of 64 sequences of up to 8192, Q8_0, heads
+  // of 128, 153 | 149 | 142 | 132 | 134 | 137; of up to 4096, f16, heads of 64, 70 | 65 | 62 | 56 |
+  // 56 | 57; 16 of up to 2000, Q8_0, 2 heads of 256, 23 | 18 | 17 | 17 | 19 | 19.
+  static constexpr int START = D == 256 ? 16 : 32;
   static constexpr bool QREG = NR * D <= 128 && W <= 8;  // query fragments in registers
 };
 
@@ -270,7 +276,7 @@ struct Piece {
 template <int FMT, int D, int NR>
 __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(const WarpParams P) {
   using G = Geo<FMT, D, NR>;
-  constexpr int W = G::W, TPS = G::TPS, S = G::S, R = G::R, NB = D / 32;
+  constexpr int W = G::W, TPS = G::TPS, S = G::S, R = G::R, NB = D / 32, START = G::START;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* const merge_at = smem + W * S * G::STAGE;
   float* const merge = reinterpret_cast<float*>(merge_at);
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 
   // ---- this CTA's share of all tiles ----------------------------------------
   struct Cost {
-    long long tiles;  // of a sequence, all heads and row tiles
+    long long tiles;  // of a sequence, all heads and row tiles, with START more a unit
     int units, n;     // its units, and their tiles each
   };
   auto cost = [&](int i) {
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     if (rows == 0 || (P.small_rows && rows > P.small_rows)) return c;
     c.units = (rows + R - 1) / R * H;
     c.n = tiles_of(s, a.window, a.sinks).n;
-    c.tiles = static_cast<long long>(c.units) * c.n;
+    c.tiles = static_cast<long long>(c.units) * (c.n + START);
     return c;
   };
   // inclusive sums over the block's threads, and the block's total in scan[W]
@@ -344,9 +350,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   if (whole_units) {
     if (blockIdx.x >= units) return;
     if (blockIdx.x >= unit_incl - first.units && blockIdx.x < unit_incl) {
-      const long long within = (blockIdx.x - (unit_incl - first.units)) * first.n;
+      const long long within = (blockIdx.x - (unit_incl - first.units)) * (first.n + START);
       scan[W + 2] = first_incl - first.tiles + within;
-      scan[W + 3] = first.n;
+      scan[W + 3] = first.n + START;
     }
     __syncthreads();
     x0 = scan[W + 2];
@@ -385,10 +391,13 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   };
   enter(static_cast<int>(scan[W]));
   {
-    const long long off = scan[W + 1], unit = kv::quotient(off, pc.t.n);
+    const long long off = scan[W + 1], unit = kv::quotient(off, pc.t.n + START);
+    const int at = static_cast<int>(off - unit * (pc.t.n + START));
+    x0 += max(START - at, 0);  // the place of its first tile
+    if (x0 >= x1) return;      // the start alone is here: the next CTA's
     pc.h = static_cast<int>(kv::quotient(unit, pc.row_tiles));
     pc.rt = static_cast<int>(unit - static_cast<long long>(pc.h) * pc.row_tiles);
-    pc.k0 = static_cast<int>(off - unit * pc.t.n);
+    pc.k0 = max(at - START, 0);
     pc.k1 = static_cast<int>(min(static_cast<long long>(pc.t.n), pc.k0 + (x1 - x0)));
   }
 
@@ -862,7 +871,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 
     // ---- the next piece's copies start before this one is joined -----------------
     const Piece done = pc;
-    x0 += done.k1 - done.k0;
+    x0 += done.k1 - done.k0 + START;
     const bool more = x0 < x1;
     if (more) {
       pc.k0 = 0;
@@ -975,7 +984,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       if (tid < d_rows) finish_lse(tid, row_m[tid], row_l[tid]);
     } else {
       // partial sums: the unit's CTAs are c0 .. c1, c0's slot 2 c0 + 1, the others' 2 c
-      const long long unit_x0 = x0 - done.k1, unit_x1 = unit_x0 + done.t.n - 1;
+      const long long unit_x0 = x0 - START - done.k1, unit_x1 = unit_x0 + done.t.n - 1;
       const int c0 = static_cast<int>(kv::quotient(unit_x0, per)), parts = static_cast<int>(kv::quotient(unit_x1, per)) - c0 + 1;
       auto slot_of = [&](int q) { return q == 0 ? 2 * c0 + 1 : 2 * (c0 + q); };
       auto part_at = [&](int slot) { return P.parts + static_cast<long long>(slot) * G::SLOT; };
