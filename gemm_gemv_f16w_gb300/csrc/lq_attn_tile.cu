@@ -150,6 +150,7 @@ struct TileInfo {
   int j0;                     // first key
   uint32_t flags;
   int p1, begin, sink_end;    // keys that rows of the unit see: [begin, p1] and [0, sink_end)
+  int ends;                   // the unit that ends with this tile here; -1: it goes on
   // where the rows of each group of 16 keys begin: f16 their row of the pool,
   // quantised the byte offsets of codes and scales (2 entries a group); -1: nowhere
   alignas(16) long long at[8];
@@ -1314,14 +1315,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = j0 + lane * 16;
         const int page = lane < KT / 16 ? kv::page_of(a.c, a.b, w.i, key) : -1;
         const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0);
-        // A slot is free when every softmax thread is done with its tile: so when
-        // the loaders have filled the tile four on (its V took the place of one
-        // whose PV came after that).
+        // A slot is free when every softmax thread is done with its tile. Within a
+        // unit that is when the loaders have filled the tile four on: its V took the
+        // place of a unit of the ring whose reader came after the next tile's PV,
+        // and so after that tile's weights. A unit's last tile has no next one, and
+        // the units that follow may leave the second row tile's group without one:
+        // there the whole unit has to be done. (Not so for its other tiles: its last
+        // PV may wait for the next unit's first keys.)
         if (tile >= kInfo / 2) {
           alive = wait(&bar->done[(tile - kInfo / 2) % kInfo], ((tile - kInfo / 2) / kInfo) & 1u);
           if (!alive) break;
         }
         TileInfo& ti = bar->info[tile % kInfo];
+        if (tile >= kInfo) {
+          const uint32_t ended = static_cast<uint32_t>(ti.ends);
+          if (ti.ends >= 0) alive = wait(&bar->unit_free[ended % kUnits], (ended / kUnits) & 1u);
+          if (!alive) break;
+          __syncwarp();  // every lane has read it
+        }
         if (lane < KT / 16) {
           const int slot = key % a.c.page_size;
           if constexpr (!QUANT) {
@@ -1344,6 +1355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ti.p1 = w.p1;
           ti.begin = w.begin;
           ti.sink_end = w.sink_end;
+          ti.ends = k + 1 == w.k1 ? static_cast<int>(un) - 1 : -1;
           *reinterpret_cast<uint4*>(bar->bad[tile % kInfo]) = make_uint4(0u, 0u, 0u, 0u);
         }
         __syncwarp();
