@@ -1083,8 +1083,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     wait_copies<0>();
     if (pend) report();
-    // a warp that gives up lets the copy engine finish first
-    if (!in_time && warp == 8) {
+    // The copy engine finishes before this warp leaves, whether or not a wait of its
+    // own has run out: the MMA warp may have given up on the last units, and nothing
+    // may land once the CTA is gone. (They have landed where all went well.)
+    if (warp == 8) {
       for (uint32_t i = 0; i < NU; ++i) {
         const uint32_t u = unit - 1 - i;  // the units before `unit` were issued
         if ((boxed >> i) & 1u) mbar_wait(&bar->full[u % NU], (u / NU) & 1u, kDrainWaitNs);

@@ -18,6 +18,11 @@ Checked: what a softmax group reads from a slot is its own tile's, and the run
 ends. Planted mistakes: a slot rewritten by the loaders' progress alone, which
 orders nothing for a group whose next units have no rows for it; and a wait for
 every tile of an earlier unit, whose last PV waits for the next unit's keys.
+
+Where waits may run out at any time (a wait limit of one poll), the CTA ends
+without a copy or an MMA of its own in flight: the MMA thread and the loaders see
+theirs complete before they leave. Planted mistake: loaders that do so only when a
+wait of their own has run out.
 """
 import random
 
@@ -27,11 +32,13 @@ SLOTS, UNIT_SLOTS = 8, 8
 
 
 class Model:
-    """units: (key tiles, row tiles) of each unit; nu: ring units."""
+    """units: (key tiles, row tiles) of each unit; nu: ring units; gives_up:
+    how likely a wait that is looked at runs out; drains: whether the loaders
+    see their copies land before they leave, or only after giving up."""
 
-    def __init__(self, units, nu, seed, unit_wait="last tile"):
+    def __init__(self, units, nu, seed, unit_wait="last tile", gives_up=0.0, drains="always"):
         self.rng = random.Random(seed)
-        self.units, self.nu, self.unit_wait = units, nu, unit_wait
+        self.units, self.nu, self.unit_wait, self.gives_up, self.drains = units, nu, unit_wait, gives_up, drains
         self.tiles = [u for u, (n, _) in enumerate(units) for _ in range(n)]
         self.firsts = [i == 0 or self.tiles[i - 1] != u for i, u in enumerate(self.tiles)]
         self.slot = [None] * SLOTS
@@ -131,6 +138,13 @@ class Model:
             yield None
             self.free[u][q] = 1
 
+    def leave(self, role, gave_up):
+        """What a role does before it leaves, with waits that do not run out."""
+        if role == "mma":
+            yield lambda: not self.mmas
+        if role == "loader" and (gave_up or self.drains == "always"):
+            yield lambda: not self.copies
+
     def read(self, q, tile, what):
         if self.slot[tile % SLOTS] != tile:
             self.issues.append(f"group {q} reads the {what} of tile {self.slot[tile % SLOTS]} for tile {tile}")
@@ -138,15 +152,20 @@ class Model:
     def run(self):
         rng, waits = self.rng, {r: None for r in self.roles}
         weight = {r: 1.0 for r in self.roles}
+        leaving = set()
         for _ in range(200000):
+            if not self.roles:
+                return "in flight" if self.copies or self.mmas else "end"
             ready = [r for r in self.roles if waits[r] is None or waits[r]()]
-            acts = ready + ["copy"] * bool(self.copies) + ["mmas"] * bool(self.mmas)
+            late = [r for r in self.roles if r not in ready and r not in leaving and rng.random() < self.gives_up]
+            acts = ready + late + ["copy"] * bool(self.copies) + ["mmas"] * bool(self.mmas)
             if not acts:
-                return "end" if not self.roles else "deadlock"
+                if self.gives_up:
+                    continue
+                return "deadlock"
             if rng.random() < 0.02:  # another role stalls, or none
                 weight = {r: 1.0 for r in self.roles}
-                if self.roles:
-                    weight[rng.choice(list(self.roles))] = rng.choice([0.002, 0.1, 1.0])
+                weight[rng.choice(list(self.roles))] = rng.choice([0.002, 0.1, 1.0])
             a = rng.choices(acts, [weight.get(x, 1.0) for x in acts])[0]
             if a == "copy":  # copies land in any order
                 self.landed.add(self.copies.pop(rng.randrange(len(self.copies))))
@@ -158,9 +177,15 @@ class Model:
                         self.add(what)
             else:
                 try:
+                    if a in late:
+                        raise StopIteration
                     waits[a] = next(self.roles[a])
                 except StopIteration:
-                    del self.roles[a]
+                    if a in leaving:
+                        del self.roles[a]
+                    else:
+                        leaving.add(a)
+                        self.roles[a], waits[a] = self.leave(a, a in late), None
         return "too long"
 
 
@@ -187,3 +212,16 @@ def test_groups_read_their_own_tiles(units, nu):
 def test_planted_mistakes_are_caught(name, unit_wait, nu):
     models = (Model(UNITS[name], nu, seed, unit_wait) for seed in range(300))
     assert any(m.run() != "end" or m.issues for m in models)
+
+
+@pytest.mark.parametrize("nu", [3, 6])
+@pytest.mark.parametrize("units", [[(1, 1)], [(1, 2)], [(3, 2), (2, 1)], [(9, 2)]], ids=str)
+def test_nothing_is_in_flight_when_a_cta_gives_up(units, nu):
+    for p in (0.05, 0.5):
+        for seed in range(100):
+            assert Model(units, nu, seed, gives_up=p).run() == "end", seed
+
+
+@pytest.mark.parametrize("nu", [3, 6])
+def test_loaders_that_leave_their_copies_are_caught(nu):
+    assert any(Model([(1, 1)], nu, seed, gives_up=0.5, drains="after giving up").run() == "in flight" for seed in range(100))
