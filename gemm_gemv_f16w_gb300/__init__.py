@@ -313,15 +313,19 @@ class KVCache:
         need = int(lib().lq_kv_pool_bytes(code, int(num_pages), int(page_size), int(kv_heads), int(head_dim)))
         if need == 0 and num_pages != 0:
             raise LQError(LQ_ERR_INVALID_ARG, "lq_kv_pool_bytes")
-        pools = []
+        pools, where = [], set()
         for pool in (k, v):
             if pool is None:
                 import torch
                 pool = torch.zeros(need, dtype=torch.uint8, device=device or "cuda")
-            elif not isinstance(pool, int) and (not pool.is_contiguous() or pool.numel() * pool.element_size() < need):
-                raise LQError(LQ_ERR_INVALID_ARG, f"KVCache: a pool of {need} contiguous bytes is needed")
+            if not isinstance(pool, int):
+                where.add(pool.get_device())
+                if not pool.is_contiguous() or pool.numel() * pool.element_size() < need or min(where) < 0 or len(where) > 1:
+                    raise LQError(LQ_ERR_INVALID_ARG, f"KVCache: pools of {need} contiguous bytes on one GPU are needed")
             pools.append(pool)
         self.k, self.v = pools
+        self.gpu = where.pop() if where else None  # None: addresses, the caller's affair
+        self.work_bytes = 0                        # what lq_attn_paged needs, once it is known
         self.struct = KVCacheStruct(code, int(page_size), int(kv_heads), int(head_dim), int(num_pages),
                                     _ptr(self.k), _ptr(self.v))
         self.ref = ctypes.byref(self.struct)
@@ -333,21 +337,33 @@ class KVBatch:
     [batch, max_pages], kv_len [batch] and q_start [batch + 1]."""
 
     def __init__(self, page_table, kv_len, q_start, tokens, max_q=0):
+        self.gpu = page_table.get_device()
         for x, shape in ((page_table, None), (kv_len, (page_table.shape[0],)), (q_start, (page_table.shape[0] + 1,))):
-            if str(x.dtype) != "torch.int32" or not x.is_contiguous() or (shape and tuple(x.shape) != shape):
+            if str(x.dtype) != "torch.int32" or not x.is_contiguous() or len(x.shape) != (1 if shape else 2) \
+                    or (shape and tuple(x.shape) != shape) or x.get_device() != self.gpu:
                 raise LQError(LQ_ERR_INVALID_ARG, "KVBatch: contiguous int32 page_table [batch, max_pages], kv_len [batch] "
-                                                  "and q_start [batch + 1]")
+                                                  "and q_start [batch + 1] on one device")
         self.page_table, self.kv_len, self.q_start, self.tokens = page_table, kv_len, q_start, int(tokens)
         self.struct = KVBatchStruct(page_table.shape[0], page_table.shape[1], int(tokens), int(max_q), _ptr(page_table),
                                     _ptr(kv_len), _ptr(q_start))
         self.ref = ctypes.byref(self.struct)
 
 
-def _rows(x, tokens, width, what):
+def _elsewhere(cache, batch, what):
+    """The cache's pools and the batch's tables have no GPU in common (pools
+    given as addresses are taken to be on the batch's)."""
+    if batch.gpu < 0 or cache.gpu is not None:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: the cache and the batch's tensors have to be on the same GPU")
+
+
+def _rows(x, batch, width, what):
     """(address, leading dimension) of f32 rows [tokens, heads, head_dim] or
     [tokens, heads * head_dim]; a raw address is taken as tightly packed."""
     if x is None or isinstance(x, int):
         return x or 0, width
+    tokens = batch.tokens
+    if x.get_device() != batch.gpu:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: a tensor on {x.device} with a batch of another device")
     shape, strides = x.shape, x.stride()
     rank, rows = len(shape), shape[0]
     ok = rows >= tokens and strides[-1] == 1 and x.dtype.itemsize == 4 and x.is_floating_point()
@@ -378,8 +394,10 @@ def _current_stream() -> int:
 def lq_kv_write(cache, batch, K, V, stream=None) -> None:
     """Stores the batch's tokens in the cache; K, V: float32 [tokens,
     kv_heads, head_dim] (token-strided slices allowed). See include/lq.h."""
-    k, ldk = _rows(K, batch.tokens, cache.width, "lq_kv_write")
-    v, ldv = _rows(V, batch.tokens, cache.width, "lq_kv_write")
+    if cache.gpu != batch.gpu:
+        _elsewhere(cache, batch, "lq_kv_write")
+    k, ldk = _rows(K, batch, cache.width, "lq_kv_write")
+    v, ldv = _rows(V, batch, cache.width, "lq_kv_write")
     st = (_lib or lib()).lq_kv_write(cache.ref, batch.ref, k, ldk, v, ldv, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "lq_kv_write")
@@ -388,8 +406,10 @@ def lq_kv_write(cache, batch, K, V, stream=None) -> None:
 def lq_kv_read(cache, batch, K, V, stream=None) -> None:
     """Reads the batch's tokens back as float32 into K and V (either may be
     None). See include/lq.h."""
-    k, ldk = _rows(K, batch.tokens, cache.width, "lq_kv_read")
-    v, ldv = _rows(V, batch.tokens, cache.width, "lq_kv_read")
+    if cache.gpu != batch.gpu:
+        _elsewhere(cache, batch, "lq_kv_read")
+    k, ldk = _rows(K, batch, cache.width, "lq_kv_read")
+    v, ldv = _rows(V, batch, cache.width, "lq_kv_read")
     st = (_lib or lib()).lq_kv_read(cache.ref, batch.ref, k, ldk, v, ldv, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "lq_kv_read")
@@ -408,8 +428,11 @@ def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=N
     """Attention of the batch's tokens (Q, O: float32 [tokens, heads,
     head_dim]) over the cache, causal, with an optional sliding window and
     sinks; lse: float32 [tokens, heads] or None; work: attn_work(...), which a
-    program keeps (None makes one for this call). ``heads`` is needed where Q
-    is not a three-dimensional tensor. See include/lq.h."""
+    program keeps (None makes one for this call); a buffer made for a cache of
+    other heads is refused if it is smaller than this one's. ``heads`` is
+    needed where Q is not a three-dimensional tensor. See include/lq.h."""
+    if cache.gpu != batch.gpu:
+        _elsewhere(cache, batch, "lq_attn_paged")
     D = cache.head_dim
     if heads is None:
         heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // D
@@ -417,10 +440,19 @@ def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=N
         if stream is not None:
             raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: a call on a stream of its own brings its work buffer")
         work = attn_work(cache, batch, heads)
-    q, ldq = _rows(Q, batch.tokens, heads * D, "lq_attn_paged")
-    o, ldo = _rows(O, batch.tokens, heads * D, "lq_attn_paged")
-    if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()):
-        raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: lse is a contiguous float32 [tokens, heads]")
+    elif not isinstance(work, int):
+        need = cache.work_bytes
+        if need == 0:  # (0 for arguments that the call itself refuses)
+            need = cache.work_bytes = int(lib().lq_attn_work_bytes(cache.ref, batch.ref, cache.struct.kv_heads))
+        if work.numel() * work.element_size() < need or not work.is_contiguous() or work.get_device() != batch.gpu:
+            raise LQError(LQ_ERR_INVALID_ARG, f"lq_attn_paged: a work buffer of {need} contiguous bytes on the batch's GPU is "
+                                              "needed (attn_work)")
+    q, ldq = _rows(Q, batch, heads * D, "lq_attn_paged")
+    o, ldo = _rows(O, batch, heads * D, "lq_attn_paged")
+    if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()
+                                                         or lse.dtype.itemsize != 4 or not lse.is_floating_point()
+                                                         or lse.get_device() != batch.gpu):
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: lse is a contiguous float32 [tokens, heads] on the batch's GPU")
     st = (_lib or lib()).lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, _ptr(lse), heads, scale, window, sinks, _ptr(work),
                                        _current_stream() if stream is None else _stream(stream))
     if st:

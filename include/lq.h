@@ -397,9 +397,12 @@ lq_status lq_kv_read(const lq_kv_cache* cache, const lq_kv_batch* batch, float* 
  *     over parts of a context can be joined.
  *   work: lq_attn_work_bytes(...) bytes of DEVICE memory, 16-byte aligned,
  *     zero-filled before its first use; each call leaves it ready for the
- *     next. It depends on the geometry alone, not on lengths, serves one
- *     call at a time and may be shared by calls on one stream (after a
- *     LQ_ERR_DEVICE_TIMEOUT it has to be zero-filled again).
+ *     next. The size depends on the cache's geometry alone, not on lengths,
+ *     and cannot be checked by the call: a buffer serves every geometry whose
+ *     lq_attn_work_bytes is no larger (head_dim decides: 128 and 256 need
+ *     twice what 64 does), one call at a time, and may be shared by calls on
+ *     one stream (after a LQ_ERR_DEVICE_TIMEOUT it has to be zero-filled
+ *     again).
  * Every product is exact to f32's precision: f16 operands in two parts with
  * f32 accumulation on the tensor cores, softmax and sums in f32; the result
  * is within 2e-5 of the 64-bit one (2-norms) for logits of ordinary size.
