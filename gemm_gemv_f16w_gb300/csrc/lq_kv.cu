@@ -92,16 +92,17 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
     float top = mine;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float m = top;
-    if constexpr (FMT == LQ_FMT_Q4_0) {
-      // the first element of the largest magnitude gives the scale its sign
-      const unsigned holders = __ballot_sync(0xffffffffu, mine == top) >> (lane & 24);
+    // the block's first element of at least this magnitude (the whole warp asks)
+    auto first_of = [&](float size) {
+      const unsigned holders = __ballot_sync(0xffffffffu, mine >= size) >> (lane & 24);
       const int first = __ffs(static_cast<int>(holders & 0xFFu)) - 1;
       float own = x[3];
 #pragma unroll
-      for (int j = 2; j >= 0; --j) own = fabsf(x[j]) == mine ? x[j] : own;
-      m = __shfl_sync(0xffffffffu, own, (lane & 24) + first);
-    }
+      for (int j = 2; j >= 0; --j) own = fabsf(x[j]) >= size ? x[j] : own;
+      return __shfl_sync(0xffffffffu, own, (lane & 24) + first);
+    };
+    float m = top;
+    if constexpr (FMT == LQ_FMT_Q4_0) m = first_of(top);  // the largest gives the scale its sign
     // q = m / 127, or m / -8 (exact)
     constexpr float kBy127 = 1.0f / 127.0f;
     float d = m * -0.125f;
@@ -126,6 +127,8 @@ __device__ __forceinline__ void put(const float4& x4, int e, unsigned char* row,
     if (__any_sync(0xffffffffu, !plain)) {  // by the definition's own divisions
       // a NaN in the block: of its eight lanes, any
       bad = ((__ballot_sync(0xffffffffu, x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3]) >> (lane & 24)) & 0xFFu) != 0u;
+      // of several values beyond the range the first counts: once clamped they are equal
+      if constexpr (FMT == LQ_FMT_Q4_0) m = first_of(fminf(top, 65504.0f));
       d = FMT == LQ_FMT_Q8_0 ? __fdiv_rn(fminf(top, 65504.0f), 127.0f) : __fdiv_rn(clamped(m), -8.0f);
       word = 0;
 #pragma unroll
