@@ -87,6 +87,7 @@ constexpr int kUnits = 8;           // units of bookkeeping kept
 constexpr int kMaxBatch = 4096;     // sequences whose totals fit in shared memory
 constexpr float kNoMax = -1e30f;    // M before the first key
 constexpr float kLift = 11.0f;
+constexpr float kLarge = 65536.0f;  // maxima from here on: logits are rounded before M is taken off
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -658,20 +659,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         top = top == -INFINITY ? top : top * f;
         float keep = 1.0f;
-        if (top > M + 15.0f) {
-          const float to = fmaxf(M, top - kLift);
+        if (top - M > 15.0f) {  // (exact between neighbours, which M + 15 need not be)
+          float to = fmaxf(M, top - kLift);
+          to = top - to > 15.0f ? top : to;  // past 2^27 the step itself is 16
           keep = ex2(M - to);
           M = to;
           l *= keep;
         }
-        // weights, in two parts, over the logits: 16 columns a 16 keys
+        // Weights, in two parts, over the logits: 16 columns a 16 keys. s f - M in one
+        // step saves the rounding of s f, but M comes from the rounded product of the
+        // largest s: where that rounding counts (past 2^24 it can be an exponent and
+        // more, and weights would leave f16's range) every product is rounded. (By
+        // scalar multiplications: packed ones are merged with the addition after all.)
+        const bool large = __any_sync(0xffffffffu, fabsf(M) >= kLarge);
         const float2 ff = make_float2(f, f), mm = make_float2(-M, -M), minus = make_float2(-1.0f, -1.0f);
         float2 l2 = make_float2(0.0f, 0.0f);
-        auto weights = [&](int j, uint32_t (&s)[16], uint32_t vis, bool masked) {
+        auto weights = [&](int j, uint32_t (&s)[16], uint32_t vis, bool masked, bool rounded) {
           uint32_t w16[16];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float2 x = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, mm);
+            const float2 raw = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            const float2 x = rounded ? fadd2(make_float2(__fmul_rn(raw.x, f), __fmul_rn(raw.y, f)), mm) : ffma2(raw, ff, mm);
             float2 p = make_float2(ex2(x.x), ex2(x.y));
             if (masked) {
               p.x = (vis >> i) & 1u ? p.x : 0.0f;
@@ -686,10 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(p_at + j, w16);
         };
         const int from = ONE ? half * (KT / 2) : 0, to = ONE ? from + KT / 2 : KT;
-        if (!edge) {
-          each([&](int j, uint32_t (&s)[16], uint32_t) { weights(j, s, 0u, false); }, false, from, to);
+        if (large) {
+          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true, true); }, true, from, to);
+        } else if (!edge) {
+          each([&](int j, uint32_t (&s)[16], uint32_t) { weights(j, s, 0u, false, false); }, false, from, to);
         } else {
-          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true); }, true, from, to);
+          each([&](int j, uint32_t (&s)[16], uint32_t vis) { weights(j, s, vis, true, false); }, true, from, to);
         }
         l += l2.x + l2.y;
         tc::wait_st();

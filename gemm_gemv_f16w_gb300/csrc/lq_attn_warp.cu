@@ -714,10 +714,13 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           const float2 y = FMT == LQ_FMT_F16 ? x[n][nt] : fadd2(x[n][nt], ld[nt]);
           top = fmaxf(top, fmaxf(y.x, y.y));
         }
-        if (__any_sync(0xffffffffu, top > M[n] + 15.0f)) {
+        // (a difference of neighbours is exact, M + 15 need not be)
+        if (__any_sync(0xffffffffu, top - M[n] > 15.0f)) {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float to = fmaxf(M[n], top - kLift), keep = ex2(M[n] - to);
+          float to = fmaxf(M[n], top - kLift);
+          to = top - to > 15.0f ? top : to;  // past 2^27 the step itself is 16
+          const float keep = ex2(M[n] - to);
           M[n] = to;
           l[n] = fmul2(l[n], make_float2(keep, keep));
 #pragma unroll
