@@ -85,7 +85,7 @@ constexpr int kMinTiles = 4;
 constexpr int kInfo = 8;            // tiles of bookkeeping kept
 constexpr int kUnits = 8;           // units of bookkeeping kept
 constexpr int kMaxBatch = 4096;     // sequences whose totals fit in shared memory
-constexpr float kNoMax = -1e30f;    // M before the first key
+constexpr float kNoMax = -3.402823466e38f;  // M before the first key: no finite logit is lower
 constexpr float kLift = 11.0f;
 constexpr float kLarge = 65536.0f;  // maxima from here on: logits are rounded before M is taken off
 constexpr float kLog2e = 1.4426950408889634f;

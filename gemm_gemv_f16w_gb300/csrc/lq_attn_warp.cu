@@ -60,7 +60,7 @@ constexpr int kTile = 16;            // keys of a tile: never crosses a page
 // positions, 8 heads of 128: 8: 16.2 | 15.6 us, 16: 12.8 | 16.5, 32: 14.8 | 15.5.
 constexpr int kMinTiles = 16;
 constexpr int kJoin = 8;              // partial results that one CTA joins at once
-constexpr float kNoMax = -1e30f;     // M before the first key
+constexpr float kNoMax = -3.402823466e38f;  // M before the first key: no finite logit is lower
 constexpr float kLift = 11.0f;       // how far M stays below the maximum
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

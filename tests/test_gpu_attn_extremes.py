@@ -10,7 +10,7 @@ from test_gpu_attn import FMTS, ROUTES, _run
 pytestmark = pytest.mark.gpu
 
 # past 2^24 a step of float32 is more than one, past 2^27 (base 2) more than 15
-SIZES = (0.0, 3.0, 1e5, 2.0**24, 3.1e7, 6.1e7, 9.9e7, 1.5e8, 1.8e8, 3e8, 1e12, 1e20, 3e29)
+SIZES = (0.0, 3.0, 1e5, 2.0**24, 3.1e7, 6.1e7, 9.9e7, 1.5e8, 1.8e8, 3e8, 1e12, 1e20, 8e29, 3e30, 1e35, 1e38)
 
 
 def _rows(lq, fmt, d, dev, keys, seed, page=16):
