@@ -117,19 +117,25 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
     part[warp][kMaxDim] = any ? m : -INFINITY;
     part[warp][kMaxDim + 1] = l;
   }
-  const bool seen = __syncthreads_or(any ? 1 : 0) != 0;
+  const bool seen = __syncthreads_or(any ? 1 : 0) != 0;  // (if not, the sum is zero)
   float top = -INFINITY, sum = 0.0f;
   for (int w = 0; w < kGWarps; ++w) top = fmaxf(top, part[w][kMaxDim]);
   const float base = top == -INFINITY ? 0.0f : top;
   for (int w = 0; w < kGWarps; ++w) sum += part[w][kMaxDim + 1] * expf(part[w][kMaxDim] - base);
+  if (sum == 0.0f && seen) {  // nothing but logits of -inf: zeros, unless a query that is not finite made them
+#pragma unroll
+    for (int b = 0; b < kMaxDim / 32; ++b)
+      if (b < blocks) sum += qrow[b * 32 + lane] * 0.0f;
+    sum = warp_sum(sum);
+  }
   float* orow = a.O + t * a.ldo + static_cast<long long>(h) * D;
   for (int d = threadIdx.x; d < D; d += kGWarps * 32) {
     float o = 0.0f;
     for (int w = 0; w < kGWarps; ++w) o += part[w][d] * expf(part[w][kMaxDim] - base);
-    if (LQ_IN_BOUNDS(t < a.b.tokens && h < a.heads)) orow[d] = seen ? o / sum : 0.0f;
+    if (LQ_IN_BOUNDS(t < a.b.tokens && h < a.heads)) orow[d] = sum == 0.0f ? 0.0f : o / sum;
   }
   if (a.lse && threadIdx.x == 0)
-    a.lse[static_cast<long long>(t) * a.heads + h] = seen ? base + logf(sum) : -INFINITY;
+    a.lse[static_cast<long long>(t) * a.heads + h] = sum == 0.0f ? -INFINITY : base + logf(sum);
 }
 
 }  // namespace

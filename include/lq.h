@@ -390,8 +390,12 @@ lq_status lq_kv_read(const lq_kv_cache* cache, const lq_kv_batch* batch, float* 
  * or j < sinks (the last `window` positions, itself among them, and the
  * first `sinks`). window == 0: no window, sinks has no effect. The new
  * tokens' own keys and values are read from the cache (lq_kv_write first).
- * A row that sees nothing gets zeros, and -inf in lse. Invisible keys have
- * no influence, NaN and infinities among them included.
+ * A row that sees nothing gets zeros, and -inf in lse; so does one whose
+ * logits are all -inf, beyond f32's range. A logit of +inf and a query that is
+ * not finite make their rows NaN. Invisible keys have no influence, NaN and
+ * infinities among them included; a visible NaN makes NaN of what it takes
+ * part in. An infinity in the pools (lq_kv_write stores none) may do so too,
+ * where the formula would give an infinity or no weight.
  *   lse (NULL or tokens * heads floats, row t at lse + t * heads): the
  *     natural logarithm of the sum of exp(scale * Q . k), by which results
  *     over parts of a context can be joined.

@@ -1,5 +1,5 @@
 """lq_attn_paged far from ordinary logits: every kernel gives the formula's
-result for any finite logit."""
+result for any finite logit, and the stated one where there is none."""
 import numpy as np
 import pytest
 
@@ -88,3 +88,53 @@ def test_one_key_above_all_others(lq, cuda_dev, route, fmt, d, order):
         compare(o[i], np.broadcast_to(v, o[i].shape), np.broadcast_to(2.0**-17 * np.abs(v) + 1e-37, o[i].shape), f"logit {aim:.3g}")
         checked += 1
     assert checked >= len(aims) - 8
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_logits_beyond_float32(lq, cuda_dev, route, fmt, d):
+    """A logit of +inf makes its row NaN, one of -inf has no weight; rows that
+    see nothing but such logits get zeros and -inf, as if they saw nothing."""
+    P = Paged(lq, fmt, [1] * 4, [40, 40, 40, 7], 2, 1, d, 16, cuda_dev, seed=34)
+    for i in range(4):
+        P.k[i][:] = P.k[i][:1]
+        if i == 2:
+            P.k[i][35] *= np.float32(1e-3)
+        P.store(0, i, P.k[i])
+        k = P.values(0, i)[0, 0].astype(np.float64)
+        big = 4e38 * np.sqrt(d) / (k @ k) * k  # scale q . k is 4e38
+        assert np.abs(big).max() < 3e38
+        P.q[i] = (big if i == 0 else -big).astype(np.float32)
+    o, lse = _run(lq, P, route=route)
+    assert np.isnan(o[0]).all() and not np.isfinite(lse[0]).any()
+    for i in (1, 3):
+        assert (o[i] == 0).all() and (lse[i] == -np.inf).all()
+    v = P.values(1, 2)[35, 0].astype(np.float64)
+    compare(o[2], np.broadcast_to(v, o[2].shape), np.broadcast_to(2.0**-17 * np.abs(v), o[2].shape), "the finite logit")
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+def test_queries_that_are_not_finite(lq, cuda_dev, route, fmt, what):
+    """Their own rows become NaN, no others; a row that sees nothing stays
+    zero whatever its query."""
+    P = Paged(lq, fmt, [3, 2, 1], [77, 2, 1], 2, 1, 128, 16, cuda_dev, seed=35)
+    P.k[0][:, :, 9] = np.abs(P.k[0][:, :, 9]) + 0.5  # every logit of that dim alone has the query's sign
+    P.store(0, 0, P.k[0])
+    table = P.table.copy()
+    table[2, 0] = -1
+    P.q[1, 1, 9] = what
+    P.q[2, 0, 100] = what
+    P.q[5, 1, 3] = what
+    Q = P.q.copy()
+    P.q[[1, 2, 5], [1, 0, 1]] = 0
+    want, tol, wl, ltol = P.expect(table=table)
+    o, lse = _run(lq, P, route=route, table=table, q=Q)
+    bad = np.zeros((6, 2), bool)
+    bad[1, 1] = bad[2, 0] = True
+    assert np.isnan(o[bad]).all() and np.isnan(lse[bad]).all()
+    compare(o[~bad], want[~bad], tol[~bad], "the other rows")
+    compare(lse[~bad], wl[~bad], ltol[~bad], "the other rows' lse")
+    assert (o[5] == 0).all() and (lse[5] == -np.inf).all()
