@@ -126,3 +126,31 @@ def test_cache_of_many_sequences(lq, cuda_dev, fmt, n):
                 P.store(w, i, x[i][t - m:], first=t - m)
     assert np.array_equal(cache.k.cpu().numpy(), P.pools[0]) and np.array_equal(cache.v.cpu().numpy(), P.pools[1])
     assert lq.last_device_error() == lq.LQ_OK
+
+
+@pytest.mark.parametrize("fmt,d", [("f16", 256), ("q8_0", 128), ("q4_0", 64)])
+def test_pools_beyond_32_bits(lq, cuda_dev, fmt, d):
+    """Pools of more than 4 GiB a side, a sequence on their last pages and one
+    that alternates between both ends: the same bits as from a small pool."""
+    page, kv_heads, heads = 64, 2, 4
+    P = Paged(lq, fmt, [3, 90], [200, 333], heads, kv_heads, d, page, cuda_dev, seed=d)
+    small = P.cache()
+    pages = (1 << 32) // (P.block * kv_heads) + 70
+    big = lq.KVCache(fmt, pages, page, kv_heads, d, device=cuda_dev)
+    used = P.table[P.table >= 0]
+    moved = {int(p): pages - 1 - n if n % 3 else n for n, p in enumerate(used)}
+    table = np.vectorize(lambda p: moved.get(int(p), -1))(P.table).astype(np.int32)
+    assert (big.k.numel() > 1 << 32) and table.max() == pages - 2
+    for a, b in ((small.k, big.k), (small.v, big.v)):
+        for p, to in moved.items():
+            b.view(pages, -1)[to] = a.view(P.pages, -1)[p]
+    for route in ROUTES:
+        P.cache = lambda: small
+        o, lse = _run(lq, P, route=route)
+        P.cache = lambda: big
+        o2, lse2 = _run(lq, P, route=route, table=table)
+        assert np.array_equal(o, o2) and np.array_equal(lse, lse2)
+    out = [torch.empty(P.tokens, kv_heads, d, device=cuda_dev) for _ in range(4)]
+    lq.lq_kv_read(small, P.batch(), *out[:2])
+    lq.lq_kv_read(big, P.batch(table=table), *out[2:])
+    assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])

@@ -138,3 +138,25 @@ def test_queries_that_are_not_finite(lq, cuda_dev, route, fmt, what):
     compare(o[~bad], want[~bad], tol[~bad], "the other rows")
     compare(lse[~bad], wl[~bad], ltol[~bad], "the other rows' lse")
     assert (o[5] == 0).all() and (lse[5] == -np.inf).all()
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_and_values_at_the_top_of_the_range(lq, cuda_dev, route, fmt, d):
+    """Elements of up to +-65504 (and clamped ones), whose blocks have the
+    largest scales that the cache holds, beside ordinary ones."""
+    P = Paged(lq, fmt, [1, 30], [140, 75], 4, 2, d, 16, cuda_dev, seed=36)
+    rng = np.random.default_rng(36)
+    for which, x in ((0, P.k), (1, P.v)):
+        for i in range(2):
+            x[i] *= np.float32(200.0)
+            at = rng.random(x[i].shape) < 0.02
+            x[i][at] = rng.choice(np.float32([65504, -65504, 65503, -65490, 1e6, -1e6, 60000, -33000]), at.sum())
+            P.store(which, i, x[i])
+    P.q *= np.float32(1e-4)
+    o, lse = _run(lq, P, route=route)
+    want, tol, wl, ltol = P.expect()
+    assert all(np.abs(P.values(w, i)).max() >= 65504 for w in (0, 1) for i in (0, 1))
+    compare(o, want, tol, "output")
+    compare(lse, wl, ltol, "lse")
