@@ -20,14 +20,18 @@
 // stay in f32: S = sum_b d_jb (q_b . code_jb) over the blocks b of 32 dims,
 // and in the value product they go to the weights, P_b = p_j d_jb (in two f16
 // parts; M then goes by x_j + log2 max_b |d_jb|, so that P <= 2^15 whatever
-// the values' size). Each step's value product starts from zero and is added
-// to the f32 sums in registers: the MMA's own accumulation truncates, which
-// over thousands of keys would show.
+// the values' size). One M for all blocks is the choice here: the parts' last
+// step is 2^-24 and the largest P at least 2^11, so that blocks whose scales
+// are 2^-k of the row's largest keep 36 - k bits of their weights. Each step's
+// value product starts from zero and is added to the f32 sums in registers: the
+// MMA's own accumulation truncates, which over thousands of keys would show.
 //
 // Split. Each warp streams its own tiles by 16-byte asynchronous copies into a
 // private ring (rows padded so that the fragment loads hit all banks), no
-// barrier between warps until a unit ends, 150 to 200 KB in flight an SM; a
-// page is looked up 16 keys at a time, 32 tiles ahead. The tiles of all units
+// barrier between warps until a unit ends; besides the steps in use the rings
+// have 64 to 128 KB on the way to an SM (f16 128, but 64 for two row groups of
+// 128 dims; quantised 90 to 108, but 68 for Q8_0 of 256 dims); a page is looked
+// up 16 keys at a time, 32 tiles ahead. The tiles of all units
 // are dealt in equal contiguous ranges to one CTA an SM, whatever the batch's
 // lengths (a unit's start counted as tiles): a CTA whose range covers a whole
 // unit writes its rows, others leave partial sums (M, l, o), and the last one

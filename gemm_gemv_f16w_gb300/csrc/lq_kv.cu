@@ -1,6 +1,6 @@
 // Writing tokens into the paged key/value cache and reading them back.
 //
-// One pass over the data: 8 bytes an element come in or go out as f32, and
+// One pass over the data: 4 bytes an element come in or go out as f32, and
 // 2 (f16), 1.0625 (Q8_0) or 0.5625 (Q4_0) as codes and scales: HBM is the
 // floor (for a decode step, the launch), and instruction issue the first
 // bound: a warp has about 40 cycles for 128 elements. A warp takes 1024
@@ -15,7 +15,7 @@
 // codes are theirs bit for bit, without a division an element: the scale
 // top / 127 comes from the rounded reciprocal by Markstein's correction (the
 // remainder top - 127 q is exact, q + remainder / 127 rounds correctly;
-// checked for every mantissa), and x / d from an approximate reciprocal, whose
+// tests/test_kv_scale_cpu.py checks every mantissa), and x / d from an approximate reciprocal, whose
 // error (3e-5 at most) cannot change a code unless x / d is within 1e-4 of a
 // half. Blocks with such an element (one in 160), with values beyond the
 // cache's range, NaNs or scales near f32's smallest take the exact divisions.
@@ -200,7 +200,7 @@ __device__ __forceinline__ float4 values4(const Four& f, int e) {
   }
 }
 
-// grid: x = groups of kKvTokens tokens, y = sides * (512-element segment) + side
+// grid: x = groups of kKvTokens tokens, y = sides * (segment of kKvGroups * 128 elements) + side
 template <int FMT, bool VEC, bool WRITE>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_kernel(const KvArgs a) {
   pdl_wait();
