@@ -41,6 +41,10 @@ constexpr int kMaxDim = 256;
 //   rows           32               48              80                96
 //   f16, 256   33/57 | 62/77    45/57 | 84/76   69/58 | 128/78    79/60 | 152/79
 //   Q8_0, 256  31/89 | 58/170   42/88 | 79/175  62/90 | 120/184   73/91 | 141/189
+// One number a format is a compromise: where the two cross also depends on the
+// head dim and on how many sequences share the SMs. f16 of 64 dims crosses at 64
+// rows (a few us given away from 49 on), and 16 sequences of Q8_0, 128 dims, would
+// gain from the warp-level kernel up to 128 rows, where one sequence loses.
 int few_rows(int fmt, int head_dim) { return fmt == LQ_FMT_F16 ? 48 : (head_dim == 256 ? 96 : 80); }
 
 template <int FMT>
@@ -58,12 +62,16 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
   const kv::Visible see = kv::visible(p, a.window, a.sinks);
 
   float q[kMaxDim / 32], acc[kMaxDim / 32];
+  bool odd = false;  // the query is not finite
   const float* qrow = a.Q + t * a.ldq + static_cast<long long>(h) * D;
 #pragma unroll
   for (int b = 0; b < kMaxDim / 32; ++b) {
-    q[b] = b < blocks ? qrow[b * 32 + lane] * a.scale : 0.0f;
+    const float x = b < blocks ? qrow[b * 32 + lane] : 0.0f;
+    odd = odd || !isfinite(x);
+    q[b] = x * a.scale;
     acc[b] = 0.0f;
   }
+  odd = __any_sync(0xffffffffu, odd);
   float m = -INFINITY, l = 0.0f;
   bool any = false;
   // keys 0 .. sink_end-1, then begin .. p, dealt to the warps in turn
@@ -122,12 +130,8 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
   for (int w = 0; w < kGWarps; ++w) top = fmaxf(top, part[w][kMaxDim]);
   const float base = top == -INFINITY ? 0.0f : top;
   for (int w = 0; w < kGWarps; ++w) sum += part[w][kMaxDim + 1] * expf(part[w][kMaxDim] - base);
-  if (sum == 0.0f && seen) {  // nothing but logits of -inf: zeros, unless a query that is not finite made them
-#pragma unroll
-    for (int b = 0; b < kMaxDim / 32; ++b)
-      if (b < blocks) sum += qrow[b * 32 + lane] * 0.0f;
-    sum = warp_sum(sum);
-  }
+  // nothing but logits of -inf: zeros, unless a query that is not finite made them
+  if (sum == 0.0f && seen && odd) sum = NAN;
   float* orow = a.O + t * a.ldo + static_cast<long long>(h) * D;
   for (int d = threadIdx.x; d < D; d += kGWarps * 32) {
     float o = 0.0f;
