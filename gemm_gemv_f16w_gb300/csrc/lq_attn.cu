@@ -10,7 +10,7 @@
 // reads a shared head's keys once per query head: one f16 sequence of 513
 // positions, 32 heads over 8 of 128, takes 66 us (the warp-level kernel 10),
 // 64 sequences of 8192 take 5.1 ms (0.34; with heads of 96, which only this
-// kernel takes, 4.5).
+// kernel takes, 4.4).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -30,7 +30,7 @@
 // same bits in both), weighs its half of the keys (P has columns of its own) and
 // sums its half of O's dims; QK of the next tile (S in two places in turn) runs
 // under the softmax. 2048 tokens over 16384 positions, 16 heads over 2, run at
-// 591 TFLOP/s of the plain formula in f16, 198 in Q8_0 (tiles of 32 keys only).
+// 607 TFLOP/s of the plain formula in f16, 195 in Q8_0 (tiles of 32 keys only).
 //
 // Roles (four warpgroups, registers moved between them): two softmax groups,
 // one per row tile; four loader warps (16-byte asynchronous copies for f16;
@@ -50,14 +50,15 @@
 // without the weights' arithmetic, or without either product, the time stays
 // within 10 %. 1024 tokens over 16384 positions, 32 heads over 8 of 128, f16: 357 us
 // (746 TFLOP/s of the plain formula, two MMAs a product); 2048 over 16384, Q8_0:
-// 1397 us (369 TFLOP/s), where the loaders' conversions (two parts of every element
+// 1380 us (374 TFLOP/s), where the loaders' conversions (two parts of every element
 // for every CTA that reads it) take as long as the MMAs. A unit's start and end add
 // 10 us: 128 KB of queries come in and as much goes out at about 20 bytes a cycle an
 // SM, and asking for the queries a tile earlier changed nothing. So 3 prompts of up
-// to 4001 tokens, f16, take 459 us (562 TFLOP/s), and a prompt of 8192 under a window
-// of 1024, 32 heads over 8 of 64, whose units have nine tiles, 235.
+// to 4001 tokens, f16, take 463 us (557 TFLOP/s), and a prompt of 8192 under a window
+// of 1024, 32 heads over 8 of 64, whose units have nine tiles, 238.
 // Every wait is bounded; on timeout the kernel records LQ_ERR_DEVICE_TIMEOUT,
-// lets its copies and MMAs finish, frees TMEM and returns.
+// lets its copies and MMAs finish, frees TMEM and returns. The roles' hand-overs
+// are modelled in tests/test_attn_tile_protocol_cpu.py.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

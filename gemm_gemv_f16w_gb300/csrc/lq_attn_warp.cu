@@ -39,12 +39,12 @@
 //
 // What bounds it. Every key and value is read once for all rows that share it,
 // so HBM is the floor. f16: 64 sequences of 8192 positions, 8 heads of 128,
-// take 340 us (6.33 TB/s, 94 % of a copy); one of 131071, 2 heads of 256, 61 us
+// take 342 us (6.29 TB/s, 93 % of a copy); one of 131071, 2 heads of 256, 61 us
 // (4.43 TB/s: 27 tiles a warp, of whose time a fifth is start and join). Q8_0:
-// the same batch with mixed lengths up to 8192 131 us (4.65 TB/s, 69 %), bound
+// the same batch with mixed lengths up to 8192 131 us (4.63 TB/s, 69 %), bound
 // by issue: the MMAs' and conversions' instructions and their fixed latency, at
 // the 12 warps that registers and stages allow. Q4_0 has half the bytes and the
-// same work: 131 us. Four tokens of 16 sequences of up to 6000, Q4_0: 50 us. One
+// same work: 128 us. Four tokens of 16 sequences of up to 6000, Q4_0: 50 us. One
 // token over 513 positions takes 9.6 us: launch, page lookup, one round of
 // loads, the join of the warps.
 #include <algorithm>

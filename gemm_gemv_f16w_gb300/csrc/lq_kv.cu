@@ -14,11 +14,12 @@
 // The rounding rules are those of the host packers (lq_pack.cpp), and the
 // codes are theirs bit for bit, without a division an element: the scale
 // top / 127 comes from the rounded reciprocal by Markstein's correction (the
-// remainder top - 127 q is exact, q + remainder / 127 rounds correctly;
-// tests/test_kv_scale_cpu.py checks every mantissa), and x / d from an approximate reciprocal, whose
-// error (3e-5 at most) cannot change a code unless x / d is within 1e-4 of a
-// half. Blocks with such an element (one in 160), with values beyond the
-// cache's range, NaNs or scales near f32's smallest take the exact divisions.
+// remainder top - 127 q is exact, q + remainder / 127 rounds correctly:
+// tests/test_kv_scale_cpu.py, for every mantissa), and x / d from an approximate
+// reciprocal, whose error (3e-5 at most) cannot change a code unless x / d is
+// within 1e-4 of a half. Blocks with such an element (one in 160), with values
+// beyond the cache's range, NaNs or scales near f32's smallest take the exact
+// divisions.
 //
 // 16384 tokens, 8 heads of 128, Q8_0: written in 42 us (4.0 TB/s; 59 % of the
 // issue slots, the loads' latency for the rest), written and read back in 69 (107
