@@ -43,6 +43,8 @@ EXPORTS = [
     "lq_gemv_q4_0i", "lq_gemm_q4_0i", "lq_matmul_q4_0i", "lq_pack_q4_0i", "lq_pack_q8_0_rcp",
     "lq_topk_work_bytes", "lq_topk_f32", "lq_gemv_topk", "lq_debug_chain_waits",
     "lq_kv_pool_bytes", "lq_kv_write", "lq_kv_read", "lq_attn_work_bytes", "lq_attn_paged", "lq_debug_attn_route",
+    "lq_rope_init", "lq_rope", "lq_tree_plan", "lq_attn_tree", "lq_tree_accept", "lq_kv_keep",
+    "lq_beam_work_bytes", "lq_beam_select", "lq_beam_pages", "lq_kv_copy",
 ]
 _COMPUTE = [n for n in EXPORTS if n.split("_")[1] in ("gemv", "gemm", "matmul")]
 
@@ -126,6 +128,21 @@ def lib() -> ctypes.CDLL:
         L.lq_attn_work_bytes.restype = ctypes.c_size_t
         L.lq_attn_paged.argtypes = [cp, bp, vp, i64, vp, i64, vp, i64, ctypes.c_float, i64, i64, vp, vp]
         L.lq_attn_paged.restype = st
+        rp, f64, c_int = ctypes.POINTER(RopeTable), ctypes.c_double, ctypes.c_int
+        L.lq_rope_init.argtypes = [rp, i64, i64, c_int, f64, vp, i64, vp, c_int, f64]
+        L.lq_rope.argtypes = [rp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, c_int, vp]
+        L.lq_tree_plan.argtypes = [bp, vp, vp, vp, i64, i64, i64, vp]
+        L.lq_attn_tree.argtypes = [cp, bp, vp, i64, vp, vp, i64, vp, i64, vp, i64, ctypes.c_float, i64, i64, vp, vp]
+        L.lq_tree_accept.argtypes = [bp, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+        L.lq_kv_keep.argtypes = [cp, bp, vp, i64, vp, vp]
+        L.lq_beam_work_bytes.argtypes = [i64, i64, i64, i64]
+        L.lq_beam_work_bytes.restype = ctypes.c_size_t
+        L.lq_beam_select.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, ctypes.c_int32, vp, vp, vp, vp, vp]
+        L.lq_beam_pages.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp]
+        L.lq_kv_copy.argtypes = [cp, vp, i64, vp]
+        for n in ("lq_rope_init", "lq_rope", "lq_tree_plan", "lq_attn_tree", "lq_tree_accept", "lq_kv_keep", "lq_beam_select",
+                  "lq_beam_pages", "lq_kv_copy"):
+            getattr(L, n).restype = st
         L.lq_debug_attn_route.argtypes = [st]
         L.lq_debug_attn_route.restype = st
         _lib = L
@@ -424,6 +441,34 @@ def attn_work(cache, batch, heads, device=None):
     return torch.zeros(nbytes, dtype=torch.uint8, device=device or batch.page_table.device)
 
 
+def _attn_operands(cache, batch, Q, O, lse, work, heads, stream, what):
+    """The checks that lq_attn_paged and lq_attn_tree share; (q, ldq, o, ldo,
+    lse, heads, work, stream) as the C calls take them."""
+    if cache.gpu != batch.gpu:
+        _elsewhere(cache, batch, what)
+    D = cache.head_dim
+    if heads is None:
+        heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // D
+    if work is None:
+        if stream is not None:
+            raise LQError(LQ_ERR_INVALID_ARG, f"{what}: a call on a stream of its own brings its work buffer")
+        work = attn_work(cache, batch, heads)
+    elif not isinstance(work, int):
+        need = cache.work_bytes
+        if need == 0:  # (0 for arguments that the call itself refuses)
+            need = cache.work_bytes = int(lib().lq_attn_work_bytes(cache.ref, batch.ref, cache.struct.kv_heads))
+        if work.numel() * work.element_size() < need or not work.is_contiguous() or work.get_device() != batch.gpu:
+            raise LQError(LQ_ERR_INVALID_ARG, f"{what}: a work buffer of {need} contiguous bytes on the batch's GPU is "
+                                              "needed (attn_work)")
+    q, ldq = _rows(Q, batch, heads * D, what)
+    o, ldo = _rows(O, batch, heads * D, what)
+    if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()
+                                                         or lse.dtype.itemsize != 4 or not lse.is_floating_point()
+                                                         or lse.get_device() != batch.gpu):
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: lse is a contiguous float32 [tokens, heads] on the batch's GPU")
+    return q, ldq, o, ldo, _ptr(lse), heads, work, _current_stream() if stream is None else _stream(stream)
+
+
 def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=None, heads=None, stream=None) -> None:
     """Attention of the batch's tokens (Q, O: float32 [tokens, heads,
     head_dim]) over the cache, causal, with an optional sliding window and
@@ -431,30 +476,8 @@ def lq_attn_paged(cache, batch, Q, O, scale, window=0, sinks=0, lse=None, work=N
     program keeps (None makes one for this call); a buffer made for a cache of
     other heads is refused if it is smaller than this one's. ``heads`` is
     needed where Q is not a three-dimensional tensor. See include/lq.h."""
-    if cache.gpu != batch.gpu:
-        _elsewhere(cache, batch, "lq_attn_paged")
-    D = cache.head_dim
-    if heads is None:
-        heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // D
-    if work is None:
-        if stream is not None:
-            raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: a call on a stream of its own brings its work buffer")
-        work = attn_work(cache, batch, heads)
-    elif not isinstance(work, int):
-        need = cache.work_bytes
-        if need == 0:  # (0 for arguments that the call itself refuses)
-            need = cache.work_bytes = int(lib().lq_attn_work_bytes(cache.ref, batch.ref, cache.struct.kv_heads))
-        if work.numel() * work.element_size() < need or not work.is_contiguous() or work.get_device() != batch.gpu:
-            raise LQError(LQ_ERR_INVALID_ARG, f"lq_attn_paged: a work buffer of {need} contiguous bytes on the batch's GPU is "
-                                              "needed (attn_work)")
-    q, ldq = _rows(Q, batch, heads * D, "lq_attn_paged")
-    o, ldo = _rows(O, batch, heads * D, "lq_attn_paged")
-    if lse is not None and not isinstance(lse, int) and (tuple(lse.shape) != (batch.tokens, heads) or not lse.is_contiguous()
-                                                         or lse.dtype.itemsize != 4 or not lse.is_floating_point()
-                                                         or lse.get_device() != batch.gpu):
-        raise LQError(LQ_ERR_INVALID_ARG, "lq_attn_paged: lse is a contiguous float32 [tokens, heads] on the batch's GPU")
-    st = (_lib or lib()).lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, _ptr(lse), heads, scale, window, sinks, _ptr(work),
-                                       _current_stream() if stream is None else _stream(stream))
+    q, ldq, o, ldo, lse, heads, work, stream = _attn_operands(cache, batch, Q, O, lse, work, heads, stream, "lq_attn_paged")
+    st = (_lib or lib()).lq_attn_paged(cache.ref, batch.ref, q, ldq, o, ldo, lse, heads, scale, window, sinks, _ptr(work), stream)
     if st:
         _check(st, "lq_attn_paged")
 
@@ -463,6 +486,215 @@ def attn_route(route: int) -> None:
     """lq_attn_paged's kernel: 0 automatic, 1 generic, 2 warp-level MMAs,
     3 tcgen05; for tests and comparisons."""
     _check(lib().lq_debug_attn_route(int(route)), "lq_debug_attn_route")
+
+
+# ---- rotary positions, drafted trees, beams ----------------------------------
+ROPE_MAX_PAIRS, ROPE_MAX_AXES, BEAM_MAX = 128, 4, 64
+
+
+class RopeTable(ctypes.Structure):
+    """The lq_rope_table struct of lq.h."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS)]
+
+
+class Rope:
+    """The angles of rotary positions (lq_rope_table), which a program keeps:
+    ``sections`` pairs by each axis of the positions, in blocks or, with
+    ``interleaved``, in turns; ``freqs``: angles a position, or None for
+    base^(-2j / rotary_dim); ``adjacent``: pairs (2j, 2j + 1) instead of (j, j +
+    rotary_dim / 2). See include/lq.h."""
+
+    def __init__(self, head_dim, rotary_dim=None, base=10000.0, adjacent=False, sections=None, interleaved=False, freqs=None, factor=1.0):
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        axes = 1 if sections is None else len(sections)
+        cut = None if sections is None else (ctypes.c_int32 * axes)(*[int(x) for x in sections])
+        if freqs is not None and len(freqs) != rotary_dim // 2:
+            raise LQError(LQ_ERR_INVALID_ARG, "Rope: one frequency a pair, rotary_dim / 2 in all")
+        given = None if freqs is None else (ctypes.c_double * len(freqs))(*[float(x) for x in freqs])
+        self.struct = RopeTable()
+        _check(lib().lq_rope_init(ctypes.byref(self.struct), int(head_dim), int(rotary_dim), 1 if adjacent else 0, float(base), given,
+                                  axes, cut, 1 if interleaved else 0, float(factor)), "lq_rope_init")
+        self.ref = ctypes.byref(self.struct)
+        self.head_dim, self.axes = int(head_dim), axes
+
+
+def _head_rows(x, tokens, D, gpu, what):
+    """(address, leading dimension, heads) of float32 rows [tokens, heads, D] or
+    [tokens, heads * D] on one GPU."""
+    shape, strides = x.shape, x.stride()
+    rank = len(shape)
+    ok = 2 <= rank <= 3 and shape[0] == tokens and x.dtype.itemsize == 4 and x.is_floating_point() and x.get_device() == gpu >= 0
+    if ok:
+        width = shape[1] if rank == 2 else shape[1] * shape[2]
+        ok = width % D == 0 and (strides[-1] == 1 or shape[-1] == 1) and (rank == 2 or (shape[2] == D and (strides[1] == D or shape[1] == 1)))
+    if not ok:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 [{tokens}, heads, {D}] with contiguous heads and dims on one GPU wanted, "
+                                          f"got {tuple(shape)} {x.dtype} on {x.device}, strides {strides}")
+    return x.data_ptr(), strides[0] if tokens > 1 else width, width // D
+
+
+def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, stream=None) -> None:
+    """Turns the rows of Q and, if given, K (float32 [tokens, heads, head_dim],
+    slices of a fused projection's rows allowed) by their positions (int32
+    [tokens] or [axes, tokens]), in place or into q_out and k_out. See
+    include/lq.h."""
+    tokens, gpu, D = Q.shape[0], Q.get_device(), rope.head_dim
+    shape = positions.shape
+    if positions.get_device() != gpu or str(positions.dtype) != "torch.int32" or shape[-1] != tokens or \
+            (rope.axes > 1 or len(shape) != 1) and (len(shape) != 2 or shape[0] != rope.axes) or (tokens > 1 and positions.stride(-1) != 1):
+        raise LQError(LQ_ERR_INVALID_ARG, f"lq_rope: int32 positions [{rope.axes}, {tokens}] on Q's GPU, contiguous along the tokens")
+    q, ldq, heads = _head_rows(Q, tokens, D, gpu, "lq_rope")
+    qo, ldqo, n = (q, ldq, heads) if q_out is None else _head_rows(q_out, tokens, D, gpu, "lq_rope")
+    k = ldk = ko = ldko = kv_heads = m = 0
+    if K is not None:
+        k, ldk, kv_heads = _head_rows(K, tokens, D, gpu, "lq_rope")
+        ko, ldko, m = (k, ldk, kv_heads) if k_out is None else _head_rows(k_out, tokens, D, gpu, "lq_rope")
+    if n != heads or m != kv_heads or (K is None and k_out is not None):
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_rope: q_out and k_out have the shapes of Q and K")
+    st = (_lib or lib()).lq_rope(rope.ref, tokens, positions.data_ptr(), positions.stride(0) if len(shape) == 2 else tokens, q, ldq, qo, ldqo,
+                                 heads, k, ldk, ko, ldko, kv_heads, 1 if inverse else 0,
+                                 _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_rope")
+
+
+def _ints(x, shape, gpu, what, name):
+    """The address of a contiguous int32 tensor of this shape on this GPU."""
+    if x.shape != shape or str(x.dtype) != "torch.int32" or not x.is_contiguous() or x.get_device() != gpu or gpu < 0:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: {name} is a contiguous int32 {list(shape)} on the same GPU, got {list(x.shape)} "
+                                          f"{x.dtype} on {x.device}")
+    return x.data_ptr()
+
+
+def lq_tree_plan(batch, parent, positions=None, mask=None, window=0, sinks=0, stream=None) -> None:
+    """Positions (int32 [tokens]) and masks (int32 [tokens, words], a bit a row
+    of the sequence) of the batch's new tokens from their parents (int32
+    [tokens]). See include/lq.h."""
+    t, g = batch.tokens, batch.gpu
+    p = _ints(parent, (t,), g, "lq_tree_plan", "parent")
+    pos = 0 if positions is None else _ints(positions, (t,), g, "lq_tree_plan", "positions")
+    words = 0 if mask is None else mask.shape[-1]
+    m = 0 if mask is None else _ints(mask, (t, words), g, "lq_tree_plan", "mask")
+    st = (_lib or lib()).lq_tree_plan(batch.ref, p, pos, m, words, window, sinks, _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_tree_plan")
+
+
+def lq_attn_tree(cache, batch, mask, Q, O, scale, positions=None, window=0, sinks=0, lse=None, work=None, heads=None, stream=None) -> None:
+    """lq_attn_paged where a row sees of its sequence's new tokens those that its
+    mask names (lq_tree_plan); positions are needed with a window. See
+    include/lq.h."""
+    t = batch.tokens
+    q, ldq, o, ldo, lse, heads, work, stream = _attn_operands(cache, batch, Q, O, lse, work, heads, stream, "lq_attn_tree")
+    words = mask.shape[-1]
+    m = _ints(mask, (t, words), batch.gpu, "lq_attn_tree", "mask")
+    pos = 0 if positions is None else _ints(positions, (t,), batch.gpu, "lq_attn_tree", "positions")
+    st = (_lib or lib()).lq_attn_tree(cache.ref, batch.ref, m, words, pos, q, ldq, o, ldo, lse, heads, scale, window, sinks, _ptr(work), stream)
+    if st:
+        _check(st, "lq_attn_tree")
+
+
+def lq_tree_accept(batch, parent, token, target, keep, count, next_token, kept_len, stream=None) -> None:
+    """The longest path of the tree that the model's choices (target) confirm:
+    its rows in keep (int32 [batch, max_keep], -1 behind them), their number in
+    count, the choice after the last in next_token and the length of the cache
+    with the path in kept_len (int32 [batch] each). See include/lq.h."""
+    t, g, b = batch.tokens, batch.gpu, batch.kv_len.shape[0]
+    rows = [_ints(x, (t,), g, "lq_tree_accept", n) for x, n in ((parent, "parent"), (token, "token"), (target, "target"))]
+    outs = [_ints(x, (b,), g, "lq_tree_accept", n) for x, n in ((count, "count"), (next_token, "next_token"), (kept_len, "kept_len"))]
+    most = keep.shape[-1]
+    st = (_lib or lib()).lq_tree_accept(batch.ref, *rows, _ints(keep, (b, most), g, "lq_tree_accept", "keep"), most, *outs,
+                                        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_tree_accept")
+
+
+def lq_kv_keep(cache, batch, keep, count, stream=None) -> None:
+    """Moves the rows keep[i, : count[i]] of each sequence's new tokens to the
+    front of them, in the cache. See include/lq.h."""
+    if cache.gpu != batch.gpu:
+        _elsewhere(cache, batch, "lq_kv_keep")
+    b, most = batch.kv_len.shape[0], keep.shape[-1]
+    st = (_lib or lib()).lq_kv_keep(cache.ref, batch.ref, _ints(keep, (b, most), batch.gpu, "lq_kv_keep", "keep"), most,
+                                    _ints(count, (b,), batch.gpu, "lq_kv_keep", "count"),
+                                    _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_kv_keep")
+
+
+def beam_buffers(groups, beams, vocab, k, device=None):
+    """(scores, parents, tokens, work) device buffers of lq_beam_select, which a
+    program keeps; work is zero-filled."""
+    import torch
+    nbytes = int(lib().lq_beam_work_bytes(int(groups), int(beams), int(vocab), int(k)))
+    if nbytes == 0:
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_beam_work_bytes")
+    device = device or "cuda"
+    return (torch.empty(groups, k, dtype=torch.float32, device=device), torch.empty(groups, k, dtype=torch.int32, device=device),
+            torch.empty(groups, k, dtype=torch.int32, device=device), torch.zeros(nbytes, dtype=torch.uint8, device=device))
+
+
+_beam_work_bytes = {}  # by (groups, beams, vocab, k): a number that depends on these alone
+
+
+def lq_beam_select(logits, scores, beams, k, out_scores, out_parents, out_tokens, work, finished=None, pad=0, stream=None) -> None:
+    """The k best continuations of each group of ``beams`` rows of logits
+    (float32 [groups * beams, vocab], rows may be strided) by scores (float32
+    [groups * beams]) + log softmax: out_scores, out_parents, out_tokens
+    [groups, k], work: beam_buffers(...). finished: int32 [groups * beams] or
+    None. See include/lq.h."""
+    what = "lq_beam_select"
+    (n, vocab), gpu = logits.shape, logits.get_device()
+    groups = n // beams if beams > 0 else 0
+    ok = gpu >= 0 and groups * beams == n and (logits.stride(1) == 1 or vocab == 1)
+    for x, shape in ((logits, (n, vocab)), (scores, (n,)), (out_scores, (groups, k))):
+        ok = ok and x.shape == shape and x.dtype.itemsize == 4 and x.is_floating_point() and x.get_device() == gpu \
+            and (x is logits or x.is_contiguous())
+    if not ok:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 logits [groups * beams, vocab], contiguous scores [groups * beams] and "
+                                          "out_scores [groups, k] on one GPU")
+    sizes = (groups, beams, vocab, k)
+    need = _beam_work_bytes.get(sizes)
+    if need is None:  # (0 for sizes that the call itself refuses)
+        need = _beam_work_bytes[sizes] = int(lib().lq_beam_work_bytes(*sizes))
+    if work.numel() * work.element_size() < need or not work.is_contiguous() or work.get_device() != gpu:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: a work buffer of {need} contiguous bytes on the logits' GPU is needed (beam_buffers)")
+    done = 0 if finished is None else _ints(finished, (n,), gpu, what, "finished")
+    st = (_lib or lib()).lq_beam_select(logits.data_ptr(), logits.stride(0) if n > 1 else vocab, scores.data_ptr(), groups, beams, vocab, k,
+                                        done, pad, out_scores.data_ptr(), _ints(out_parents, (groups, k), gpu, what, "out_parents"),
+                                        _ints(out_tokens, (groups, k), gpu, what, "out_tokens"), work.data_ptr(),
+                                        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, what)
+
+
+def lq_beam_pages(parent, beams, table, kv_len, page_size, table_out, copies, stream=None) -> None:
+    """Page tables (int32 [groups * beams, max_pages]) of the beams that go on
+    from parent (int32 [groups * beams]), and the copies of last pages that this
+    takes (int32 [groups * beams, 3], for lq_kv_copy). See include/lq.h."""
+    what, n, gpu = "lq_beam_pages", parent.shape[0], parent.get_device()
+    if beams < 1 or n % beams != 0 or table.dim() != 2:
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: parents and tables of groups * beams rows")
+    width = table.shape[1]
+    st = (_lib or lib()).lq_beam_pages(_ints(parent, (n,), gpu, what, "parent"), n // beams, beams, _ints(table, (n, width), gpu, what, "table"),
+                                       width, _ints(kv_len, (n,), gpu, what, "kv_len"), page_size,
+                                       _ints(table_out, (n, width), gpu, what, "table_out"), _ints(copies, (n, 3), gpu, what, "copies"),
+                                       _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, what)
+
+
+def lq_kv_copy(cache, copies, stream=None) -> None:
+    """Copies the first tokens of pages of the cache to other pages: copies is
+    int32 [n, 3] of (from, to, tokens), as lq_beam_pages gives them. See
+    include/lq.h."""
+    gpu = copies.get_device() if cache.gpu is None else cache.gpu
+    st = (_lib or lib()).lq_kv_copy(cache.ref, _ints(copies, (copies.shape[0], 3), gpu, "lq_kv_copy", "copies"), copies.shape[0],
+                                    _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "lq_kv_copy")
 
 
 # ---- host packers --------------------------------------------------------

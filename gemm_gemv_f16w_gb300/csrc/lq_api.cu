@@ -268,7 +268,9 @@ lq_status lq_last_device_error(void) {
   unsigned v = 0;  // the first error of any unit; all are cleared
   for (unsigned (*read)() : {read_clear_gemv_error, read_clear_gemm_error, read_clear_gemm_tma_error, read_clear_chain_error,
                              read_clear_batch_error, read_clear_small_error, read_clear_kv_error, read_clear_attn_error,
-                             read_clear_attn_warp_error, read_clear_attn_tile_error}) {
+                             read_clear_attn_warp_error, read_clear_attn_tile_error, read_clear_attn_warp_tree_error,
+                             read_clear_attn_tile_tree_error, read_clear_rope_error, read_clear_tree_error, read_clear_move_error,
+                             read_clear_beam_error}) {
     const unsigned e = read();
     v = v ? v : e;
   }

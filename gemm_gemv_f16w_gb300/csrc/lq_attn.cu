@@ -1,5 +1,5 @@
-// lq_attn_paged: argument checks, the choice of a kernel, and the generic
-// kernel that takes every geometry.
+// lq_attn_paged and lq_attn_tree: argument checks, the choice of a kernel, and
+// the generic kernel that takes every geometry.
 //
 // Generic kernel: one CTA per (row, query head). Its eight warps stride over
 // the visible keys, a lane holding the dims lane, lane + 32, ... of the query
@@ -47,7 +47,7 @@ constexpr int kMaxDim = 256;
 // gain from the warp-level kernel up to 128 rows, where one sequence loses.
 int few_rows(int fmt, int head_dim) { return fmt == LQ_FMT_F16 ? 48 : (head_dim == 256 ? 96 : 80); }
 
-template <int FMT>
+template <int FMT, bool TREE>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
   __shared__ float part[kGWarps][kMaxDim + 2];
   pdl_wait();
@@ -58,8 +58,15 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
   const int i = kv::find_sequence(a.b, t, lane);
   if (i < 0) return;  // the whole CTA
   const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
-  const int p = s.len - s.rows + (t - s.row0);
-  const kv::Visible see = kv::visible(p, a.window, a.sinks);
+  const int base = s.len - s.rows;
+  const int p = TREE ? tree::position(a, t, base, s.len) : base + (t - s.row0);
+  kv::Visible see = kv::visible(TREE ? max(p, 0) : p, a.window, a.sinks);
+  int cached = p + 1;  // keys before it are the window's to choose
+  if constexpr (TREE) {
+    cached = max(base, 0);
+    see.begin = min(see.begin, cached);
+    see.sink_end = min(see.sink_end, cached);
+  }
 
   float q[kMaxDim / 32], acc[kMaxDim / 32];
   bool odd = false;  // the query is not finite
@@ -75,10 +82,13 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
   float m = -INFINITY, l = 0.0f;
   bool any = false;
   // keys 0 .. sink_end-1, then begin .. p, dealt to the warps in turn
-  const int count = p < 0 ? 0 : see.sink_end + (p - see.begin + 1);
+  // (and, for a tree, the sequence's new tokens that the row's bits name)
+  const int chosen = see.sink_end + (cached - see.begin);
+  const int count = TREE ? chosen + (s.len - cached) : (p < 0 ? 0 : chosen);
   const long long scale_at = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
   for (int n = warp; n < count; n += kGWarps) {
     const int j = n < see.sink_end ? n : see.begin + (n - see.sink_end);
+    if (TREE && n >= chosen && !(tree::bits(a, t, j - base) & 1u)) continue;
     const int page = kv::page_of(a.c, a.b, i, j);
     if (page < 0) continue;
     const int slot = j % a.c.page_size;
@@ -110,8 +120,8 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
     x = warp_sum(x);
     any = true;
     const float to = fmaxf(m, x);
-    const float base = to == -INFINITY ? 0.0f : to;  // every logit so far is -inf
-    const float keep = expf(m - base), w = expf(x - base);
+    const float ref = to == -INFINITY ? 0.0f : to;  // every logit so far is -inf
+    const float keep = expf(m - ref), w = expf(x - ref);
     m = to;
     l = l * keep + w;
 #pragma unroll
@@ -128,18 +138,18 @@ __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnAr
   const bool seen = __syncthreads_or(any ? 1 : 0) != 0;  // (if not, the sum is zero)
   float top = -INFINITY, sum = 0.0f;
   for (int w = 0; w < kGWarps; ++w) top = fmaxf(top, part[w][kMaxDim]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  for (int w = 0; w < kGWarps; ++w) sum += part[w][kMaxDim + 1] * expf(part[w][kMaxDim] - base);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  for (int w = 0; w < kGWarps; ++w) sum += part[w][kMaxDim + 1] * expf(part[w][kMaxDim] - ref);
   // nothing but logits of -inf: zeros, unless a query that is not finite made them
   if (sum == 0.0f && seen && odd) sum = NAN;
   float* orow = a.O + t * a.ldo + static_cast<long long>(h) * D;
   for (int d = threadIdx.x; d < D; d += kGWarps * 32) {
     float o = 0.0f;
-    for (int w = 0; w < kGWarps; ++w) o += part[w][d] * expf(part[w][kMaxDim] - base);
+    for (int w = 0; w < kGWarps; ++w) o += part[w][d] * expf(part[w][kMaxDim] - ref);
     if (LQ_IN_BOUNDS(t < a.b.tokens && h < a.heads)) orow[d] = sum == 0.0f ? 0.0f : o / sum;
   }
   if (a.lse && threadIdx.x == 0)
-    a.lse[static_cast<long long>(t) * a.heads + h] = sum == 0.0f ? -INFINITY : base + logf(sum);
+    a.lse[static_cast<long long>(t) * a.heads + h] = sum == 0.0f ? -INFINITY : ref + logf(sum);
 }
 
 }  // namespace
@@ -156,9 +166,13 @@ lq_status launch_attn_generic(const AttnArgs& a, int fmt, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void (*kernel)(AttnArgs) = fmt == LQ_FMT_F16    ? attn_generic_kernel<LQ_FMT_F16>
-                             : fmt == LQ_FMT_Q8_0 ? attn_generic_kernel<LQ_FMT_Q8_0>
-                                                  : attn_generic_kernel<LQ_FMT_Q4_0>;
+  void (*kernel)(AttnArgs) = fmt == LQ_FMT_F16    ? attn_generic_kernel<LQ_FMT_F16, false>
+                             : fmt == LQ_FMT_Q8_0 ? attn_generic_kernel<LQ_FMT_Q8_0, false>
+                                                  : attn_generic_kernel<LQ_FMT_Q4_0, false>;
+  if (a.mask)
+    kernel = fmt == LQ_FMT_F16    ? attn_generic_kernel<LQ_FMT_F16, true>
+             : fmt == LQ_FMT_Q8_0 ? attn_generic_kernel<LQ_FMT_Q8_0, true>
+                                  : attn_generic_kernel<LQ_FMT_Q4_0, true>;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) count_route(kAttnRouteGeneric);
@@ -173,22 +187,10 @@ unsigned read_clear_attn_error() {
   return v;
 }
 
-}  // namespace lq
-
-using namespace lq;
-
-extern "C" {
-
-size_t lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, int64_t heads) {
-  bool noop;
-  if (kv_check(cache, batch, &noop) != LQ_OK) return 0;
-  if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
-  return std::max(attn_warp_work_bytes(), attn_tile_work_bytes(cache->head_dim));
-}
-
-lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
-                        float* O, int64_t ldo, float* lse, int64_t heads, float scale, int64_t window,
-                        int64_t sinks, void* work, void* stream) {
+// lq_attn_paged, and with a mask lq_attn_tree.
+static lq_status attend(const lq_kv_cache* cache, const lq_kv_batch* batch, const uint32_t* mask, int64_t mask_words,
+                        const int32_t* positions, const float* Q, int64_t ldq, float* O, int64_t ldo, float* lse, int64_t heads,
+                        float scale, int64_t window, int64_t sinks, void* work, void* stream) {
   bool noop;
   lq_status st = kv_check(cache, batch, &noop);
   if (st != LQ_OK) return st;
@@ -214,6 +216,9 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   const int64_t most = 1LL << 30;  // past every position (kv_check)
   a.window = static_cast<int>(std::min(window, most));
   a.sinks = static_cast<int>(std::min(sinks, most));
+  a.mask = mask;
+  a.positions = positions;
+  a.mask_words = static_cast<int>(mask_words);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int route = g_attn_route.load();
   // (without pages the other kernels have no address that they may read)
@@ -234,6 +239,37 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
     if (st != LQ_OK) return st;
   }
   return launch_attn_tile(a, cache->fmt, split, work, s);
+}
+
+}  // namespace lq
+
+using namespace lq;
+
+extern "C" {
+
+size_t lq_attn_work_bytes(const lq_kv_cache* cache, const lq_kv_batch* batch, int64_t heads) {
+  bool noop;
+  if (kv_check(cache, batch, &noop) != LQ_OK) return 0;
+  if (heads < 1 || heads % cache->kv_heads != 0 || heads > 65536) return 0;
+  return std::max(attn_warp_work_bytes(), attn_tile_work_bytes(cache->head_dim));
+}
+
+lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, const float* Q, int64_t ldq,
+                        float* O, int64_t ldo, float* lse, int64_t heads, float scale, int64_t window,
+                        int64_t sinks, void* work, void* stream) {
+  return attend(cache, batch, nullptr, 0, nullptr, Q, ldq, O, ldo, lse, heads, scale, window, sinks, work, stream);
+}
+
+lq_status lq_attn_tree(const lq_kv_cache* cache, const lq_kv_batch* batch, const uint32_t* mask, int64_t mask_words,
+                       const int32_t* positions, const float* Q, int64_t ldq, float* O, int64_t ldo, float* lse, int64_t heads,
+                       float scale, int64_t window, int64_t sinks, void* work, void* stream) {
+  bool noop;
+  const lq_status st = kv_check(cache, batch, &noop);
+  if (st != LQ_OK) return st;
+  if (mask_words < 1) return LQ_ERR_INVALID_ARG;
+  if (!noop && (!mask || !aligned_to(mask, 4) || !aligned_to(positions, 4) || (window > 0 && !positions))) return LQ_ERR_INVALID_ARG;
+  if (mask_words > LQ_TREE_MAX_WORDS) return LQ_ERR_UNSUPPORTED;
+  return attend(cache, batch, mask, mask_words, positions, Q, ldq, O, ldo, lse, heads, scale, window, sinks, work, stream);
 }
 
 lq_status lq_debug_attn_route(int route) {

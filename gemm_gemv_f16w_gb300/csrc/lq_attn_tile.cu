@@ -75,6 +75,14 @@
 namespace lq {
 namespace {
 
+// The same kernels twice: this file, and with the rows' masks of lq_attn_tree
+// lq_attn_tile_tree.cu, which includes it.
+#ifdef LQ_ATTN_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 __device__ unsigned g_attnt_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnt_err, 0u, code); }
 
@@ -313,8 +321,9 @@ struct Work {
 template <int KT, int ROWS>
 __device__ __forceinline__ void unit_tiles(Work& w, const AttnArgs& a) {
   const int rows = w.s.rows * a.group, rho0 = w.rt * ROWS;
-  w.p0 = w.s.len - w.s.rows + rho0 / a.group;
-  w.p1 = w.s.len - w.s.rows + min(rho0 + ROWS - 1, rows - 1) / a.group;
+  // (a tree's rows may have any position, and see any of the new tokens)
+  w.p0 = w.s.len - w.s.rows + (kTree ? 0 : rho0 / a.group);
+  w.p1 = kTree ? w.s.len - 1 : w.s.len - w.s.rows + min(rho0 + ROWS - 1, rows - 1) / a.group;
   const kv::Visible v = kv::visible(max(w.p0, 0), a.window, a.sinks);
   w.begin = v.begin;
   w.sink_end = v.sink_end;
@@ -522,7 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool active = w.rho0 + rq * 128 < w.rows;  // the row tile has rows
       const bool row = rho < w.rows;
       const int token = min(rho, w.rows - 1) / a.group;
-      const int t = w.row0 + token, head = w.head0 + (min(rho, w.rows - 1) - token * a.group), pos = w.pos0 + token;
+      const int t = w.row0 + token, head = w.head0 + (min(rho, w.rows - 1) - token * a.group);
+      const int pos = kTree ? tree::position(a, t, w.pos0, w.pos0 + w.rows / a.group) : w.pos0 + token;
+      const int near = kTree ? w.pos0 - 1 : pos;  // keys up to here are the window's alone to choose
       float om[DO], M = kNoMax, l = 0.0f, f = 0.0f;
       if (active) {
         // The warp's 32 query rows come as f32 into the very bytes of shared memory
@@ -605,17 +616,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         const int j0 = bar->info[tile % kInfo].j0;
         const uint32_t pages = bar->info[tile % kInfo].flags & 0xFFu;
-        const bool clear = pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= pos &&
+        const bool clear = pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= near &&
                            (a.window == 0 || j0 > pos - a.window || j0 + KT <= a.sinks);
         const bool edge = __any_sync(0xffffffffu, !clear);
         // bit i: the row sees key j + i of the tile (i < 32; j a multiple of 16)
         auto vis32 = [&](int j) -> uint32_t {
           const int last = pos - j0 - j;  // keys up to here are not ahead of the row
           uint32_t m = last < 0 ? 0u : (last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u);
+          if constexpr (kTree) {
+            const int old = near - j0 - j;  // keys up to here are not of the new tokens
+            m = old < 0 ? 0u : (old >= 31 ? 0xFFFFFFFFu : (2u << old) - 1u);
+          }
           if (a.window != 0) {
             const int from = last >= a.window ? last - a.window + 1 : 0;  // keys from here on are in the window
             const int sink = min(max(a.sinks - j0 - j, 0), 32);           // keys below are sinks
             m &= (from >= 32 ? 0u : 0xFFFFFFFFu << from) | (sink >= 32 ? 0xFFFFFFFFu : (1u << sink) - 1u);
+          }
+          if constexpr (kTree) {
+            const int first = j0 + j - w.pos0, left = w.rows / a.group - first;  // among the new tokens; of them from there on
+            if (first > -32 && left > 0) m |= tree::bits(a, t, first) & (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u);
           }
           const uint32_t pg = pages >> (j >> 4);
           return m & ((pg & 1u ? 0xFFFFu : 0u) | (pg & 2u ? 0xFFFF0000u : 0u));
@@ -1361,7 +1380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t flags = pages;
           if (w.rt * ROWS + 128 < w.s.rows * a.group) flags |= kTwo;
           if (first) flags |= kFirst;
-          if (w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && every)) flags |= kMixed;
+          if (kTree ? !(j0 + KT <= w.p0 && every) : w.s.rows > 1 && !(j0 + KT - 1 <= w.p0 && every)) flags |= kMixed;
           if (pages == (1u << (KT / 16)) - 1u && j0 + KT - 1 <= w.p1 && (j0 >= w.begin || j0 + KT <= w.sink_end)) flags |= kAll;
           ti.j0 = j0;
           ti.flags = flags;
@@ -1458,6 +1477,7 @@ lq_status pick(const TileParams& p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
+#ifndef LQ_ATTN_TREE
 size_t attn_tile_work_bytes(int head_dim) {
   const int ctas = std::min(std::max(device_info().sm_count, 152), kAttnMaxCtas);
   const int slot = head_dim == 64    ? Geo<LQ_FMT_F16, 64>::SLOT
@@ -1473,6 +1493,10 @@ bool attn_tile_eligible(const AttnArgs& a) {
 }
 
 lq_status launch_attn_tile(const AttnArgs& a, int fmt, int small_rows, void* work, cudaStream_t stream) {
+  if (a.mask) return launch_attn_tile_tree(a, fmt, small_rows, work, stream);
+#else
+lq_status launch_attn_tile_tree(const AttnArgs& a, int fmt, int small_rows, void* work, cudaStream_t stream) {
+#endif
   if (!attn_tile_eligible(a)) return LQ_ERR_UNSUPPORTED;
   TileParams p;
   p.a = a;
@@ -1494,7 +1518,11 @@ lq_status launch_attn_tile(const AttnArgs& a, int fmt, int small_rows, void* wor
   }
 }
 
+#ifdef LQ_ATTN_TREE
+unsigned read_clear_attn_tile_tree_error() {
+#else
 unsigned read_clear_attn_tile_error() {
+#endif
   unsigned v = 0;
   const unsigned zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_attnt_err, sizeof(v)) != cudaSuccess) return 0;

@@ -56,6 +56,14 @@
 namespace lq {
 namespace {
 
+// The same kernels twice: this file, and with the rows' masks of lq_attn_tree
+// lq_attn_warp_tree.cu, which includes it.
+#ifdef LQ_ATTN_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 __device__ unsigned g_attnw_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_attnw_err, 0u, code); }
 
@@ -544,18 +552,24 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
     }
     float f[NR], M[NR];
     float2 l[NR], om[NR][D / 8];
-    int pos[NR];
+    int pos[NR], row_t[kTree ? NR : 1];  // a tree's rows: the row of the call
+    const int tree_base = pc.s.len - pc.s.rows;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       f[n] = row_f[n * 8 + g];
       M[n] = kNoMax;
       l[n] = make_float2(0.0f, 0.0f);
       pos[n] = pc.s.len - pc.s.rows + min(rho0 + n * 8 + g, rows_all - 1) / group;
+      if constexpr (kTree) {
+        row_t[n] = pc.s.row0 + pos[n] - tree_base;
+        pos[n] = tree::position(a, row_t[n], tree_base, pc.s.len);
+      }
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) om[n][i] = make_float2(0.0f, 0.0f);
     }
-    const int p_first = pc.s.len - pc.s.rows + rho0 / group;
-    const int p_last = pc.s.len - pc.s.rows + min(rho0 + R - 1, rows_all - 1) / group;
+    // (a tree: keys before the new tokens, and the largest position there can be)
+    const int p_first = kTree ? tree_base - 1 : pc.s.len - pc.s.rows + rho0 / group;
+    const int p_last = kTree ? pc.s.len - 1 : pc.s.len - pc.s.rows + min(rho0 + R - 1, rows_all - 1) / group;
 
     const int steps = (pc.k1 - pc.k0 + TPS - 1) / TPS;
     int m = 0;
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         const bool clear = j0[t] + kTile - 1 <= p_first &&
                            (a.window == 0 || j0[t] > p_last - a.window || j0[t] + kTile <= a.sinks);
         edge = edge || any[t] != 0xFFFFu || !clear;
-        mixed = mixed || (!clear && pc.s.rows > 1);
+        mixed = mixed || (!clear && (kTree || pc.s.rows > 1));
       }
       // ---- logits ---------------------------------------------------------------
       constexpr int NT = TPS * 2;  // n-tiles of 8 keys
@@ -677,13 +691,23 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       if (edge) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
+          uint32_t named[TPS];  // the tile's keys among the new tokens that the row's mask names
+          if constexpr (kTree) {
+#pragma unroll
+            for (int t = 0; t < TPS; ++t) named[t] = tree::bits(a, row_t[n], j0[t] - tree_base);
+          }
 #pragma unroll
           for (int nt = 0; nt < TPS * 2; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int at = (nt & 1) * 8 + 2 * c + j, key = j0[nt >> 1] + at;
-              const bool see = ((any[nt >> 1] >> at) & 1u) && key <= pos[n] &&
-                               (a.window == 0 || key > pos[n] - a.window || key < a.sinks);
+              const bool in_window = a.window == 0 || key > pos[n] - a.window || key < a.sinks;
+              bool see;
+              if constexpr (kTree) {
+                see = ((any[nt >> 1] >> at) & 1u) && (key < tree_base ? in_window : ((named[nt >> 1] >> at) & 1u) != 0u);
+              } else {
+                see = ((any[nt >> 1] >> at) & 1u) && key <= pos[n] && in_window;
+              }
               if (!see) {
                 vis[n] &= ~(1u << (2 * nt + j));
                 if (j == 0) x[n][nt].x = -INFINITY; else x[n][nt].y = -INFINITY;
@@ -1169,6 +1193,7 @@ lq_status pick(const WarpParams& p, int nr, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
+#ifndef LQ_ATTN_TREE
 // Counters, then two slots of up to 16 rows a CTA.
 size_t attn_warp_work_bytes() {
   const int ctas = std::max(device_info().sm_count, 152);
@@ -1181,6 +1206,10 @@ bool attn_warp_eligible(const AttnArgs& a) {
 }
 
 lq_status launch_attn_warp(const AttnArgs& a, int fmt, int rows, int small_rows, void* work, cudaStream_t stream) {
+  if (a.mask) return launch_attn_warp_tree(a, fmt, rows, small_rows, work, stream);
+#else
+lq_status launch_attn_warp_tree(const AttnArgs& a, int fmt, int rows, int small_rows, void* work, cudaStream_t stream) {
+#endif
   if (!attn_warp_eligible(a)) return LQ_ERR_UNSUPPORTED;
   WarpParams p;
   p.a = a;
@@ -1197,7 +1226,11 @@ lq_status launch_attn_warp(const AttnArgs& a, int fmt, int rows, int small_rows,
   }
 }
 
+#ifdef LQ_ATTN_TREE
+unsigned read_clear_attn_warp_tree_error() {
+#else
 unsigned read_clear_attn_warp_error() {
+#endif
   unsigned v = 0;
   const unsigned zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_attnw_err, sizeof(v)) != cudaSuccess) return 0;

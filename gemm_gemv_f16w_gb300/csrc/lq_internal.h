@@ -111,6 +111,12 @@ unsigned read_clear_kv_error();
 unsigned read_clear_attn_error();
 unsigned read_clear_attn_warp_error();
 unsigned read_clear_attn_tile_error();
+unsigned read_clear_attn_warp_tree_error();
+unsigned read_clear_attn_tile_tree_error();
+unsigned read_clear_rope_error();
+unsigned read_clear_tree_error();
+unsigned read_clear_move_error();
+unsigned read_clear_beam_error();
 
 lq_status cuda_status(cudaError_t e);
 

@@ -1,0 +1,346 @@
+// Moving tokens inside the paged cache: lq_kv_keep (the accepted path of a
+// draft), lq_kv_copy and lq_beam_pages (beams that go on from one another).
+//
+// Codes and scales are moved as they are: nothing is rounded anew.
+//
+// Keep. Row keep[k] of a sequence's new tokens goes to the place of row k; keep[]
+// ascends, so k <= keep[k]. A thread owns one column (16 bytes of the codes, or
+// one scale) of one head of K or V and takes the rows in order, eight loads and then
+// eight stores: what a store overwrites, its own thread has read, and no
+// other touches the column. So the move is in place without a barrier.
+//
+// Pages. The beams of a group have one length; all pages before its last, partly
+// filled one are full and shared, that page and those behind are each
+// beam's own. Of the children of a beam the first goes on in its parent's own
+// pages. There are as many further children as beams without a child: the m-th
+// takes the m-th such beam's own pages and, for the last page's tokens, a copy.
+// So no copy's target is another's source, no spare pages are needed, and every
+// page keeps exactly one owner.
+//
+// Copy. One CTA for each side and head of a copy; a (page, head) is contiguous,
+// so it moves two runs of bytes. What bounds both is HBM for many beams and the
+// launch and the chain list -> page -> bytes for few.
+#include <algorithm>
+
+#include "lq_device.cuh"
+#include "lq_internal.h"
+#include "lq_kv.cuh"
+
+namespace lq {
+namespace {
+
+__device__ unsigned g_move_err;
+__device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_move_err, 0u, code); }
+
+constexpr int kKeepThreads = 128;
+constexpr int kKeepRows = 128;  // rows whose places are looked up together
+constexpr int kKeepAhead = 8;   // loads on their way
+constexpr int kCopyThreads = 256;
+constexpr int kMapThreads = 256;
+
+struct KeepArgs {
+  kv::Cache c;
+  kv::Batch b;
+  const int* keep;  // [batch][most]
+  const int* count;
+  int most;
+  int code_columns, scale_columns;  // of a head: of `width` and of two bytes
+};
+
+// Moves of a column of T from src[k] to dst[k] (offsets of the token's codes or
+// scales in the pool; -1: nothing is moved), in order.
+template <class T>
+__device__ __forceinline__ void move_column(unsigned char* at, const long long* src, const long long* dst, int n) {
+#pragma unroll 1
+  for (int k = 0; k < n; k += kKeepAhead) {
+    T x[kKeepAhead];
+    long long to[kKeepAhead];
+#pragma unroll
+    for (int j = 0; j < kKeepAhead; ++j) {
+      const bool there = k + j < n && src[k + j] >= 0 && dst[k + j] >= 0;
+      to[j] = there ? dst[k + j] : -1;
+      if (there) x[j] = *reinterpret_cast<const T*>(at + src[k + j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kKeepAhead; ++j)
+      if (to[j] >= 0) *reinterpret_cast<T*>(at + to[j]) = x[j];
+  }
+}
+
+// T: what a thread moves of the codes.
+template <class T>
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a) {
+  // places of codes and of scales, from the (page, head)'s first byte on
+  __shared__ long long code_src[kKeepRows], code_dst[kKeepRows], scale_src[kKeepRows], scale_dst[kKeepRows];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int i = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
+  const kv::Seq s = kv::sequence(a.b, a.c.page_size, i);
+  const int base = s.len - s.rows;
+  const int* const keep = a.keep + static_cast<long long>(i) * a.most;
+  const int count = min(min(a.count[i], a.most), s.rows);
+  // this thread's column
+  const int columns = a.code_columns + a.scale_columns;
+  const int column = static_cast<int>(blockIdx.y) * kKeepThreads + tid, head = column / columns, within = column - head * columns;
+  const bool mine = head < 2 * a.c.kv_heads;
+  unsigned char* const pool = head < a.c.kv_heads ? a.c.k : a.c.v;
+  const long long head_at = static_cast<long long>(head < a.c.kv_heads ? head : head - a.c.kv_heads) * a.c.head_bytes;
+  const bool is_scale = within >= a.code_columns;
+  unsigned char* const at =
+      pool + head_at + (is_scale ? static_cast<long long>(within - a.code_columns) * 2 : static_cast<long long>(within) * static_cast<int>(sizeof(T)));
+#pragma unroll 1
+  for (int k0 = 0; k0 < count; k0 += kKeepRows) {
+    const int n = min(kKeepRows, count - k0);
+    bool good = true;
+    if (tid < n) {
+      const int k = k0 + tid, from = keep[k];
+      good = from >= 0 && from < s.rows && (k == 0 ? true : from > keep[k - 1]);
+      const int p_src = base + from, p_dst = base + k;
+      int src = -1, dst = -1;
+      if (good && from != k && p_dst >= 0) {
+        src = kv::page_of(a.c, a.b, i, p_src);
+        dst = kv::page_of(a.c, a.b, i, p_dst);
+      }
+      const bool moves = src >= 0 && dst >= 0 && LQ_IN_BOUNDS(src < a.c.num_pages && dst < a.c.num_pages);
+      const long long scales = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
+      const int s_src = moves ? p_src % a.c.page_size : 0, s_dst = moves ? p_dst % a.c.page_size : 0;
+      code_src[tid] = moves ? src * a.c.page_bytes + static_cast<long long>(s_src) * a.c.row_bytes : -1;
+      code_dst[tid] = moves ? dst * a.c.page_bytes + static_cast<long long>(s_dst) * a.c.row_bytes : -1;
+      scale_src[tid] = moves ? src * a.c.page_bytes + scales + s_src * (a.c.head_dim / 16) : -1;
+      scale_dst[tid] = moves ? dst * a.c.page_bytes + scales + s_dst * (a.c.head_dim / 16) : -1;
+    }
+    // the list ends at the first entry that does not ascend
+    __shared__ int stop;
+    if (tid == 0) stop = n;
+    __syncthreads();
+    if (tid < n && !good) atomicMin(&stop, tid);
+    __syncthreads();
+    const int m = stop;
+    if (mine) {
+      if (is_scale) {
+        move_column<unsigned short>(at, scale_src, scale_dst, m);
+      } else {
+        move_column<T>(at, code_src, code_dst, m);
+      }
+    }
+    __syncthreads();  // the places are free
+    if (m < n) break;
+  }
+}
+
+struct CopyArgs {
+  kv::Cache c;
+  const int* copies;  // [n][3]: from page, to page, tokens
+};
+
+// bytes (a multiple of sizeof(T)) from one place to another by the whole block
+template <class T>
+__device__ __forceinline__ void copy_run(unsigned char* to, const unsigned char* from, long long bytes) {
+  const long long n = bytes / static_cast<int>(sizeof(T));
+  T* const dst = reinterpret_cast<T*>(to);
+  const T* const src = reinterpret_cast<const T*>(from);
+#pragma unroll 1
+  for (long long k = threadIdx.x; k < n; k += kCopyThreads * 8) {
+    T x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k + j * kCopyThreads < n) x[j] = src[k + j * kCopyThreads];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k + j * kCopyThreads < n) dst[k + j * kCopyThreads] = x[j];
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int* const c = a.copies + static_cast<long long>(blockIdx.x) * 3;
+  const int src = c[0], dst = c[1], rows = min(c[2], a.c.page_size);
+  if (rows <= 0 || src < 0 || dst < 0 || src >= a.c.num_pages || dst >= a.c.num_pages || src == dst) return;
+  const int head = static_cast<int>(blockIdx.y), h = head < a.c.kv_heads ? head : head - a.c.kv_heads;
+  unsigned char* const pool = head < a.c.kv_heads ? a.c.k : a.c.v;
+  const unsigned char* const from = pool + src * a.c.page_bytes + h * a.c.head_bytes;
+  unsigned char* const to = pool + dst * a.c.page_bytes + h * a.c.head_bytes;
+  if (!LQ_IN_BOUNDS(h < a.c.kv_heads)) return;
+  copy_run<T>(to, from, static_cast<long long>(rows) * a.c.row_bytes);
+  const long long scales = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
+  if (a.c.head_bytes > scales) copy_run<unsigned short>(to + scales, from + scales, static_cast<long long>(rows) * (a.c.head_dim / 16));
+}
+
+struct PagesArgs {
+  const int* parent;  // [groups * beams]
+  const int* table;   // [groups * beams][max_pages]
+  const int* len;     // [groups * beams]
+  int* out;
+  int* copies;  // [groups * beams][3]
+  int beams, max_pages, page_size;
+};
+
+// grid: x = group, y = part of the tables' columns
+__global__ void __launch_bounds__(kMapThreads) pages_kernel(const PagesArgs a) {
+  __shared__ int parent[LQ_BEAM_MAX], place[LQ_BEAM_MAX], free_list[LQ_BEAM_MAX];
+  __shared__ unsigned bits[2][LQ_BEAM_MAX / 32];  // beams without a child; further children
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = a.beams, tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const long long first = static_cast<long long>(blockIdx.x) * n;
+  if (tid < LQ_BEAM_MAX) {
+    const int p = tid < n ? a.parent[first + tid] : -1;
+    parent[tid] = p >= 0 && p < n ? p : -1;
+  }
+  __syncthreads();
+  if (tid < LQ_BEAM_MAX) {
+    bool childless = tid < n, further = tid < n && parent[tid] < 0;
+    for (int b = 0; b < n; ++b) {
+      childless = childless && parent[b] != tid;
+      further = further || (tid < n && b < tid && parent[b] == parent[tid]);
+    }
+    const unsigned c = __ballot_sync(0xffffffffu, childless), f = __ballot_sync(0xffffffffu, further);
+    if (lane == 0) {
+      bits[0][warp] = c;
+      bits[1][warp] = f;
+    }
+  }
+  __syncthreads();
+  // how many of a kind are before this thread's beam, and whether it is one
+  auto rank = [&](const unsigned (&of)[LQ_BEAM_MAX / 32], bool& is) {
+    int before = __popc(of[warp] & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) before += __popc(of[w]);
+    is = (of[warp] >> lane) & 1u;
+    return before;
+  };
+  bool is = false;
+  if (tid < n) {
+    const int before = rank(bits[0], is);
+    if (is) free_list[before] = tid;
+  }
+  __syncthreads();
+  if (tid < n) {  // whose own pages it goes on in
+    const int before = rank(bits[1], is);
+    place[tid] = is ? free_list[before] : parent[tid];
+  }
+  __syncthreads();
+  const int len = max(a.len[first], 0), whole = len / a.page_size, rows = len - whole * a.page_size;
+  const int from = static_cast<int>(blockIdx.y) * kMapThreads, step = static_cast<int>(gridDim.y) * kMapThreads;
+#pragma unroll 1
+  for (int b = 0; b < n; ++b) {
+    const int p = parent[b] < 0 ? place[b] : parent[b], o = place[b];
+    const int* const shared = a.table + (first + p) * a.max_pages;
+    const int* const owned = a.table + (first + o) * a.max_pages;
+    int* const out = a.out + (first + b) * a.max_pages;
+    for (int e = from + tid; e < a.max_pages; e += step)
+      if (LQ_IN_BOUNDS(e >= 0)) out[e] = e < whole ? shared[e] : owned[e];
+    if (blockIdx.y == 0 && tid == 0) {
+      int* const c = a.copies + (first + b) * 3;
+      const bool copies = parent[b] >= 0 && o != p && rows > 0 && whole < a.max_pages;
+      c[0] = copies ? shared[whole] : -1;
+      c[1] = copies ? owned[whole] : -1;
+      c[2] = copies ? rows : 0;
+    }
+  }
+}
+
+lq_status launch(const void* kernel, dim3 grid, unsigned threads, void* args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* list[1] = {args};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, list);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_status(e);
+}
+
+// 16-byte steps where every (page, head) begins on a 16-byte boundary.
+bool wide(const kv::Cache& c) { return c.head_bytes % 16 == 0 && aligned_to(c.k, 16) && aligned_to(c.v, 16); }
+
+}  // namespace
+
+unsigned read_clear_move_error() {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_move_err, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_move_err, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace lq
+
+using namespace lq;
+
+extern "C" {
+
+lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const int32_t* keep, int64_t max_keep, const int32_t* count,
+                     void* stream) {
+  bool noop;
+  const lq_status st = kv_check(cache, batch, &noop);
+  if (st != LQ_OK) return st;
+  if (max_keep < 1) return LQ_ERR_INVALID_ARG;
+  if (max_keep > (1LL << 24)) return LQ_ERR_UNSUPPORTED;
+  if (noop) return LQ_OK;
+  if (!keep || !count || !aligned_to(keep, 4) || !aligned_to(count, 4)) return LQ_ERR_INVALID_ARG;
+  KeepArgs a = {};
+  a.c = kv_cache_view(*cache);
+  a.b = kv_batch_view(*batch);
+  a.keep = keep;
+  a.count = count;
+  a.most = static_cast<int>(max_keep);
+  const bool w = wide(a.c);
+  a.code_columns = a.c.row_bytes / (w ? 16 : 2);
+  a.scale_columns = cache->fmt == LQ_FMT_F16 ? 0 : a.c.head_dim / 32;
+  const int64_t columns = 2LL * a.c.kv_heads * (a.code_columns + a.scale_columns);
+  const dim3 grid(static_cast<unsigned>(a.b.batch), static_cast<unsigned>((columns + kKeepThreads - 1) / kKeepThreads));
+  if (grid.y > 65535) return LQ_ERR_UNSUPPORTED;
+  const void* kernel = w ? reinterpret_cast<const void*>(keep_kernel<uint4>) : reinterpret_cast<const void*>(keep_kernel<unsigned short>);
+  return launch(kernel, grid, kKeepThreads, &a, static_cast<cudaStream_t>(stream));
+}
+
+lq_status lq_kv_copy(const lq_kv_cache* cache, const int32_t* copies, int64_t n, void* stream) {
+  lq_kv_batch any = {};  // no tokens: the cache alone is checked
+  bool noop;
+  const lq_status st = kv_check(cache, &any, &noop);
+  if (st != LQ_OK) return st;
+  if (n < 0) return LQ_ERR_INVALID_ARG;
+  if (n == 0 || cache->num_pages == 0) return LQ_OK;
+  if (!cache->k || !cache->v || !aligned_to(cache->k, 2) || !aligned_to(cache->v, 2) || !copies || !aligned_to(copies, 4))
+    return LQ_ERR_INVALID_ARG;
+  const int64_t most = (1LL << 31) - 1;
+  if (cache->head_dim > 256 || cache->num_pages > most || cache->kv_heads > 4096 || n > most) return LQ_ERR_UNSUPPORTED;
+  CopyArgs a = {};
+  a.c = kv_cache_view(*cache);
+  a.copies = copies;
+  const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>(2 * a.c.kv_heads));
+  const void* kernel = wide(a.c) ? reinterpret_cast<const void*>(copy_kernel<uint4>) : reinterpret_cast<const void*>(copy_kernel<unsigned short>);
+  return launch(kernel, grid, kCopyThreads, &a, static_cast<cudaStream_t>(stream));
+}
+
+lq_status lq_beam_pages(const int32_t* parent, int64_t groups, int64_t beams, const int32_t* table, int64_t max_pages,
+                        const int32_t* kv_len, int64_t page_size, int32_t* table_out, int32_t* copies, void* stream) {
+  if (groups < 0 || beams < 1 || max_pages < 0 || page_size < 1 || page_size > 65536) return LQ_ERR_INVALID_ARG;
+  if (beams > LQ_BEAM_MAX || groups * beams > (1LL << 30) || max_pages * page_size > (1LL << 30)) return LQ_ERR_UNSUPPORTED;
+  if (groups == 0) return LQ_OK;
+  for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(kv_len), static_cast<const void*>(copies)})
+    if (!p || !aligned_to(p, 4)) return LQ_ERR_INVALID_ARG;
+  if (max_pages > 0 && (!table || !table_out || !aligned_to(table, 4) || !aligned_to(table_out, 4) || table == table_out))
+    return LQ_ERR_INVALID_ARG;
+  PagesArgs a = {};
+  a.parent = parent;
+  a.table = table;
+  a.len = kv_len;
+  a.out = table_out;
+  a.copies = copies;
+  a.beams = static_cast<int>(beams);
+  a.max_pages = static_cast<int>(max_pages);
+  a.page_size = static_cast<int>(page_size);
+  const int64_t parts = std::min<int64_t>(std::max<int64_t>((max_pages + kMapThreads - 1) / kMapThreads, 1), 64);
+  const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(parts));
+  return launch(reinterpret_cast<const void*>(pages_kernel), grid, kMapThreads, &a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -423,6 +423,138 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
                         float* O, int64_t ldo, float* lse, int64_t heads, float scale, int64_t window,
                         int64_t sinks, void* work, void* stream);
 
+/* ---- rotary positions ------------------------------------------------------
+ * Pair j of a head's first rotary_dim values is turned by the angle
+ * t = positions[axis(j)] * freq_j, and multiplied by `factor`:
+ *     y_a = factor (x_a cos t - x_b sin t),  y_b = factor (x_b cos t + x_a sin t);
+ * the values behind them stay as they are. A pair is values (j, j +
+ * rotary_dim / 2) (LQ_ROPE_HALVES) or (2j, 2j + 1) (LQ_ROPE_ADJACENT).
+ *
+ * lq_rope_init fills a table (HOST memory; plain CPU code), which a program keeps:
+ *   freqs: rotary_dim / 2 angles a position, or NULL for base^(-2j / rotary_dim);
+ *   axes (1..LQ_ROPE_MAX_AXES): the rows of `positions`, say time, height and
+ *     width; sections[axes]: how many pairs go by each, rotary_dim / 2 in all
+ *     (NULL with one axis). interleaved == 0: the first sections[0] pairs by axis
+ *     0, the next sections[1] by axis 1 and so on; else pair j by axis j % axes
+ *     while j < axes * sections[j % axes], and by axis 0 beyond.
+ *   rotary_dim and head_dim even, rotary_dim <= head_dim, frequencies of at most
+ *   2^32 in size, base > 0, base and factor finite, sections not negative and as
+ *   said, interleaved ones such that each axis gets its number, else
+ *   LQ_ERR_INVALID_ARG; rotary_dim >
+ *   2 * LQ_ROPE_MAX_PAIRS, more axes or head_dim > 65536 -> LQ_ERR_UNSUPPORTED.
+ *
+ * lq_rope turns the rows of Q (heads * head_dim floats, into QO) and of K
+ * (kv_heads, into KO) in one launch, each with a leading dimension in floats;
+ * heads or kv_heads 0: that side is left out. QO may be Q (and KO K) with the same
+ * leading dimension; any other overlap is not allowed. positions: DEVICE
+ * int32, row x at positions + x * ldp, any sign. inverse != 0 turns backwards (and
+ * multiplies by factor all the same). Angles are exact to 2^-31 of a turn at every
+ * position; the result is within 6 * 2^-24 of |factor| (|x_a| + |x_b|). */
+#define LQ_ROPE_MAX_PAIRS 128
+#define LQ_ROPE_MAX_AXES 4
+enum { LQ_ROPE_HALVES = 0, LQ_ROPE_ADJACENT = 1 };
+typedef struct {
+  int32_t  head_dim, rotary_dim, pairs, axes;
+  float    factor;
+  int32_t  reserved;
+  uint64_t turns[LQ_ROPE_MAX_PAIRS]; /* of a pair at position 1, in 2^-64 turns */
+  uint8_t  axis[LQ_ROPE_MAX_PAIRS];
+} lq_rope_table;
+lq_status lq_rope_init(lq_rope_table* table, int64_t head_dim, int64_t rotary_dim, int pairs, double base,
+                       const double* freqs, int64_t axes, const int32_t* sections, int interleaved,
+                       double factor);
+lq_status lq_rope(const lq_rope_table* table, int64_t tokens, const int32_t* positions, int64_t ldp,
+                  const float* Q, int64_t ldq, float* QO, int64_t ldqo, int64_t heads, const float* K,
+                  int64_t ldk, float* KO, int64_t ldko, int64_t kv_heads, int inverse, void* stream);
+
+/* ---- trees of drafted tokens -------------------------------------------------
+ * A step verifies drafted tokens in one call: a sequence's new tokens are the
+ * nodes of a tree. parent[t] (DEVICE, tokens entries) is the number, within its
+ * sequence's rows, of the row that row t follows; anything that is not below t's
+ * own number (-1, say) makes it a root. Row r of a sequence is stored in slot base
+ * + r, base = kv_len - rows, as lq_kv_write does; its position in the text is
+ * base + its depth.
+ *
+ * lq_tree_plan: from the parents, once a step,
+ *   positions (NULL or tokens): base + depth, for lq_rope and lq_attn_tree;
+ *   mask (NULL or tokens * mask_words): bit a (of word a / 32) of row t is set
+ *     where row a of its sequence is t itself or an ancestor and, with window >
+ *     0, less than `window` positions before it or below position `sinks`.
+ *   mask_words 1..LQ_TREE_MAX_WORDS: 32 rows each; rows beyond get no bits.
+ *
+ * lq_attn_tree: lq_attn_paged where row t sees, of the keys before base, what its
+ *   window and sinks leave (by positions[t], taken as within base .. kv_len - 1;
+ *   positions may be NULL with window 0) and of the sequence's new tokens those
+ *   that its bits name, whichever they are. A row with neither gets zeros, and
+ *   -inf in lse. All else (work, lse, precision, refusals) as lq_attn_paged.
+ *
+ * lq_tree_accept: the longest path that the model's own choices confirm. token[t]:
+ *   row t's token; target[t]: the model's choice after row t. The path starts with
+ *   row 0 and goes on to the lowest row whose parent is the last one and whose
+ *   token is target[last]. Its rows go to keep (batch * max_keep, -1 behind the
+ *   path, which ends at max_keep rows), their number to count (batch), target[last]
+ *   to next (batch; -1 without rows) and base + count to kept_len (batch, not
+ *   kv_len itself: lq_kv_keep needs the batch as it was).
+ *
+ * lq_kv_keep: moves row keep[i * max_keep + k] of sequence i's new tokens to the
+ *   slot of row k, for k < count[i], keys and values, in place: with kv_len =
+ *   kept_len the cache goes on behind the path. keep must ascend: the list ends at
+ *   the first entry that does not, or is not a row. What has no page is not moved. */
+#define LQ_TREE_MAX_WORDS 65536
+lq_status lq_tree_plan(const lq_kv_batch* batch, const int32_t* parent, int32_t* positions, uint32_t* mask,
+                       int64_t mask_words, int64_t window, int64_t sinks, void* stream);
+lq_status lq_attn_tree(const lq_kv_cache* cache, const lq_kv_batch* batch, const uint32_t* mask,
+                       int64_t mask_words, const int32_t* positions, const float* Q, int64_t ldq, float* O,
+                       int64_t ldo, float* lse, int64_t heads, float scale, int64_t window, int64_t sinks,
+                       void* work, void* stream);
+lq_status lq_tree_accept(const lq_kv_batch* batch, const int32_t* parent, const int32_t* token,
+                         const int32_t* target, int32_t* keep, int64_t max_keep, int32_t* count,
+                         int32_t* next, int32_t* kept_len, void* stream);
+lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const int32_t* keep,
+                     int64_t max_keep, const int32_t* count, void* stream);
+
+/* ---- beam search ---------------------------------------------------------------
+ * lq_beam_select: the k best continuations of each group of `beams` rows, by
+ *     scores[b] + (logits[b, j] - log sum_j exp(logits[b, j])),
+ *   best first: out_scores (f32), out_parents (the beam within its group) and
+ *   out_tokens, groups * k each. Scores are compared in 64 bits; equal ones go by the
+ *   lower beam, then the larger logit, then the lower token. Logits and scores of NaN
+ *   or -inf are never chosen (a row with NaN or +inf among its logits gives no
+ *   candidate); with fewer than k candidates the rest are (-inf, -1, -1). finished
+ *   (NULL or groups * beams): beams other than 0 stand for one candidate, their
+ *   score as it is and token `pad`; their logits are not read.
+ *   logits: row b of group g at logits + (g * beams + b) * ld. work:
+ *   lq_beam_work_bytes(...) bytes of DEVICE memory, 16-byte aligned, zero-filled
+ *   before its first use; each call leaves it ready for the next of the same
+ *   sizes, one call at a time (0 for sizes out of range).
+ *   ld >= vocab, 0 <= pad < vocab, else LQ_ERR_INVALID_ARG; beams or k >
+ *   LQ_BEAM_MAX, vocab > 2^26 or more than 2^24 rows -> LQ_ERR_UNSUPPORTED.
+ *
+ * lq_beam_pages: the beams' page tables (groups * beams rows of max_pages) for the
+ *   beams that go on from parent[] (beam numbers within the group). The beams of a
+ *   group have one length, kv_len of its first; full pages are shared, the last,
+ *   partly filled one and those behind it are each beam's own. The first child of a
+ *   beam goes on in its parent's own pages; the m-th of the other children takes
+ *   the own pages of the group's m-th beam without a child, and copies names
+ *   what has to be copied into the first of them: groups * beams entries (from
+ *   page, to page, tokens), (-1, -1, 0) where nothing is. So every own page keeps
+ *   one owner and no copy's target is a source. A parent outside 0 .. beams - 1 gives the
+ *   beam such pages too, and the table of the beam that it takes them from.
+ *   table_out must not be table.
+ * lq_kv_copy: the first `tokens` tokens of page `from` to page `to`, keys and
+ *   values of every head, for n such entries (as above; pages outside the pool and
+ *   counts below 1 are passed over). No entry's target may be another's source or
+ *   target. A model copies in each of its layers' caches with one list. */
+#define LQ_BEAM_MAX 64
+size_t    lq_beam_work_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k);
+lq_status lq_beam_select(const float* logits, int64_t ld, const float* scores, int64_t groups, int64_t beams,
+                         int64_t vocab, int64_t k, const int32_t* finished, int32_t pad, float* out_scores,
+                         int32_t* out_parents, int32_t* out_tokens, void* work, void* stream);
+lq_status lq_beam_pages(const int32_t* parent, int64_t groups, int64_t beams, const int32_t* table,
+                        int64_t max_pages, const int32_t* kv_len, int64_t page_size, int32_t* table_out,
+                        int32_t* copies, void* stream);
+lq_status lq_kv_copy(const lq_kv_cache* cache, const int32_t* copies, int64_t n, void* stream);
+
 /* ---- status ---------------------------------------------------------- */
 const char* lq_status_string(lq_status s);
 /* Synchronises the current device, then reads and clears its device status
