@@ -520,19 +520,43 @@ class Rope:
         self.head_dim, self.axes = int(head_dim), axes
 
 
+_int32 = _float32 = None  # torch's types, once it is there (comparing them is the quickest check)
+
+
+def _types():
+    global _int32, _float32
+    import torch
+    _int32, _float32 = torch.int32, torch.float32
+    return True
+
+
+def _ints(x, shape, gpu, what, name):
+    """The address of a contiguous int32 tensor of this shape on this GPU."""
+    if _int32 is None:
+        _types()
+    if x.dtype is not _int32 or x.shape != shape or x.get_device() != gpu or gpu < 0 or not x.is_contiguous():
+        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: {name} is a contiguous int32 {list(shape)} on the same GPU, got {list(x.shape)} "
+                                          f"{x.dtype} on {x.device}")
+    return x.data_ptr()
+
+
 def _head_rows(x, tokens, D, gpu, what):
     """(address, leading dimension, heads) of float32 rows [tokens, heads, D] or
     [tokens, heads * D] on one GPU."""
     shape, strides = x.shape, x.stride()
     rank = len(shape)
-    ok = 2 <= rank <= 3 and shape[0] == tokens and x.dtype.itemsize == 4 and x.is_floating_point() and x.get_device() == gpu >= 0
-    if ok:
-        width = shape[1] if rank == 2 else shape[1] * shape[2]
-        ok = width % D == 0 and (strides[-1] == 1 or shape[-1] == 1) and (rank == 2 or (shape[2] == D and (strides[1] == D or shape[1] == 1)))
-    if not ok:
+    ok = x.dtype is _float32 and x.get_device() == gpu >= 0
+    if ok and rank == 3:
+        n, heads, d = shape
+        ok = n == tokens and d == D and strides[2] == 1 and (strides[1] == D or heads == 1)
+    elif ok and rank == 2:
+        n, width = shape
+        heads = width // D
+        ok = n == tokens and heads * D == width and strides[1] == 1
+    if not ok or rank < 2 or rank > 3:
         raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 [{tokens}, heads, {D}] with contiguous heads and dims on one GPU wanted, "
                                           f"got {tuple(shape)} {x.dtype} on {x.device}, strides {strides}")
-    return x.data_ptr(), strides[0] if tokens > 1 else width, width // D
+    return x.data_ptr(), strides[0] if tokens > 1 else heads * D, heads
 
 
 def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, stream=None) -> None:
@@ -540,10 +564,12 @@ def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, s
     slices of a fused projection's rows allowed) by their positions (int32
     [tokens] or [axes, tokens]), in place or into q_out and k_out. See
     include/lq.h."""
-    tokens, gpu, D = Q.shape[0], Q.get_device(), rope.head_dim
-    shape = positions.shape
-    if positions.get_device() != gpu or str(positions.dtype) != "torch.int32" or shape[-1] != tokens or \
-            (rope.axes > 1 or len(shape) != 1) and (len(shape) != 2 or shape[0] != rope.axes) or (tokens > 1 and positions.stride(-1) != 1):
+    if _int32 is None:
+        _types()
+    tokens, gpu, D, axes = Q.shape[0], Q.get_device(), rope.head_dim, rope.axes
+    shape, ldp = positions.shape, positions.stride()
+    if shape != (axes, tokens) and (axes > 1 or shape != (tokens,)) or positions.dtype is not _int32 or positions.get_device() != gpu \
+            or tokens > 1 and ldp[-1] != 1:
         raise LQError(LQ_ERR_INVALID_ARG, f"lq_rope: int32 positions [{rope.axes}, {tokens}] on Q's GPU, contiguous along the tokens")
     q, ldq, heads = _head_rows(Q, tokens, D, gpu, "lq_rope")
     qo, ldqo, n = (q, ldq, heads) if q_out is None else _head_rows(q_out, tokens, D, gpu, "lq_rope")
@@ -553,19 +579,11 @@ def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, s
         ko, ldko, m = (k, ldk, kv_heads) if k_out is None else _head_rows(k_out, tokens, D, gpu, "lq_rope")
     if n != heads or m != kv_heads or (K is None and k_out is not None):
         raise LQError(LQ_ERR_INVALID_ARG, "lq_rope: q_out and k_out have the shapes of Q and K")
-    st = (_lib or lib()).lq_rope(rope.ref, tokens, positions.data_ptr(), positions.stride(0) if len(shape) == 2 else tokens, q, ldq, qo, ldqo,
+    st = (_lib or lib()).lq_rope(rope.ref, tokens, positions.data_ptr(), ldp[0], q, ldq, qo, ldqo,
                                  heads, k, ldk, ko, ldko, kv_heads, 1 if inverse else 0,
                                  _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "lq_rope")
-
-
-def _ints(x, shape, gpu, what, name):
-    """The address of a contiguous int32 tensor of this shape on this GPU."""
-    if x.shape != shape or str(x.dtype) != "torch.int32" or not x.is_contiguous() or x.get_device() != gpu or gpu < 0:
-        raise LQError(LQ_ERR_INVALID_ARG, f"{what}: {name} is a contiguous int32 {list(shape)} on the same GPU, got {list(x.shape)} "
-                                          f"{x.dtype} on {x.device}")
-    return x.data_ptr()
 
 
 def lq_tree_plan(batch, parent, positions=None, mask=None, window=0, sinks=0, stream=None) -> None:
@@ -649,9 +667,11 @@ def lq_beam_select(logits, scores, beams, k, out_scores, out_parents, out_tokens
     (n, vocab), gpu = logits.shape, logits.get_device()
     groups = n // beams if beams > 0 else 0
     ok = gpu >= 0 and groups * beams == n and (logits.stride(1) == 1 or vocab == 1)
-    for x, shape in ((logits, (n, vocab)), (scores, (n,)), (out_scores, (groups, k))):
-        ok = ok and x.shape == shape and x.dtype.itemsize == 4 and x.is_floating_point() and x.get_device() == gpu \
-            and (x is logits or x.is_contiguous())
+    if _int32 is None:
+        _types()
+    ok = ok and logits.dtype is _float32
+    for x, shape in ((scores, (n,)), (out_scores, (groups, k))):
+        ok = ok and x.dtype is _float32 and x.shape == shape and x.get_device() == gpu and x.is_contiguous()
     if not ok:
         raise LQError(LQ_ERR_INVALID_ARG, f"{what}: float32 logits [groups * beams, vocab], contiguous scores [groups * beams] and "
                                           "out_scores [groups, k] on one GPU")

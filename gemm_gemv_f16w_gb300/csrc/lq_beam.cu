@@ -4,29 +4,39 @@
 //     score_b + (x_bj - lse_b),   lse_b = log sum_j exp(x_bj).
 // Within a beam that is the order of x itself, so one pass over the logits gives
 // each part of a row its k best logits and its share of the sum, and only those
-// candidates ever get a score. lse_b and the scores are held in 64 bits: beams
-// are compared across lse's, where f32's steps (5e-7 at 8) would be ties.
+// candidates ever get a score. lse_b and the scores are held in two f32 parts (48 bits;
+// 64-bit arithmetic is slow on this chip and cost the join 4 us): beams are compared
+// across lse's, where f32's steps (5e-7 at 8) would be ties.
 //
 // The sum. A thread keeps a running maximum M and S = sum 2^(c (x - M)), c = log2(e),
 // in f32; x - M is taken first, so that roundings weigh on distances from the maximum
 // only (and a row of the type's lowest value is a row like any other). Of the
 // terms' errors (2^-22 each) the sum of a vocabulary keeps next to nothing.
 //
-// The candidates. The k-th largest of the 256 threads' first maxima (16 logits
-// each) is at most the part's k-th largest logit: from then on only logits above it
-// are noted, in shared memory, a few per cent of k more than are needed. The
-// notes hold one round of 4096 logits whatever they are; should they run full
-// (rows that grow, rows of one value) the best k are picked and the limit is raised.
+// The candidates. If each of the 8 warps has ceil(k / 8) maxima (of what a thread has
+// seen) at or above a limit, k logits of the part are: the least of the warps'
+// ceil(k / 8)-th largest maxima, taken in the 1st, 4th, 16th ... round of 4096 logits,
+// costs a sort of 32 values by shuffles. Of the 16 logits that a thread has of a round
+// only the largest is noted, and only at or above the limit: the k best logits are
+// among the 16 of the k best notes (were one in another, k notes would rank above it),
+// and those few are read once more when the part ends. Should the notes run full (rows
+// that grow, rows of one value) the warps meet, the best k stay and the limit rises.
 // Keys (logit, lower token first) are distinct, so that k of them are well defined and
 // the result does not depend on the order in which threads took notes.
 //
-// Split. A row is cut into parts so that all parts fill the SMs evenly (plan_parts);
-// the last part of a group to arrive joins them: the sums of each beam by a
-// warp, then k rounds in which the best of all lists' heads is taken.
+// Split. The rounds of all rows that are read are dealt to the CTAs in equal
+// contiguous ranges; a range's part of a row leaves k candidates and (M, S). Each warp
+// streams its own 512 logits of a round by asynchronous copies, two rounds ahead and
+// across rows, and no warp waits for another but where a limit is taken or a row ends.
+// A second kernel, a CTA a group, joins the parts: the sums of each beam by a warp, a
+// limit from the lists' first entries, and the best k of what is at or above it. (Joined by the
+// last part to arrive instead, whose range then ends late, 32 groups of 8 beams over a
+// vocabulary of 151936 take 67 us.)
 //
 // What bounds it: logits are read once, HBM. An ended beam (one candidate, its score
 // as it is) and one with a score of -inf are not read at all.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "lq_argmax.cuh"
@@ -42,9 +52,13 @@ __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_beam_
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPer = 16;                   // logits of a thread and round
 constexpr int kRound = kThreads * kPer;
-constexpr int kNotes = kRound + 1024;      // room for a round behind what was noted before
-constexpr int kSlots = 152 * 4;            // CTAs that the parts are planned for
-constexpr int kMaxParts = 64;
+constexpr int kStages = 3;                 // rounds in shared memory
+constexpr int kStep = kThreads;            // notes that all warps may take between two looks at their number
+constexpr int kNotes = 4 * kStep;
+constexpr int kCtas = 152 * 3;             // ranges that the rounds are dealt to
+constexpr int kScanRows = 4096;            // rows up to which those that are not read are left out of the deal
+constexpr int kPicks = 1024;               // candidates that a join ranks together
+constexpr int kAtOnce = 2;                 // of a list, in a join
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTokenBits = 26;             // of a vocabulary
 
@@ -55,11 +69,14 @@ struct BeamArgs {
   float* out_scores;
   int* out_parents;
   int* out_tokens;
-  int* counters;                // [groups]; zero between calls
-  float2* sums;                 // [rows][parts]: M and S
-  unsigned long long* lists;    // [rows][parts][k], best first, 0: none
+  int* per;                     // rounds of a range
+  int* number;                  // [rows]: of a row among those that are read
+  float2* sums;                 // [parts]: M and S
+  unsigned long long* lists;    // [parts][k], best first, 0: none
   long long ld;
-  int beams, vocab, k, pad, parts, chunk;
+  int rows, beams, vocab, k, pad;
+  int rounds;                   // of a row
+  int scan;                     // the rows that are not read are left out of the deal
 };
 
 // A candidate of the join: its score, then (equal scores) the lower beam, the
@@ -68,17 +85,40 @@ struct Pick {
   unsigned long long hi, lo;
 };
 
-// Shared memory, first of a part, then of the join.
+__device__ __forceinline__ bool better(const Pick& a, const Pick& b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
+__device__ __forceinline__ bool better(unsigned long long a, unsigned long long b) { return a > b; }
+__device__ __forceinline__ bool is(const Pick& p) { return p.hi != 0ull; }
+__device__ __forceinline__ bool is(unsigned long long k) { return k != 0ull; }
+
+// A number in two parts, the first its value in f32.
+struct Pair {
+  float hi, lo;
+};
+
+// A part's shared memory besides the rounds.
 struct Notes {
-  unsigned long long key[kNotes];
-  alignas(16) unsigned long long few[kThreads];
+  unsigned long long key[kNotes];  // the largest of a thread's round
+  unsigned long long all[LQ_BEAM_MAX * kPer];  // the logits of the best notes' rounds
+  unsigned long long few[kThreads];
   float2 sum[kWarps];
+  float limit[kWarps];
 };
 struct Join {
-  double lse[LQ_BEAM_MAX];
-  unsigned char taken[LQ_BEAM_MAX * kMaxParts];  // of a list
-  Pick win[2][kWarps];
-  int win_list[2][kWarps];
+  Pick pick[kPicks];
+  Pick few[kThreads];
+  Pair lse[LQ_BEAM_MAX];
+  unsigned long long limit[kWarps];
+  float score[LQ_BEAM_MAX], base[LQ_BEAM_MAX];  // base NaN: an ended beam
+  int start[LQ_BEAM_MAX + 1], part[LQ_BEAM_MAX];  // lists before a beam's, and its first part
+  int count;
+};
+constexpr int kRing = kStages * kRound * 4;
+constexpr int kSmem = kRing + static_cast<int>(sizeof(Notes));
+
+// Rows before row r that are read (s.before: of r / q; q: rows a thread counted).
+struct Scan {
+  int before[kThreads + 1];
+  int warp[kWarps];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -90,322 +130,510 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
   const unsigned hi = static_cast<unsigned>(key >> 32);
   return __uint_as_float((hi & 0x80000000u) ? (hi & 0x7FFFFFFFu) : ~hi);
 }
-// The next float above a finite one.
-__device__ __forceinline__ float above(float x) {
-  if (x == 0.0f) return __uint_as_float(1u);
-  const int i = __float_as_int(x);
-  return __int_as_float(x > 0.0f ? i + 1 : i - 1);
-}
-
-// The k-th largest of the block's keys, one a thread (distinct or zero); 0 if
-// there are fewer. few[] is scratch; every thread takes part.
-__device__ __forceinline__ unsigned long long kth_of_block(unsigned long long mine, int k, unsigned long long* few, unsigned long long* out) {
-  const int tid = static_cast<int>(threadIdx.x);
-  few[tid] = mine;
-  if (tid == 0) *out = 0ull;
-  __syncthreads();
-  int before = 0;
-#pragma unroll 8
-  for (int j = 0; j < kThreads; j += 2) {
-    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(few + j);
-    before += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+// The warp's values in descending order, one a lane.
+template <class T>
+__device__ __forceinline__ T sorted(T x, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+      const T y = __shfl_xor_sync(0xffffffffu, x, step);
+      const bool larger = ((lane & step) == 0) == ((lane & size) == 0);  // this lane keeps the larger one
+      x = larger == (x > y) ? x : y;
+    }
   }
-  if (mine != 0ull && before == k - 1) *out = mine;
-  __syncthreads();
-  const unsigned long long t = *out;
-  __syncthreads();  // few and out are free
-  return t;
+  return x;
 }
 
-// Leaves the best min(k, n) of the n noted keys, best first, in key[0 .. ).
-__device__ __forceinline__ int best_notes(Notes& s, int n, int k) {
+// Leaves the best min(k, n) of n distinct keys, best first, in key[0 .. ), by the
+// whole block; few[kThreads] is scratch.
+template <class K>
+__device__ __noinline__ int best_of(K* key, K* few, int n, int k) {
   const int tid = static_cast<int>(threadIdx.x);
-  __shared__ unsigned long long limit;
   __shared__ int fewer;
-  // No more than k threads have a largest key at or above the k-th largest of
-  // them, and every one of the best k is at or above it: at most k / 256 of the
-  // notes stay, rounded up a thread, so that the loop ends.
+  // Each thread's best, and of those the k-th: no more than k threads have keys at or
+  // above it, and every one of the best k is. So at most k / 256 of the keys
+  // stay, rounded up a thread, and the loop ends.
   while (n > kThreads) {
-    unsigned long long mine = 0ull;
-    for (int i = tid; i < n; i += kThreads) mine = s.key[i] > mine ? s.key[i] : mine;
-    const unsigned long long least = kth_of_block(mine, k, s.few, &limit);
-    // in place: a round of the block's reads lies ahead of its writes
+    K mine = {};
+    for (int i = tid; i < n; i += kThreads) mine = better(key[i], mine) ? key[i] : mine;
+    few[tid] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < kThreads; ++j) before += better(few[j], mine) ? 1 : 0;
+    __syncthreads();
+    if (before == k - 1) few[0] = mine;
     if (tid == 0) fewer = 0;
     __syncthreads();
+    const K least = few[0];
+    // in place: a round of the block's reads lies ahead of its writes
     for (int i0 = 0; i0 < n; i0 += kThreads) {
-      const unsigned long long key = i0 + tid < n ? s.key[i0 + tid] : 0ull;
+      K x = {};
+      if (i0 + tid < n) x = key[i0 + tid];
       __syncthreads();
-      if (key != 0ull && key >= least) s.key[atomicAdd(&fewer, 1)] = key;
+      if (is(x) && !better(least, x)) key[atomicAdd(&fewer, 1)] = x;
       __syncthreads();
     }
     n = fewer;
     __syncthreads();
   }
-  const unsigned long long key = tid < n ? s.key[tid] : 0ull;
-  int rank = 0;
-  for (int j = 0; j < n; ++j) rank += s.key[j] > key ? 1 : 0;
+  K x = {};
+  int rank = k;
+  if (tid < n) {
+    x = key[tid];
+    rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += better(key[j], x) ? 1 : 0;
+  }
   __syncthreads();
-  if (key != 0ull && rank < k) s.key[rank] = key;
+  if (rank < k) key[rank] = x;
   __syncthreads();
   return min(n, k);
 }
 
-__device__ __forceinline__ bool better(const Pick& a, const Pick& b) { return a.hi != b.hi ? a.hi > b.hi : a.lo > b.lo; }
-__device__ __forceinline__ Pick pick_of(double score, int beam, unsigned long long key) {
+__device__ __forceinline__ Pair sum_of(float a, float b) {  // exactly
+  const float t = a + b, v = t - a;
+  return {t, (a - (t - v)) + (b - v)};
+}
+__device__ __forceinline__ Pair sum_of(const Pair& a, float b) {
+  const Pair t = sum_of(a.hi, b);
+  return sum_of(t.hi, t.lo + a.lo);
+}
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned u = __float_as_uint(x + 0.0f);  // -0 as +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ Pick pick_of(const Pair& score, int beam, unsigned long long key) {
   Pick p = {0ull, 0ull};
-  if (!(score > -INFINITY)) return p;  // -inf, NaN
-  score += 0.0;                        // -0 as +0
-  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(score));
-  p.hi = (u >> 63) ? ~u : (u | (1ull << 63));
+  if (!(score.hi > -INFINITY)) return p;  // -inf, NaN
+  p.hi = static_cast<unsigned long long>(ordered(score.hi)) << 32 | ordered(score.lo);
   const unsigned token = 0xFFFFFFFFu - static_cast<unsigned>(key);
   p.lo = (static_cast<unsigned long long>(LQ_BEAM_MAX - 1 - beam) << 58) | ((key >> 32) << kTokenBits) | ((1u << kTokenBits) - 1u - token);
   return p;
 }
 
-// The group's k best from the parts' lists, by the whole block.
-__device__ void join(const BeamArgs& a, Join& s, int group) {
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int row0 = group * a.beams, lists = a.beams * a.parts;
-  for (int b = warp; b < a.beams; b += kWarps) {
-    const bool read = !(a.finished && a.finished[row0 + b] != 0) && a.scores[row0 + b] > -INFINITY;
-    double l = 0.0;
-    if (read) {
-      float2 mine[kMaxParts / 32];
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kMaxParts / 32; ++i) {
-        const int p = i * 32 + lane;
-        mine[i] = p < a.parts ? __ldcg(a.sums + static_cast<long long>(row0 + b) * a.parts + p) : make_float2(-INFINITY, 0.0f);
-        top = fmaxf(top, mine[i].x);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kMaxParts / 32; ++i)
-        if (i * 32 + lane < a.parts) sum += mine[i].y * expf(mine[i].x - base);
-      sum = warp_sum(sum);
-      l = static_cast<double>(base) + log(static_cast<double>(sum));
-    }
-    if (lane == 0) s.lse[b] = l;
+__device__ __forceinline__ bool is_read(const BeamArgs& a, int row) {
+  return a.scores[row] > -INFINITY && !(a.finished && a.finished[row] != 0);
+}
+
+// How the rounds are dealt: CTA c has rounds [c per, (c + 1) per) of the rows that are
+// read, in order; the part of the l-th such row that CTA c has is number l + c.
+struct Deal {
+  int per, rounds;
+  __device__ __forceinline__ int cta_of(long long x) const {  // (the 32-bit division where it will do)
+    return (x >> 31) == 0 ? static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(per)) : static_cast<int>(x / per);
   }
-  for (int i = tid; i < lists; i += kThreads) s.taken[i] = 0;
+  __device__ __forceinline__ int first_cta(int l) const { return cta_of(static_cast<long long>(l) * rounds); }
+  __device__ __forceinline__ int last_cta(int l) const { return cta_of(static_cast<long long>(l) * rounds + rounds - 1); }
+};
+
+// The group's k best from its parts' lists.
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
+  __shared__ Join s;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int group = static_cast<int>(blockIdx.x), row0 = group * a.beams;
+  if (warp == 0) {  // two beams a lane
+    int n[2], before = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = 2 * lane + h;
+      n[h] = 0;
+      if (b < a.beams) {
+        const float score = a.scores[row0 + b];
+        s.score[b] = score;
+        if (a.finished && a.finished[row0 + b] != 0) {
+          s.base[b] = NAN;  // its logits give no candidate
+        } else if (!a.scan || score > -INFINITY) {
+          Deal deal;
+          deal.per = __ldcg(a.per);
+          deal.rounds = a.rounds;
+          const int l = __ldcg(a.number + row0 + b), c0 = deal.first_cta(l);
+          s.part[b] = l + c0;
+          n[h] = deal.last_cta(l) - c0 + 1;
+          s.base[b] = 0.0f;
+        }
+      }
+      before += n[h];
+    }
+    int incl = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    s.start[2 * lane] = incl - before;
+    s.start[2 * lane + 1] = incl - before + n[0];
+    if (lane == 31) s.start[LQ_BEAM_MAX] = incl;
+    if (lane == 0) s.count = 0;
+  }
   __syncthreads();
-  auto head = [&](int list, int taken) -> Pick {
-    const Pick none = {0ull, 0ull};
-    const int b = list / a.parts, part = list - b * a.parts;
-    const float score = a.scores[row0 + b];
-    if (a.finished && a.finished[row0 + b] != 0) {  // as it is, with the padding token
-      if (part != 0 || taken != 0) return none;
-      return pick_of(static_cast<double>(score), b, amax::make_key(0.0f, static_cast<unsigned>(a.pad)));
-    }
-    if (!(score > -INFINITY) || taken >= a.k) return none;
-    const unsigned long long key = __ldcg(a.lists + (static_cast<long long>(row0 + b) * a.parts + part) * a.k + taken);
-    if (key == 0ull) return none;
-    return pick_of(static_cast<double>(score) + (static_cast<double>(value_of(key)) - s.lse[b]), b, key);
+  const int lists = s.start[LQ_BEAM_MAX];
+  auto beam_of = [&](int list) {
+    int b = 0;
+#pragma unroll 1
+    for (int step = LQ_BEAM_MAX / 2; step > 0; step /= 2)
+      if (b + step < a.beams && s.start[b + step] <= list) b += step;
+    return b;
   };
-  // a thread's lists: tid, tid + 256, ...; the best of their heads
-  auto best_here = [&](int& which) {
-    Pick p = {0ull, 0ull};
-    which = -1;
-    for (int i = tid; i < lists; i += kThreads) {
-      const Pick c = head(i, s.taken[i]);
-      if (better(c, p)) {
-        p = c;
-        which = i;
-      }
-    }
-    return p;
+  auto key_of = [&](int list, int b, int at) {
+    return at < a.k ? __ldcg(a.lists + static_cast<long long>(s.part[b] + list - s.start[b]) * a.k + at) : 0ull;
   };
-  int which;
-  Pick mine = best_here(which);
-  for (int r = 0; r < a.k; ++r) {
-    Pick p = mine;
-    int list = which;
+  // The first entries of the lists, one a thread and as many of each list as there are
+  // threads for (a warp's are of every eighth place: beams that are far ahead are in every
+  // warp), and the next ones of a thread's own list: asked for before the sums.
+  const int m = lists > 0 ? max(1, min(a.k, kThreads / lists)) : 1, place = lane * kWarps + warp, mine = place / m;
+  const int covered = kThreads / m, mine_beam = mine < lists ? beam_of(mine) : 0, own_beam = tid < lists ? beam_of(tid) : 0;
+  const unsigned long long mine_key = mine < min(lists, covered) ? key_of(mine, mine_beam, place - mine * m) : 0ull;
+  unsigned long long key[kAtOnce];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Pick q;
-      q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
-      q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
-      const int other = __shfl_xor_sync(0xffffffffu, list, o);
-      if (better(q, p)) {
-        p = q;
-        list = other;
-      }
+  for (int i = 0; i < kAtOnce; ++i) key[i] = tid < lists ? key_of(tid, own_beam, (tid < covered ? m : 0) + i) : 0ull;
+#pragma unroll 1
+  for (int b = warp; b < a.beams; b += kWarps) {
+    const int n = s.start[b + 1] - s.start[b];
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const float2 m = __ldcg(a.sums + s.part[b] + i);
+      const float to = fmaxf(top, m.x), ref = to == -INFINITY ? 0.0f : to;
+      sum = sum * expf(top - ref) + m.y * expf(m.x - ref);
+      top = to;
     }
+    float all = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    const float ref = all == -INFINITY ? 0.0f : all;
+    sum = warp_sum(sum * expf(top - ref));
+    // log sum: f32's logarithm, and by how much it misses the sum
+    const float l = logf(sum), miss = fmaf(sum, expf(-l), -1.0f);
     if (lane == 0) {
-      s.win[r & 1][warp] = p;
-      s.win_list[r & 1][warp] = list;
+      const Pair all_of = sum_of(sum_of(ref, l), miss);
+      s.lse[b] = s.base[b] != s.base[b] ? Pair{NAN, 0.0f} : all_of;
     }
-    __syncthreads();
-    p = s.win[r & 1][0];
-    list = s.win_list[r & 1][0];
+  }
+  __syncthreads();
+  auto scored = [&](unsigned long long key, int b) {
+    const Pick none = {0ull, 0ull};
+    if (key == 0ull) return none;
+    const Pair d = sum_of(value_of(key), -s.lse[b].hi), t = sum_of(s.score[b], d.hi);
+    return pick_of(sum_of(t, d.lo - s.lse[b].lo), b, key);
+  };
+  // ended beams: one candidate each
+  if (tid < a.beams && s.base[tid] != s.base[tid]) {
+    const Pick p = pick_of(Pair{s.score[tid], 0.0f}, tid, amax::make_key(0.0f, static_cast<unsigned>(a.pad)));
+    if (is(p)) s.pick[atomicAdd(&s.count, 1)] = p;
+  }
+  // A limit: with ceil(k / 8) of each warp's entries at or above it, k are.
+  const Pick p = scored(mine_key, mine_beam);
+  const unsigned long long nth = sorted(p.hi, lane);
+  if (lane == (a.k + kWarps - 1) / kWarps - 1) s.limit[warp] = nth;
+  __syncthreads();
+  unsigned long long limit = s.limit[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      if (better(s.win[r & 1][w], p)) {
-        p = s.win[r & 1][w];
-        list = s.win_list[r & 1][w];
+  for (int w = 1; w < kWarps; ++w) limit = min(limit, s.limit[w]);
+  limit = max(limit, 1ull);  // (scores' own are above it)
+  if (p.hi >= limit) s.pick[atomicAdd(&s.count, 1)] = p;
+  // The lists are sorted: a thread goes down the rest of each of its own until it is below.
+#pragma unroll 1
+  for (int i0 = 0; i0 < lists; i0 += kThreads) {
+    const int list = i0 + tid, at0 = list < covered ? m : 0;
+    bool on = list < lists;
+    const int b = i0 == 0 ? own_beam : (on ? beam_of(list) : 0);
+#pragma unroll 1
+    for (int at = 0; at < a.k; at += kAtOnce) {
+      if (i0 + at > 0) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) key[i] = on ? key_of(list, b, at0 + at + i) : 0ull;
       }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const Pick x = scored(key[i], b);
+        on = on && x.hi >= limit;
+        if (on) {
+          const int to = atomicAdd(&s.count, 1);
+          if (LQ_IN_BOUNDS(to < kPicks)) s.pick[to] = x;
+        }
+      }
+      const bool more = __syncthreads_or(on);
+      const int have = s.count;
+      __syncthreads();  // everyone has read it
+      if (have > kPicks - kAtOnce * kThreads) {
+        const int kept = best_of(s.pick, s.few, have, a.k);
+        if (tid == 0) s.count = kept;
+        __syncthreads();
+      }
+      if (!more) break;
     }
-    const long long out = static_cast<long long>(group) * a.k + r;
-    if (tid == 0) {
-      const bool none = p.hi == 0ull;
-      const unsigned long long u = (p.hi >> 63) ? (p.hi & ~(1ull << 63)) : ~p.hi;
-      const double score = __longlong_as_double(static_cast<long long>(u));
-      a.out_scores[out] = none ? -INFINITY : static_cast<float>(score);
-      a.out_parents[out] = none ? -1 : LQ_BEAM_MAX - 1 - static_cast<int>(p.lo >> 58);
-      a.out_tokens[out] = none ? -1 : static_cast<int>(((1u << kTokenBits) - 1u) - static_cast<unsigned>(p.lo & ((1u << kTokenBits) - 1u)));
-    }
-    if (list >= 0 && list % kThreads == tid) {  // its owner
-      ++s.taken[list];
-      mine = best_here(which);
-    }
+  }
+  __syncthreads();
+  const int n = best_of(s.pick, s.few, s.count, a.k);
+  if (tid < a.k) {
+    const long long out = static_cast<long long>(group) * a.k + tid;
+    const bool some = tid < n;
+    const Pick x = s.pick[some ? tid : 0];
+    constexpr unsigned kTokens = (1u << kTokenBits) - 1u;
+    a.out_scores[out] = some ? value_of(x.hi) : -INFINITY;
+    a.out_parents[out] = some ? LQ_BEAM_MAX - 1 - static_cast<int>(x.lo >> 58) : -1;
+    a.out_tokens[out] = some ? static_cast<int>(kTokens - (static_cast<unsigned>(x.lo) & kTokens)) : -1;
   }
 }
 
-// grid: x = part + parts * row
+// 16 (or 4) bytes; what is beyond `bytes` is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) beam_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
-  Notes& s = *reinterpret_cast<Notes*>(raw);
-  __shared__ unsigned long long limit;
-  __shared__ int last, count;  // count: notes taken
+  Notes& s = *reinterpret_cast<Notes*>(raw + kRing);
+  __shared__ Scan scan;
+  __shared__ int count;  // notes taken
   pdl_wait();
   pdl_launch_dependents();  // the next kernel's launch runs under this one; it waits for its end
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int row = static_cast<int>(blockIdx.x) / a.parts, part = static_cast<int>(blockIdx.x) - row * a.parts;
-  const bool read = !(a.finished && a.finished[row] != 0) && a.scores[row] > -INFINITY;
-  if (read) {
-    const int c0 = min(part * a.chunk, a.vocab), c1 = min(c0 + a.chunk, a.vocab);
-    const float* const x0 = a.logits + row * a.ld;
-    float M = -INFINITY, S = 0.0f;
-    float lim = -3.402823466e38f;   // logits from here on are noted
-    int noted = 0;
-    if (tid == 0) count = 0;
-#pragma unroll 1
-    for (int base = c0; base < c1; base += kRound) {
-      float v[kPer];
+  const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+  const int R = a.rounds;
+
+  // ---- the rows that are read, and this CTA's range of their rounds -----------------
+  const int q = a.scan ? (a.rows + kThreads - 1) / kThreads : 1;
+  int live = a.rows;
+  if (a.scan) {
+    int mine = 0;
+    for (int r = tid * q; r < min(tid * q + q, a.rows); ++r) mine += is_read(a, r) ? 1 : 0;
+    int incl = mine;
 #pragma unroll
-      for (int q = 0; q < kPer / 4; ++q) {
-        if constexpr (VEC) {  // (parts begin on multiples of four)
-          const int j = base + (q * kThreads + tid) * 4;
-          if (j + 3 < c1 && LQ_IN_BOUNDS(j >= 0 && j + 3 < a.vocab)) {
-            const float4 f = __ldcs(reinterpret_cast<const float4*>(x0 + j));
-            v[4 * q] = f.x;
-            v[4 * q + 1] = f.y;
-            v[4 * q + 2] = f.z;
-            v[4 * q + 3] = f.w;
-          } else {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) scan.warp[warp] = incl;
+    __syncthreads();
+    live = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) incl += live;
+      live += scan.warp[w];
+    }
+    scan.before[tid + 1] = incl;
+    if (tid == 0) scan.before[0] = 0;
+    __syncthreads();
+  }
+  auto is_live = [&](int r) { return !a.scan || is_read(a, r); };
+  Deal deal;
+  deal.rounds = R;
+  deal.per = static_cast<int>(max((static_cast<long long>(live) * R + ctas - 1) / ctas, 1ll));
+  if (cta == 0 && tid == 0) *a.per = deal.per;
+  const long long x0 = static_cast<long long>(cta) * deal.per, x1 = min(x0 + deal.per, static_cast<long long>(live) * R);
+  if (x0 >= x1) return;
+  int number = static_cast<int>(x0 / R), round = static_cast<int>(x0 - static_cast<long long>(number) * R);  // of the row; in it
+  int row = number;
+  if (a.scan) {  // the number-th row that is read
+    int at = 0;
+    for (int step = kThreads / 2; step > 0; step /= 2)
+      if (scan.before[at + step] <= number) at += step;
+    row = at * q;
+    for (int skip = number - scan.before[at];; ++row)
+      if (is_read(a, row) && skip-- == 0) break;
+  }
+  int left = static_cast<int>(x1 - x0);
+
+  // ---- copies, ahead of the work -------------------------------------------------------
+  float* const ring = reinterpret_cast<float*>(raw) + warp * (kRound / kWarps);
+  int copy_row = row, copy_round = round, copy_left = left, copy_stage = 0;
+  auto copy = [&]() {
+    if (copy_left > 0) {
+      const int base = copy_round * kRound + warp * (kRound / kWarps);
+      const float* const from = a.logits + copy_row * a.ld;
+      const uint32_t to = smem_u32(ring + copy_stage * kRound);
+      const int inside = a.vocab - base;  // logits of the row from there on
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * q + i] = j + i < c1 ? x0[j + i] : -INFINITY;
-          }
+      for (int n = 0; n < (VEC ? kPer / 4 : kPer); ++n) {
+        const int e = VEC ? (n * 32 + lane) * 4 : n * 32 + lane;
+        const int bytes = max(0, min(inside - e, VEC ? 4 : 1)) * 4;
+        const float* const at = bytes > 0 && LQ_IN_BOUNDS(copy_row >= 0 && copy_row < a.rows) ? from + base + e : a.logits;
+        if constexpr (VEC) {
+          copy16(to + e * 4, at, bytes);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = base + (4 * q + i) * kThreads + tid;
-            v[4 * q + i] = j < c1 && LQ_IN_BOUNDS(j >= 0 && j < a.vocab) ? __ldcs(x0 + j) : -INFINITY;
-          }
+          copy4(to + e * 4, at, bytes);
         }
+      }
+      --copy_left;
+      if (++copy_round == R) {
+        copy_round = 0;
+        ++copy_row;
+        if (copy_left > 0)
+          while (!is_live(copy_row)) ++copy_row;
+      }
+      copy_stage = copy_stage + 1 == kStages ? 0 : copy_stage + 1;
+    }
+    commit_copies();
+  };
+#pragma unroll
+  for (int n = 0; n < kStages - 1; ++n) copy();
+
+  int stage = 0;
+  // ---- the parts of rows ------------------------------------------------------------------
+#pragma unroll 1
+  while (left > 0) {
+    if (tid == 0) {
+      count = 0;
+      a.number[row] = number;
+    }
+    __syncthreads();
+    const int rounds = min(R - round, left);  // here
+    float M = -INFINITY, S = 0.0f, highest = -INFINITY;
+    float lim = -3.402823466e38f;     // logits above are noted, and those equal to it
+    int lim_token = 1 << kTokenBits;  // whose tokens are below this one
+    // The notes are full, or this warp has taken all of its own: the warps meet until none
+    // has more. The best k stay; what follows has to rank above the least of them.
+    auto meet = [&](bool done) {
+      if (!__syncthreads_or(!done)) return false;
+      const int kept = best_of(s.key, s.few, count, a.k);
+      if (kept == a.k) {
+        lim = value_of(s.key[a.k - 1]);
+        lim_token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(s.key[a.k - 1]));
+      }
+      if (tid == 0) count = kept;
+      __syncthreads();
+      return true;
+    };
+    int next_limit = 0;
+#pragma unroll 1
+    for (int i = 0; i < rounds; ++i, ++round) {
+      wait_copies<kStages - 2>();
+      float v[kPer];
+      const float* const at = ring + stage * kRound;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int n = 0; n < kPer / 4; ++n) {
+          const float4 f = *reinterpret_cast<const float4*>(at + (n * 32 + lane) * 4);
+          v[4 * n] = f.x;
+          v[4 * n + 1] = f.y;
+          v[4 * n + 2] = f.z;
+          v[4 * n + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < kPer; ++n) v[n] = at[n * 32 + lane];
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      copy();
+      const int base = round * kRound + warp * (kRound / kWarps);  // token of the warp's first
+      if (base + kRound / kWarps > a.vocab) {
+#pragma unroll
+        for (int n = 0; n < kPer; ++n)
+          if (base + (VEC ? ((n / 4) * 32 + lane) * 4 + n % 4 : n * 32 + lane) >= a.vocab) v[n] = -INFINITY;
       }
       float top = v[0];
 #pragma unroll
-      for (int i = 1; i < kPer; ++i) top = fmaxf(top, v[i]);
+      for (int n = 1; n < kPer; ++n) top = fmaxf(top, v[n]);
       // the sum
       const float to = fmaxf(M, top), ref = to == -INFINITY ? 0.0f : to;
       S *= ex2((M - ref) * kLog2e);
       M = to;
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 y = fmul2(fadd2(make_float2(v[i], v[i + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+      for (int n = 0; n < kPer; n += 2) {
+        const float2 y = fmul2(fadd2(make_float2(v[n], v[n + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
         sum = fadd2(sum, make_float2(ex2(y.x), ex2(y.y)));
       }
       S += sum.x + sum.y;
       // the candidates
-      if (base == c0) {
-        // (a thread's number tells equal maxima apart)
-        const unsigned long long t = kth_of_block(top > -INFINITY ? amax::make_key(top, static_cast<unsigned>(tid)) : 0ull, a.k, s.few, &limit);
-        if (t != 0ull) lim = value_of(t);
-      } else {
-        __syncthreads();  // the count of the round before is whole
-        noted = count;
-        if (noted + kRound > kNotes) {  // full: the best k stay, and what follows has to beat them all
-          __syncthreads();
-          noted = best_notes(s, noted, a.k);
-          if (noted == a.k) lim = fmaxf(lim, value_of(s.key[a.k - 1]) < INFINITY ? above(value_of(s.key[a.k - 1])) : INFINITY);
-          if (tid == 0) count = noted;
+      highest = fmaxf(highest, top);
+      if (i == next_limit) {
+        while (i > 0 && meet(true)) {
         }
+        const float nth = sorted(highest, lane);  // (a NaN is no maximum)
+        if (lane == (a.k + kWarps - 1) / kWarps - 1) s.limit[warp] = nth;
         __syncthreads();
-      }
-      if (top >= lim) {
+        float least = s.limit[0];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (v[i] >= lim) {
-            const int j = VEC ? base + ((i / 4) * kThreads + tid) * 4 + i % 4 : base + i * kThreads + tid;
-            const int at = atomicAdd(&count, 1);
-            if (LQ_IN_BOUNDS(at < kNotes)) s.key[at] = amax::make_key(v[i], static_cast<unsigned>(j));
+        for (int w = 1; w < kWarps; ++w) least = fminf(least, s.limit[w]);
+        if (least > lim) {
+          lim = least;
+          lim_token = 1 << kTokenBits;
+        }
+        next_limit = 4 * i + 3;
+      }
+      if (__any_sync(0xffffffffu, top >= lim)) {
+        // (eight warps take no more than kStep notes between this and their next looks)
+        while (__shfl_sync(0xffffffffu, *static_cast<volatile int*>(&count), 0) > kNotes - kStep) meet(false);
+        if (top >= lim) {
+          int n = kPer - 1;  // the first of the largest
+#pragma unroll
+          for (int m = kPer - 2; m >= 0; --m) n = v[m] == top ? m : n;
+          const int j = base + (VEC ? ((n / 4) * 32 + lane) * 4 + n % 4 : n * 32 + lane);
+          if (top > lim || j < lim_token) {
+            const int to_note = atomicAdd(&count, 1);
+            if (LQ_IN_BOUNDS(to_note < kNotes)) s.key[to_note] = amax::make_key(top, static_cast<unsigned>(j));
           }
         }
+        __syncwarp();
       }
     }
-    __syncthreads();
-    const int n = best_notes(s, c0 < c1 ? count : 0, a.k);
-    const long long at = static_cast<long long>(row) * a.parts + part;
-    if (tid < a.k) a.lists[at * a.k + tid] = tid < n ? s.key[tid] : 0ull;
+    left -= rounds;
     // the block's sum
     float top = M;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
     const float w = warp_sum(S * ex2((M - ref) * kLog2e));
+    while (meet(true)) {
+    }
     if (lane == 0) s.sum[warp] = make_float2(top, w);
+    const int notes = best_of(s.key, s.few, count, a.k);  // (a barrier, too)
+    if (tid == 0) count = 0;
     __syncthreads();
-    if (tid == 0) {
+    // the logits of the notes' rounds that are no worse than the last note
+    const unsigned long long least = notes == a.k ? s.key[a.k - 1] : 1ull;
+    for (int e = tid; e < notes * kPer; e += kThreads) {
+      const int j = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(s.key[e / kPer])), n = e % kPer;
+      const int within = j % (kRound / kWarps), first = j - within;  // of the warp's 512
+      const int token = first + (VEC ? (n / 4) * 128 + within % 128 / 4 * 4 + n % 4 : n * 32 + within % 32);
+      if (token >= a.vocab || !LQ_IN_BOUNDS(token >= 0)) continue;
+      const float x = a.logits[row * a.ld + token];
+      const unsigned long long key = x > -INFINITY ? amax::make_key(x, static_cast<unsigned>(token)) : 0ull;
+      if (key >= least) {
+        const int to = atomicAdd(&count, 1);
+        if (LQ_IN_BOUNDS(to < LQ_BEAM_MAX * kPer)) s.all[to] = key;
+      }
+    }
+    __syncthreads();
+    const int n = best_of(s.all, s.few, count, a.k);
+    const int part = number + cta;
+    if (tid < a.k) a.lists[static_cast<long long>(part) * a.k + tid] = tid < n ? s.all[tid] : 0ull;
+    if (warp == 1 && lane == 0) {
       float all = -INFINITY, total = 0.0f;
       for (int i = 0; i < kWarps; ++i) all = fmaxf(all, s.sum[i].x);
       const float r = all == -INFINITY ? 0.0f : all;
       for (int i = 0; i < kWarps; ++i) total += s.sum[i].y * ex2((s.sum[i].x - r) * kLog2e);
-      a.sums[at] = make_float2(all, total);
+      a.sums[part] = make_float2(all, total);
+    }
+    __syncthreads();  // the notes are free
+    if (round == R && left > 0) {
+      round = 0;
+      ++number;
+      do ++row;
+      while (!is_live(row));
     }
   }
-  // the last of the group's parts joins them
-  const int group = row / a.beams;
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    const int all = a.beams * a.parts, before = atomicAdd(a.counters + group, 1);
-    last = before == all - 1;
-    if (last) a.counters[group] = 0;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  join(a, *reinterpret_cast<Join*>(raw), group);
 }
 
-// Parts of a row: as many as make the CTAs' rounds fewest, counting a CTA's start
-// and end as three rounds of its own.
-int plan_parts(int64_t rows, int64_t vocab) {
-  const int64_t rounds = (vocab + kRound - 1) / kRound;
-  int best = 1;
-  double least = 1e300;
-  for (int64_t p = 1; p <= std::min<int64_t>(rounds, kMaxParts); ++p) {
-    const int64_t each = (rounds + p - 1) / p, waves = (rows * p + kSlots - 1) / kSlots;
-    const double cost = static_cast<double>(waves) * static_cast<double>(each + 3);
-    if (cost < least) {
-      least = cost;
-      best = static_cast<int>(p);
-    }
-  }
-  return best;
-}
-
+int64_t row_rounds(int64_t vocab) { return (vocab + kRound - 1) / kRound; }
 bool sizes_fit(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
   return groups >= 1 && beams >= 1 && beams <= LQ_BEAM_MAX && vocab >= 1 && vocab <= (1LL << kTokenBits) && k >= 1 && k <= LQ_BEAM_MAX &&
          groups * beams <= (1LL << 24);
 }
-size_t counter_bytes(int64_t groups) { return (static_cast<size_t>(groups) * 4 + 255) / 256 * 256; }
+size_t number_bytes(int64_t rows) { return (static_cast<size_t>(rows + 1) * 4 + 15) / 16 * 16; }
 
 }  // namespace
 
@@ -425,8 +653,8 @@ extern "C" {
 
 size_t lq_beam_work_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
   if (groups < 1 || groups > (1LL << 24) || !sizes_fit(groups, beams, vocab, k)) return 0;
-  const size_t lists = static_cast<size_t>(groups * beams) * plan_parts(groups * beams, vocab);
-  return counter_bytes(groups) + lists * (sizeof(float2) + static_cast<size_t>(k) * 8);
+  const size_t lists = static_cast<size_t>(groups * beams) + kCtas;  // a part ends where a row or a range does
+  return number_bytes(groups * beams) + lists * (sizeof(float2) + static_cast<size_t>(k) * 8);
 }
 
 lq_status lq_beam_select(const float* logits, int64_t ld, const float* scores, int64_t groups, int64_t beams, int64_t vocab, int64_t k,
@@ -449,31 +677,45 @@ lq_status lq_beam_select(const float* logits, int64_t ld, const float* scores, i
   a.out_scores = out_scores;
   a.out_parents = out_parents;
   a.out_tokens = out_tokens;
+  const int64_t rows = groups * beams;
+  a.rows = static_cast<int>(rows);
   a.beams = static_cast<int>(beams);
   a.vocab = static_cast<int>(vocab);
   a.k = static_cast<int>(k);
   a.pad = pad;
-  const int64_t rows = groups * beams;
-  a.parts = plan_parts(rows, vocab);
-  a.chunk = static_cast<int>((((vocab + a.parts - 1) / a.parts) + 3) / 4 * 4);
-  a.counters = static_cast<int*>(work);
-  a.lists = reinterpret_cast<unsigned long long*>(static_cast<char*>(work) + counter_bytes(groups));
-  a.sums = reinterpret_cast<float2*>(a.lists + rows * a.parts * k);
-  const int64_t ctas = rows * a.parts;
-  if (ctas > (1LL << 31) - 1) return LQ_ERR_UNSUPPORTED;
+  a.rounds = static_cast<int>(row_rounds(vocab));
+  a.scan = rows <= kScanRows;
+  a.per = static_cast<int*>(work);
+  a.number = a.per + 1;
+  a.lists = reinterpret_cast<unsigned long long*>(static_cast<char*>(work) + number_bytes(rows));
+  a.sums = reinterpret_cast<float2*>(a.lists + (rows + kCtas) * k);
+  const int64_t ctas = std::min<int64_t>(rows * a.rounds, kCtas);
   const bool vec = aligned_to(logits, 16) && ld % 4 == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Notes);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = use_pdl() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static_assert(sizeof(Notes) <= 47 * 1024 && sizeof(Join) <= sizeof(Notes));
-  cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? beam_kernel<true> : beam_kernel<false>, a);
+  static std::atomic<bool> ready[2][kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices) return LQ_ERR_CUDA;
+  void (*const kernel)(BeamArgs) = vec ? beam_kernel<true> : beam_kernel<false>;
+  if (!ready[vec][dev].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return LQ_ERR_CUDA;
+    }
+    ready[vec][dev].store(true);
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  cfg.gridDim = dim3(static_cast<unsigned>(groups));
+  cfg.dynamicSmemBytes = 0;
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, beam_join_kernel, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_status(e);
 }

@@ -517,7 +517,7 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  * lq_beam_select: the k best continuations of each group of `beams` rows, by
  *     scores[b] + (logits[b, j] - log sum_j exp(logits[b, j])),
  *   best first: out_scores (f32), out_parents (the beam within its group) and
- *   out_tokens, groups * k each. Scores are compared in 64 bits; equal ones go by the
+ *   out_tokens, groups * k each. Scores are compared in 48 bits; equal ones go by the
  *   lower beam, then the larger logit, then the lower token. Logits and scores of NaN
  *   or -inf are never chosen (a row with NaN or +inf among its logits gives no
  *   candidate); with fewer than k candidates the rest are (-inf, -1, -1). finished

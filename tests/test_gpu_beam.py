@@ -19,9 +19,8 @@ def _scores(logits, scores, finished=None, pad=0):
     """Every continuation's score in float64 [rows, vocab]; -inf: never chosen."""
     x = logits.astype(np.float64)
     with np.errstate(all="ignore"):
-        top = x.max(1, keepdims=True)
-        lse = top + np.log(np.exp(x - top).sum(1, keepdims=True))
-        s = scores.astype(np.float64)[:, None] + (x - lse)
+        top = x.max(1, keepdims=True)  # (taken off first: 2.5e38 + log(30000) is 2.5e38 in 64 bits)
+        s = scores.astype(np.float64)[:, None] + ((x - top) - np.log(np.exp(x - top).sum(1, keepdims=True)))
     s[np.isnan(s)] = -np.inf
     s[np.isneginf(scores) | np.isnan(scores)] = -np.inf
     if finished is not None:
@@ -294,3 +293,18 @@ def test_a_search_keeps_each_beams_own_past(lq, cuda_dev, fmt):
         k2, v2 = torch.empty_like(k), torch.empty_like(v)
         lq.lq_kv_read(fresh, alone, k2, v2)
         assert torch.equal(k, k2) and torch.equal(v, v2), f"beam {r}"
+
+
+@pytest.mark.parametrize("k", [3, 64])
+def test_long_parts_whose_notes_run_full(lq, cuda_dev, k):
+    """Rows enough that each is one part of many rounds: rows of one value, rising
+    (every round's logits are noted), falling, of ties and plain ones."""
+    rng = np.random.default_rng(k)
+    n, v = 640, 40003
+    x = rng.standard_normal((n, v)).astype(np.float32)
+    x[0::5] = 0.25
+    x[1::5] = np.arange(v, dtype=np.float32) / 1000
+    x[2::5] = -np.arange(v, dtype=np.float32) / 1000
+    x[3::5] = np.round(x[3::5] * 2) / 2
+    scores = -rng.random(n).astype(np.float32)
+    _check(_select(lq, cuda_dev, x, scores, 4, k), _best(_scores(x, scores), 4, k))
