@@ -47,6 +47,22 @@ constexpr int kMaxDim = 256;
 // gain from the warp-level kernel up to 128 rows, where one sequence loses.
 int few_rows(int fmt, int head_dim) { return fmt == LQ_FMT_F16 ? 48 : (head_dim == 256 ? 96 : 80); }
 
+// The same for the trees of a call, whose sequences have about as many rows each: all of
+// them go to one kernel, by their mean. us, warp-level / tile, the batches above in full:
+//   rows           32                48                96                128               192
+//   f16, 128   110/106 | 61/75   155/116 | 81/85   280/107 | 145/77
+//   Q8_0, 64   61/142 | 36/70    85/150 | 45/75    159/155 | 77/71
+//   Q8_0, 128  100/305 | 54/138  141/313 | 71/150  267/307 | 129/148  351/307 | 168/151
+//   Q4_0, 128  98/289 | 53/130   141/310 | 71/138  268/332 | 131/131  354/351 | 171/131
+//   Q8_0, 256  62/133 | 41/147   81/149 | 51/158   145/155 | 80/154   190/164 | 99/153   274/283 | 133/153
+//   Q4_0, 256  58/121 | 39/155   75/131 | 48/163   131/133 | 76/158   173/150 | 93/161   247/261 | 125/163
+// (of 256 dims the tile kernel's steps are of 128 rows). 16 trees of up to 61 rows of four
+// query heads, f16, 8192 positions: 148 us in one kernel, 171 when the shorter ones go first.
+int few_tree_rows(int fmt, int head_dim) {
+  if (fmt == LQ_FMT_F16) return head_dim == 128 ? 40 : 48;
+  return head_dim == 64 ? 80 : (head_dim == 128 ? 104 : 160);
+}
+
 template <int FMT, bool TREE>
 __global__ void __launch_bounds__(kGWarps * 32) attn_generic_kernel(const AttnArgs a) {
   __shared__ float part[kGWarps][kMaxDim + 2];
@@ -230,7 +246,12 @@ static lq_status attend(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
   if (route == 2) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   if (route == 3) return launch_attn_tile(a, cache->fmt, 0, work, s);
   if (!attn_warp_eligible(a)) return launch_attn_generic(a, cache->fmt, s);
-  const int few = few_rows(cache->fmt, cache->head_dim);
+  const int few = mask ? few_tree_rows(cache->fmt, cache->head_dim) : few_rows(cache->fmt, cache->head_dim);
+  if (mask && attn_tile_eligible(a)) {
+    const int64_t mean = batch->tokens * a.group / batch->batch;
+    if (mean > few) return launch_attn_tile(a, cache->fmt, 0, work, s);
+    if (rows <= 4 * few) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
+  }
   if (rows <= few || !attn_tile_eligible(a)) return launch_attn_warp(a, cache->fmt, rows, 0, work, s);
   // one sequence: all of it is one kernel's; else each kernel takes its own
   const int split = a.b.batch > 1 ? few : 0;

@@ -109,7 +109,9 @@ struct Geo {
   // split 12.5; 1100 positions: 13.4 and 12.9)
   static constexpr int WHOLE = 6 * W;
   static constexpr int QF = NR * (D / 16) * 512;           // fragments of the query rows
-  static constexpr int MERGE = (W / 2) * R * (D + 2) * 4;  // partial sums of half the warps
+  // partial sums of the warps that are joined at once: half of them, two where the sums are large
+  static constexpr int JOINS = NR * D <= 256 ? W / 2 : 2;
+  static constexpr int MERGE = JOINS * R * (D + 2) * 4;
   static constexpr int FIXED = QF + MERGE + 2048;
   static constexpr int FIT = (kSmemMax - FIXED) / (W * STAGE);
   static constexpr int S = FIT > 6 ? 6 : FIT;
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
       }
       // ---- logits ---------------------------------------------------------------
       constexpr int NT = TPS * 2;  // n-tiles of 8 keys
+      constexpr bool MANY = NR * D > 256;
       float2 x[NR][NT];
       auto query = [&](int n, int i, uint32_t (&q4)[4]) {  // MMA i of a row tile's query
         if constexpr (G::QREG) {
@@ -649,11 +652,13 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
           for (int nt = 0; nt < NT; ++nt) x[n][nt] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          uint32_t q4[NR][2][4];
+          uint32_t q4[MANY ? 1 : NR][2][4], kfs[MANY ? NT : 1][4];
+          if constexpr (!MANY) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) query(n, 2 * b + h, q4[n][h]);
+              for (int h = 0; h < 2; ++h) query(n, 2 * b + h, q4[n][h]);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t row = t0 + (nt >> 1) * G::TILE + ((nt & 1) * 8 + g) * G::KP;
@@ -669,13 +674,33 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
               kf[2] = nibbles_hi(w);
               kf[3] = nibbles_hi(w8);
             }
+            if constexpr (MANY) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) kfs[nt][j] = kf[j];
+              continue;
+            }
             const float2 d = make_float2(half_at(kd[nt][0], b), half_at(kd[nt][1], b));
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
+            for (int n = 0; n < (MANY ? 0 : NR); ++n) {
               float acc[4];
               mma_f16_first(acc, q4[n][0], kf[0], kf[1]);
               mma_f16(acc, q4[n][1], kf[2], kf[3]);
               x[n][nt] = ffma2(d, fadd2(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3])), x[n][nt]);
+            }
+          }
+          if constexpr (MANY) {  // (queries a row group at a time: fewer registers)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              query(n, 2 * b, q4[0][0]);
+              query(n, 2 * b + 1, q4[0][1]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 d = make_float2(half_at(kd[nt][0], b), half_at(kd[nt][1], b));
+                float acc[4];
+                mma_f16_first(acc, q4[0][0], kfs[nt][0], kfs[nt][1]);
+                mma_f16(acc, q4[0][1], kfs[nt][2], kfs[nt][3]);
+                x[n][nt] = ffma2(d, fadd2(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3])), x[n][nt]);
+              }
             }
           }
         }
@@ -837,24 +862,25 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
         auto add_values = [&](const bool masked) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          float acc[NR][4][4];
+          float acc[MANY ? 1 : NR][4][4];
 #pragma unroll
           for (int t = 0; t < TPS; ++t) {
             const uint32_t tv = t0 + t * G::TILE + kTile * G::KP;
-            uint32_t pa[NR][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            uint32_t pa[MANY ? 1 : NR][4];
+            auto weigh = [&](int n, int u, uint32_t (&to)[4]) {  // row group n's weights times the block's scales
               const int nt = 2 * t + u;
-              const float2 d = make_float2(half_at(vd[nt][0], b), half_at(vd[nt][1], b));
-#pragma unroll
-              for (int n = 0; n < NR; ++n) {
-                float2 w = fmul2(p[n][nt], d);
-                if (masked) {  // the scale of a key that the row does not see may be NaN
-                  w.x = (vis[n] >> (2 * nt)) & 1u ? w.x : 0.0f;
-                  w.y = (vis[n] >> (2 * nt + 1)) & 1u ? w.y : 0.0f;
-                }
-                split2(w, pa[n][2 * u], pa[n][2 * u + 1]);
+              float2 w = fmul2(p[n][nt], make_float2(half_at(vd[nt][0], b), half_at(vd[nt][1], b)));
+              if (masked) {  // the scale of a key that the row does not see may be NaN
+                w.x = (vis[n] >> (2 * nt)) & 1u ? w.x : 0.0f;
+                w.y = (vis[n] >> (2 * nt + 1)) & 1u ? w.y : 0.0f;
               }
+              split2(w, to[2 * u], to[2 * u + 1]);
+            };
+            if constexpr (!MANY) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) weigh(n, u, pa[n]);
             }
             uint32_t vf[4][2];  // n-tile, register
 #pragma unroll
@@ -872,8 +898,21 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
                 vf[3][u] = nibbles_hi(w8);
               }
             }
+            if constexpr (MANY) {
+              static_assert(!MANY || TPS == 1);
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+              for (int n = 0; n < NR; ++n) {
+                weigh(n, 0, pa[0]);
+                weigh(n, 1, pa[0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  mma_f16_first(acc[0][i], pa[0], vf[i][0], vf[i][1]);
+                  om[n][4 * b + i] = fadd2(om[n][4 * b + i], fadd2(make_float2(acc[0][i][0], acc[0][i][1]), make_float2(acc[0][i][2], acc[0][i][3])));
+                }
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < (MANY ? 0 : NR); ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (t == 0) {
@@ -884,7 +923,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
               }
           }
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+          for (int n = 0; n < (MANY ? 0 : NR); ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               om[n][4 * b + i] = fadd2(om[n][4 * b + i], fadd2(make_float2(acc[n][i][0], acc[n][i][1]), make_float2(acc[n][i][2], acc[n][i][3])));
@@ -929,36 +968,39 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
 #pragma unroll
     for (int n_left = W; n_left > 1; n_left = (n_left + 1) / 2) {
       const int half = (n_left + 1) / 2;
-      if (warp >= half && warp < n_left) {
-        float* at = merge + (warp - half) * (R * (D + 2));
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
+      for (int w0 = 0; w0 < n_left - half; w0 += G::JOINS) {
+        if (warp >= half + w0 && warp < min(half + w0 + G::JOINS, n_left)) {
+          float* at = merge + (warp - half - w0) * (R * (D + 2));
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2) = om[n][i];
-          if (c == 0) {
-            at[R * D + n * 8 + g] = M[n];
-            at[R * D + R + n * 8 + g] = l[n].x;
+          for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2) = om[n][i];
+            if (c == 0) {
+              at[R * D + n * 8 + g] = M[n];
+              at[R * D + R + n * 8 + g] = l[n].x;
+            }
           }
         }
-      }
-      __syncthreads();
-      if (warp < n_left - half) {
-        const float* at = merge + warp * (R * (D + 2));
+        __syncthreads();
+        if (warp >= w0 && warp < min(w0 + G::JOINS, n_left - half)) {
+          const float* at = merge + (warp - w0) * (R * (D + 2));
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          const float om2 = at[R * D + n * 8 + g], l2 = at[R * D + R + n * 8 + g];
-          const float to = fmaxf(M[n], om2), f1 = ex2(M[n] - to), f2 = ex2(om2 - to);
-          M[n] = to;
-          l[n].x = l[n].x * f1 + l2 * f2;
+          for (int n = 0; n < NR; ++n) {
+            const float om2 = at[R * D + n * 8 + g], l2 = at[R * D + R + n * 8 + g];
+            const float to = fmaxf(M[n], om2), f1 = ex2(M[n] - to), f2 = ex2(om2 - to);
+            M[n] = to;
+            l[n].x = l[n].x * f1 + l2 * f2;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const float2 o2 = *reinterpret_cast<const float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2);
-            om[n][i] = ffma2(om[n][i], make_float2(f1, f1), fmul2(o2, make_float2(f2, f2)));
+            for (int i = 0; i < D / 8; ++i) {
+              const float2 o2 = *reinterpret_cast<const float2*>(at + ((n * (D / 8) + i) * 32 + lane) * 2);
+              om[n][i] = ffma2(om[n][i], make_float2(f1, f1), fmul2(o2, make_float2(f2, f2)));
+            }
           }
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
     // warp 0 lays the rows out: [R][D], then M and l
     if (warp == 0) {
@@ -1187,7 +1229,12 @@ lq_status pick(const WarpParams& p, int nr, int ctas, cudaStream_t stream) {
   switch (p.a.c.head_dim) {
     case 64: return nr == 1 ? run<FMT, 64, 1>(p, ctas, stream) : run<FMT, 64, 2>(p, ctas, stream);
     case 128: return nr == 1 ? run<FMT, 128, 1>(p, ctas, stream) : run<FMT, 128, 2>(p, ctas, stream);
-    default: return run<FMT, 256, 1>(p, ctas, stream);
+    default:
+#ifdef LQ_ATTN_TREE
+      if constexpr (FMT != LQ_FMT_F16)
+        if (nr == 2) return run<FMT, 256, 2>(p, ctas, stream);
+#endif
+      return run<FMT, 256, 1>(p, ctas, stream);
   }
 }
 
@@ -1218,7 +1265,11 @@ lq_status launch_attn_warp_tree(const AttnArgs& a, int fmt, int rows, int small_
   p.small_rows = small_rows;
   p.vec = a.ldo % 4 == 0 && aligned_to(a.O, 16);
   const int ctas = std::max(1, std::min(device_info().sm_count, kAttnMaxCtas));
-  const int nr = rows > 8 ? 2 : 1;
+  // row groups that share a tile's keys. Two of 256 dims are for trees of quantised caches: few other
+  // calls have the rows. Q4_0, 16 sequences of 4096 | one of 32768, 4 heads over one, us with two | one:
+  // 32 rows 58 | 64, 39 | 39; 64: 95 | 115, 59 | 63; 128: 173 | 217, 93 | 109; 24: 57 | 50, 38 | 33; in f16
+  // 64 rows take 138 | 142, 74 | 77, and the tile kernel 57 for the first.
+  const int nr = a.c.head_dim == 256 ? (kTree && rows > 32 ? 2 : 1) : (rows > 8 ? 2 : 1);
   switch (fmt) {
     case LQ_FMT_F16: return pick<LQ_FMT_F16>(p, nr, ctas, stream);
     case LQ_FMT_Q8_0: return pick<LQ_FMT_Q8_0>(p, nr, ctas, stream);

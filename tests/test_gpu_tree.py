@@ -167,16 +167,32 @@ def test_pages_that_are_not_there(lq, cuda_dev, route):
     compare(lse, wl, ltol, "lse")
 
 
-def test_routes_by_the_rows(lq, cuda_dev):
-    """Few rows, many rows and both in one call; max_q steers, results stay."""
-    P = Paged(lq, "q8_0", [2, 90, 5], [700, 400, 33], 8, 2, 128, 16, cuda_dev, seed=5)
+@pytest.mark.parametrize("news,max_q,kernels", [
+    ([2, 90, 5], 90, (0, 1)), ([2, 90, 5], 0, (0, 1)), ([20, 5, 9], 20, (1, 0)), ([20, 5, 9], 1, (1, 0)), ([1], 1, (1, 0)),
+    ([2] * 9 + [120], 120, (1, 1)), ([2] * 9 + [120], 0, (1, 1)), ([2] * 9 + [120], 7, (1, 0))])
+def test_routes_by_the_rows(lq, cuda_dev, news, max_q, kernels):
+    """Trees go to one kernel by their mean, unless some are far from it; max_q
+    steers, results stay."""
+    P = Paged(lq, "q8_0", news, [n + 37 * (i + 3) for i, n in enumerate(news)], 8, 2, 128, 16, cuda_dev, seed=5)
     bits, positions = _trees(P, np.random.default_rng(2))
     want, tol, _, _ = expect_tree(P, bits, positions)
-    for max_q in (0, 90, 1):
-        lq.reset_counts()
-        o, _ = _attend(lq, P, _mask(P, bits), None, max_q=max_q)
-        assert lq.route_count(9) == 1 and lq.route_count(10) == (0 if max_q == 1 else 1)
-        compare(o, want, tol, f"max_q {max_q}")
+    lq.reset_counts()
+    o, _ = _attend(lq, P, _mask(P, bits), None, max_q=max_q)
+    assert (lq.route_count(9), lq.route_count(10)) == kernels
+    compare(o, want, tol, "output")
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("news,totals,page", [([40, 9], [300, 200], 16), ([17, 33, 1], [17, 900, 5], 64), ([130], [5000], 128)])
+def test_wide_heads_of_quantised_caches(lq, cuda_dev, fmt, news, totals, page):
+    """Heads of 256 with more than 32 rows: two row groups a tile of keys."""
+    P = Paged(lq, fmt, news, totals, 4, 1, 256, page, cuda_dev, seed=sum(news), fill="nan")
+    bits, positions = _trees(P, np.random.default_rng(4), roots=0.05)
+    for window, sinks in ((0, 0), (50, 3)):
+        o, lse = _attend(lq, P, _mask(P, bits), positions, route=WARP, window=window, sinks=sinks, max_q=max(news))
+        want, tol, wl, ltol = expect_tree(P, bits, positions, window, sinks)
+        compare(o, want, tol, "output")
+        compare(lse, wl, ltol, "lse")
 
 
 # ---- plan ---------------------------------------------------------------------
