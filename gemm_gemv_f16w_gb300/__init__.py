@@ -644,14 +644,14 @@ def lq_kv_keep(cache, batch, keep, count, stream=None) -> None:
 
 def beam_buffers(groups, beams, vocab, k, device=None):
     """(scores, parents, tokens, work) device buffers of lq_beam_select, which a
-    program keeps; work is zero-filled."""
+    program keeps."""
     import torch
     nbytes = int(lib().lq_beam_work_bytes(int(groups), int(beams), int(vocab), int(k)))
     if nbytes == 0:
         raise LQError(LQ_ERR_INVALID_ARG, "lq_beam_work_bytes")
     device = device or "cuda"
     return (torch.empty(groups, k, dtype=torch.float32, device=device), torch.empty(groups, k, dtype=torch.int32, device=device),
-            torch.empty(groups, k, dtype=torch.int32, device=device), torch.zeros(nbytes, dtype=torch.uint8, device=device))
+            torch.empty(groups, k, dtype=torch.int32, device=device), torch.empty(nbytes, dtype=torch.uint8, device=device))
 
 
 _beam_work_bytes = {}  # by (groups, beams, vocab, k): a number that depends on these alone

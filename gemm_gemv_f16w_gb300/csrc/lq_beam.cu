@@ -205,7 +205,7 @@ __device__ __forceinline__ unsigned ordered(float x) {
 }
 __device__ __forceinline__ Pick pick_of(const Pair& score, int beam, unsigned long long key) {
   Pick p = {0ull, 0ull};
-  if (!(score.hi > -INFINITY)) return p;  // -inf, NaN
+  if (!(fabsf(score.hi) < INFINITY)) return p;
   p.hi = static_cast<unsigned long long>(ordered(score.hi)) << 32 | ordered(score.lo);
   const unsigned token = 0xFFFFFFFFu - static_cast<unsigned>(key);
   p.lo = (static_cast<unsigned long long>(LQ_BEAM_MAX - 1 - beam) << 58) | ((key >> 32) << kTokenBits) | ((1u << kTokenBits) - 1u - token);
@@ -214,6 +214,26 @@ __device__ __forceinline__ Pick pick_of(const Pair& score, int beam, unsigned lo
 
 __device__ __forceinline__ bool is_read(const BeamArgs& a, int row) {
   return a.scores[row] > -INFINITY && !(a.finished && a.finished[row] != 0);
+}
+
+// Logits above `value` are noted, and those equal to it whose tokens are below `token`.
+struct Limit {
+  float value;
+  int token;
+};
+// The notes are full, or this warp has taken all of its own (done): the warps meet until
+// none has more. The best k stay; what follows has to rank above the least of them. (Not
+// inlined, so that all warps meet at one and the same barrier.)
+__device__ __noinline__ bool meet_warps(Notes& s, int& count, int k, bool done, Limit& limit) {
+  if (!__syncthreads_or(!done)) return false;
+  const int kept = best_of(s.key, s.few, count, k);
+  if (kept == k) {
+    limit.value = value_of(s.key[k - 1]);
+    limit.token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(s.key[k - 1]));
+  }
+  if (threadIdx.x == 0) count = kept;
+  __syncthreads();
+  return true;
 }
 
 // How the rounds are dealt: CTA c has rounds [c per, (c + 1) per) of the rows that are
@@ -493,18 +513,12 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
     float M = -INFINITY, S = 0.0f, highest = -INFINITY;
     float lim = -3.402823466e38f;     // logits above are noted, and those equal to it
     int lim_token = 1 << kTokenBits;  // whose tokens are below this one
-    // The notes are full, or this warp has taken all of its own: the warps meet until none
-    // has more. The best k stay; what follows has to rank above the least of them.
     auto meet = [&](bool done) {
-      if (!__syncthreads_or(!done)) return false;
-      const int kept = best_of(s.key, s.few, count, a.k);
-      if (kept == a.k) {
-        lim = value_of(s.key[a.k - 1]);
-        lim_token = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(s.key[a.k - 1]));
-      }
-      if (tid == 0) count = kept;
-      __syncthreads();
-      return true;
+      Limit limit = {lim, lim_token};
+      const bool more = meet_warps(s, count, a.k, done, limit);
+      lim = limit.value;
+      lim_token = limit.token;
+      return more;
     };
     int next_limit = 0;
 #pragma unroll 1

@@ -517,16 +517,16 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  * lq_beam_select: the k best continuations of each group of `beams` rows, by
  *     scores[b] + (logits[b, j] - log sum_j exp(logits[b, j])),
  *   best first: out_scores (f32), out_parents (the beam within its group) and
- *   out_tokens, groups * k each. Scores are compared in 48 bits; equal ones go by the
- *   lower beam, then the larger logit, then the lower token. Logits and scores of NaN
- *   or -inf are never chosen (a row with NaN or +inf among its logits gives no
- *   candidate); with fewer than k candidates the rest are (-inf, -1, -1). finished
- *   (NULL or groups * beams): beams other than 0 stand for one candidate, their
- *   score as it is and token `pad`; their logits are not read.
+ *   out_tokens, groups * k each. Scores are compared in two f32 parts (48 bits); equal
+ *   ones go by the lower beam, then the larger logit, then the lower token. Logits
+ *   and scores that are not finite, and sums beyond f32's range, are never chosen (a
+ *   row with NaN or +inf among its logits gives no candidate); with fewer than k
+ *   candidates the rest are (-inf, -1, -1). finished (NULL or groups * beams): a beam
+ *   where it is not 0 stands for one candidate, its score as it is and token `pad`;
+ *   its logits do not count.
  *   logits: row b of group g at logits + (g * beams + b) * ld. work:
- *   lq_beam_work_bytes(...) bytes of DEVICE memory, 16-byte aligned, zero-filled
- *   before its first use; each call leaves it ready for the next of the same
- *   sizes, one call at a time (0 for sizes out of range).
+ *   lq_beam_work_bytes(...) bytes of DEVICE scratch memory, 16-byte aligned, one call at
+ *   a time (0 for sizes out of range). The same inputs give the same bits.
  *   ld >= vocab, 0 <= pad < vocab, else LQ_ERR_INVALID_ARG; beams or k >
  *   LQ_BEAM_MAX, vocab > 2^26 or more than 2^24 rows -> LQ_ERR_UNSUPPORTED.
  *

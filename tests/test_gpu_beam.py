@@ -162,6 +162,53 @@ def test_work_is_ready_for_the_next_call(lq, cuda_dev):
         _check([b.cpu().numpy() for b in buffers[:3]], _best(_scores(x, scores), 4, 8))
 
 
+@pytest.mark.parametrize("groups,beams,vocab,k", [(1100, 4, 301, 6), (70, 64, 64, 64), (5000, 1, 4100, 2)])
+def test_more_rows_than_are_looked_over(lq, cuda_dev, groups, beams, vocab, k):
+    """Beyond 4096 rows the rows that do not count are dealt like the others."""
+    rng = np.random.default_rng(groups)
+    n = groups * beams
+    x = rng.standard_normal((n, vocab)).astype(np.float32)
+    scores = (-9 * rng.random(n)).astype(np.float32)
+    scores[rng.random(n) < 0.1] = -np.inf
+    ended = (rng.random(n) < 0.3).astype(np.int32)
+    ended[:3 * beams] = 1
+    scores[3 * beams:5 * beams] = -np.inf
+    x[ended != 0] = np.nan
+    _check(_select(lq, cuda_dev, x, scores, beams, k, finished=ended, pad=vocab - 1),
+           _best(_scores(np.nan_to_num(x), scores, ended, vocab - 1), beams, k))
+
+
+def test_scores_that_are_not_finite(lq, cuda_dev):
+    x = np.zeros((5, 100), np.float32)
+    x[1, 7] = 2.0
+    x[4, 3] = -np.finfo(np.float32).max
+    x[4, 5] = np.finfo(np.float32).max
+    scores = np.array([np.inf, -1.0, np.nan, np.inf, -2.0], np.float32)
+    s, p, t = _select(lq, cuda_dev, x, scores, 5, 3, finished=np.array([0, 0, 1, 1, 0]), pad=0)
+    # the last row's 5 has all of its weight: -2; of row 1, log(99 + e^2) = 4.667: 7 gives -3.667, 0 gives -5.667
+    assert p.tolist() == [[4, 1, 1]] and t.tolist() == [[5, 7, 0]]
+
+
+def test_scratch_of_any_content_two_streams(lq, cuda_dev):
+    """Nothing is expected of the scratch memory; calls with their own run at once."""
+    rng = np.random.default_rng(12)
+    data, outs = [], []
+    for i in range(2):
+        x, scores = rng.standard_normal((32, 50000)).astype(np.float32), -rng.random(32).astype(np.float32)
+        data.append((x, scores, torch.from_numpy(x).to(cuda_dev), torch.from_numpy(scores).to(cuda_dev)))
+        buffers = lq.beam_buffers(8, 4, 50000, 8)
+        buffers[3].fill_(255 - 85 * i)
+        outs.append(buffers)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            lq.lq_beam_select(data[i][2], data[i][3], 4, 8, *outs[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        _check([b.cpu().numpy() for b in outs[i][:3]], _best(_scores(data[i][0], data[i][1]), 4, 8))
+
+
 # ---- pages and copies ------------------------------------------------------------
 def _pages(parent, beams, table, lens, page):
     """(tables, copies) by the definition."""

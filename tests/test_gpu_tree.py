@@ -154,6 +154,21 @@ def test_a_chain_is_the_causal_call(lq, cuda_dev, route, fmt):
 
 
 @pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_lengths_below_the_rows(lq, cuda_dev, route, fmt):
+    """Caches shorter than the call's rows: the first rows have no slots."""
+    P = Paged(lq, fmt, [40, 9, 5, 70], [30, 0, 5, 1], 4, 2, 128, 16, cuda_dev, seed=6)
+    rng = np.random.default_rng(3)
+    bits = [rng.random((n, n)) < 0.5 for n in P.news]
+    positions = rng.integers(0, 40, P.tokens)
+    for window, sinks in ((0, 0), (8, 2)):
+        o, lse = _attend(lq, P, _mask(P, bits), positions, route=route, window=window, sinks=sinks)
+        want, tol, wl, ltol = expect_tree(P, bits, positions, window, sinks)
+        compare(o, want, tol, "output")
+        compare(lse, wl, ltol, "lse")
+
+
+@pytest.mark.parametrize("route", ROUTES)
 def test_pages_that_are_not_there(lq, cuda_dev, route):
     P = Paged(lq, "f16", [20, 30], [200, 130], 4, 2, 128, 16, cuda_dev, seed=8)
     table = P.table.copy()
