@@ -5,7 +5,7 @@
 // Within a beam that is the order of x itself, so one pass over the logits gives
 // each part of a row its k best logits and its share of the sum, and only those
 // candidates ever get a score. lse_b and the scores are held in two f32 parts (48 bits;
-// 64-bit arithmetic is slow on this chip and cost the join 4 us): beams are compared
+// 64-bit arithmetic is slow on this chip and cost the join 1 to 3 us): beams are compared
 // across lse's, where f32's steps (5e-7 at 8) would be ties.
 //
 // The sum. A thread keeps a running maximum M and S = sum 2^(c (x - M)), c = log2(e),
@@ -33,8 +33,12 @@
 // last part to arrive instead, whose range then ends late, 32 groups of 8 beams over a
 // vocabulary of 151936 take 67 us.)
 //
-// What bounds it: logits are read once, HBM. An ended beam (one candidate, its score
-// as it is) and one with a score of -inf are not read at all.
+// What bounds it: logits are read once, HBM. 32 groups of 8 beams, a fifth of them ended,
+// vocabulary 151936, k 16: 43 us (the parts 33, the join 9; the logits at a copy's rate
+// take 23, those of the live beams 19): the parts begin with the look for the rows that
+// count and end with a wait for the slowest warp, and the join is a chain of four
+// dependent loads and as many barriers. One group of 4 beams, k 8: 11 us. An ended beam
+// (one candidate, its score as it is) and one with a score of -inf are not read at all.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -4,10 +4,12 @@
 // Codes and scales are moved as they are: nothing is rounded anew.
 //
 // Keep. Row keep[k] of a sequence's new tokens goes to the place of row k; keep[]
-// ascends, so k <= keep[k]. A thread owns one column (16 bytes of the codes, or
-// one scale) of one head of K or V and takes the rows in order, eight loads and then
-// eight stores: what a store overwrites, its own thread has read, and no
-// other touches the column. So the move is in place without a barrier.
+// ascends, so k <= keep[k]. A CTA has one head of K or V of a sequence and takes the
+// rows in order, as many at a time as its threads hold in registers (1024 pieces of
+// 16 bytes, or of one scale): all loads, a barrier, all stores. What a store overwrites
+// is the source of rows of its own or an earlier time only, so the move is in place.
+// 256 rows of Q8_0, 8 heads of 128, moved by one: 15 us (44 when a thread
+// takes all rows of its column in order); the accepted paths of 32 sequences 3.4.
 //
 // Pages. The beams of a group have one length; all pages before its last, partly
 // filled one are full and shared, that page and those behind are each
@@ -33,8 +35,7 @@ __device__ unsigned g_move_err;
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_move_err, 0u, code); }
 
 constexpr int kKeepThreads = 128;
-constexpr int kKeepRows = 128;  // rows whose places are looked up together
-constexpr int kKeepAhead = 8;   // loads on their way
+constexpr int kKeepPieces = 8;  // of a thread at a time
 constexpr int kCopyThreads = 256;
 constexpr int kMapThreads = 256;
 
@@ -44,34 +45,16 @@ struct KeepArgs {
   const int* keep;  // [batch][most]
   const int* count;
   int most;
-  int code_columns, scale_columns;  // of a head: of `width` and of two bytes
+  int code_columns, columns;  // pieces of a token's head: of the codes, and with the scales
+  int rows;                   // at a time: columns * rows pieces
 };
 
-// Moves of a column of T from src[k] to dst[k] (offsets of the token's codes or
-// scales in the pool; -1: nothing is moved), in order.
-template <class T>
-__device__ __forceinline__ void move_column(unsigned char* at, const long long* src, const long long* dst, int n) {
-#pragma unroll 1
-  for (int k = 0; k < n; k += kKeepAhead) {
-    T x[kKeepAhead];
-    long long to[kKeepAhead];
-#pragma unroll
-    for (int j = 0; j < kKeepAhead; ++j) {
-      const bool there = k + j < n && src[k + j] >= 0 && dst[k + j] >= 0;
-      to[j] = there ? dst[k + j] : -1;
-      if (there) x[j] = *reinterpret_cast<const T*>(at + src[k + j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kKeepAhead; ++j)
-      if (to[j] >= 0) *reinterpret_cast<T*>(at + to[j]) = x[j];
-  }
-}
-
-// T: what a thread moves of the codes.
+// T: a piece of the codes.
 template <class T>
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a) {
-  // places of codes and of scales, from the (page, head)'s first byte on
-  __shared__ long long code_src[kKeepRows], code_dst[kKeepRows], scale_src[kKeepRows], scale_dst[kKeepRows];
+  // where the rows' codes come from and go to (-1: they stay), and their scales
+  __shared__ long long src[kKeepThreads], dst[kKeepThreads], scale_src[kKeepThreads], scale_dst[kKeepThreads];
+  __shared__ int stop;
   pdl_wait();
   pdl_launch_dependents();
   const int i = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
@@ -79,51 +62,66 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a) {
   const int base = s.len - s.rows;
   const int* const keep = a.keep + static_cast<long long>(i) * a.most;
   const int count = min(min(a.count[i], a.most), s.rows);
-  // this thread's column
-  const int columns = a.code_columns + a.scale_columns;
-  const int column = static_cast<int>(blockIdx.y) * kKeepThreads + tid, head = column / columns, within = column - head * columns;
-  const bool mine = head < 2 * a.c.kv_heads;
-  unsigned char* const pool = head < a.c.kv_heads ? a.c.k : a.c.v;
-  const long long head_at = static_cast<long long>(head < a.c.kv_heads ? head : head - a.c.kv_heads) * a.c.head_bytes;
-  const bool is_scale = within >= a.code_columns;
-  unsigned char* const at =
-      pool + head_at + (is_scale ? static_cast<long long>(within - a.code_columns) * 2 : static_cast<long long>(within) * static_cast<int>(sizeof(T)));
+  const int side = static_cast<int>(blockIdx.y) / a.c.kv_heads, head = static_cast<int>(blockIdx.y) - side * a.c.kv_heads;
+  unsigned char* const pool = (side ? a.c.v : a.c.k) + head * a.c.head_bytes;
 #pragma unroll 1
-  for (int k0 = 0; k0 < count; k0 += kKeepRows) {
-    const int n = min(kKeepRows, count - k0);
+  for (int k0 = 0; k0 < count; k0 += a.rows) {
+    const int n = min(a.rows, count - k0);
     bool good = true;
     if (tid < n) {
       const int k = k0 + tid, from = keep[k];
       good = from >= 0 && from < s.rows && (k == 0 ? true : from > keep[k - 1]);
       const int p_src = base + from, p_dst = base + k;
-      int src = -1, dst = -1;
+      int page_src = -1, page_dst = -1;
       if (good && from != k && p_dst >= 0) {
-        src = kv::page_of(a.c, a.b, i, p_src);
-        dst = kv::page_of(a.c, a.b, i, p_dst);
+        page_src = kv::page_of(a.c, a.b, i, p_src);
+        page_dst = kv::page_of(a.c, a.b, i, p_dst);
       }
-      const bool moves = src >= 0 && dst >= 0 && LQ_IN_BOUNDS(src < a.c.num_pages && dst < a.c.num_pages);
+      const bool moves = page_src >= 0 && page_dst >= 0 && LQ_IN_BOUNDS(page_src < a.c.num_pages && page_dst < a.c.num_pages);
       const long long scales = static_cast<long long>(a.c.page_size) * a.c.row_bytes;
       const int s_src = moves ? p_src % a.c.page_size : 0, s_dst = moves ? p_dst % a.c.page_size : 0;
-      code_src[tid] = moves ? src * a.c.page_bytes + static_cast<long long>(s_src) * a.c.row_bytes : -1;
-      code_dst[tid] = moves ? dst * a.c.page_bytes + static_cast<long long>(s_dst) * a.c.row_bytes : -1;
-      scale_src[tid] = moves ? src * a.c.page_bytes + scales + s_src * (a.c.head_dim / 16) : -1;
-      scale_dst[tid] = moves ? dst * a.c.page_bytes + scales + s_dst * (a.c.head_dim / 16) : -1;
+      src[tid] = moves ? page_src * a.c.page_bytes + static_cast<long long>(s_src) * a.c.row_bytes : -1;
+      dst[tid] = moves ? page_dst * a.c.page_bytes + static_cast<long long>(s_dst) * a.c.row_bytes : -1;
+      scale_src[tid] = moves ? page_src * a.c.page_bytes + scales + s_src * (a.c.head_dim / 16) : -1;
+      scale_dst[tid] = moves ? page_dst * a.c.page_bytes + scales + s_dst * (a.c.head_dim / 16) : -1;
     }
     // the list ends at the first entry that does not ascend
-    __shared__ int stop;
     if (tid == 0) stop = n;
     __syncthreads();
     if (tid < n && !good) atomicMin(&stop, tid);
     __syncthreads();
-    const int m = stop;
-    if (mine) {
-      if (is_scale) {
-        move_column<unsigned short>(at, scale_src, scale_dst, m);
-      } else {
-        move_column<T>(at, code_src, code_dst, m);
+    const int m = stop, pieces = m * a.columns;
+    T x[kKeepPieces];
+    unsigned char* to[kKeepPieces];
+    bool scale[kKeepPieces];
+#pragma unroll
+    for (int j = 0; j < kKeepPieces; ++j) {
+      const int e = j * kKeepThreads + tid, r = e / a.columns, column = e - r * a.columns;
+      to[j] = nullptr;
+      scale[j] = column >= a.code_columns;
+      if (e < pieces && src[r] >= 0) {
+        if (scale[j]) {
+          const int at = (column - a.code_columns) * 2;
+          to[j] = pool + scale_dst[r] + at;
+          *reinterpret_cast<unsigned short*>(&x[j]) = *reinterpret_cast<const unsigned short*>(pool + scale_src[r] + at);
+        } else {
+          const int at = column * static_cast<int>(sizeof(T));
+          to[j] = pool + dst[r] + at;
+          x[j] = *reinterpret_cast<const T*>(pool + src[r] + at);
+        }
       }
     }
-    __syncthreads();  // the places are free
+    __syncthreads();  // all has been read
+#pragma unroll
+    for (int j = 0; j < kKeepPieces; ++j) {
+      if (!to[j]) continue;
+      if (scale[j]) {
+        *reinterpret_cast<unsigned short*>(to[j]) = *reinterpret_cast<const unsigned short*>(&x[j]);
+      } else {
+        *reinterpret_cast<T*>(to[j]) = x[j];
+      }
+    }
+    __syncthreads();  // and written, before the next rows are read
     if (m < n) break;
   }
 }
@@ -177,7 +175,7 @@ struct PagesArgs {
   int beams, max_pages, page_size;
 };
 
-// grid: x = group, y = part of the tables' columns
+// grid: x = group, y = part of its tables' entries
 __global__ void __launch_bounds__(kMapThreads) pages_kernel(const PagesArgs a) {
   __shared__ int parent[LQ_BEAM_MAX], place[LQ_BEAM_MAX], free_list[LQ_BEAM_MAX];
   __shared__ unsigned bits[2][LQ_BEAM_MAX / 32];  // beams without a child; further children
@@ -223,21 +221,19 @@ __global__ void __launch_bounds__(kMapThreads) pages_kernel(const PagesArgs a) {
   __syncthreads();
   const int len = max(a.len[first], 0), whole = len / a.page_size, rows = len - whole * a.page_size;
   const int from = static_cast<int>(blockIdx.y) * kMapThreads, step = static_cast<int>(gridDim.y) * kMapThreads;
-#pragma unroll 1
-  for (int b = 0; b < n; ++b) {
-    const int p = parent[b] < 0 ? place[b] : parent[b], o = place[b];
-    const int* const shared = a.table + (first + p) * a.max_pages;
-    const int* const owned = a.table + (first + o) * a.max_pages;
-    int* const out = a.out + (first + b) * a.max_pages;
-    for (int e = from + tid; e < a.max_pages; e += step)
-      if (LQ_IN_BOUNDS(e >= 0)) out[e] = e < whole ? shared[e] : owned[e];
-    if (blockIdx.y == 0 && tid == 0) {
-      int* const c = a.copies + (first + b) * 3;
-      const bool copies = parent[b] >= 0 && o != p && rows > 0 && whole < a.max_pages;
-      c[0] = copies ? shared[whole] : -1;
-      c[1] = copies ? owned[whole] : -1;
-      c[2] = copies ? rows : 0;
-    }
+  const int entries = n * a.max_pages;
+#pragma unroll 4
+  for (int x = from + tid; x < entries; x += step) {
+    const int b = x / a.max_pages, e = x - b * a.max_pages;
+    const int of = e < whole && parent[b] >= 0 ? parent[b] : place[b];  // full pages are the parent's
+    if (LQ_IN_BOUNDS(of >= 0 && of < n)) a.out[first * a.max_pages + x] = a.table[(first + of) * a.max_pages + e];
+  }
+  if (blockIdx.y == 0 && tid < n) {
+    const bool copies = parent[tid] >= 0 && place[tid] != parent[tid] && rows > 0 && whole < a.max_pages;
+    int* const c = a.copies + (first + tid) * 3;
+    c[0] = copies ? a.table[(first + parent[tid]) * a.max_pages + whole] : -1;
+    c[1] = copies ? a.table[(first + place[tid]) * a.max_pages + whole] : -1;
+    c[2] = copies ? rows : 0;
   }
 }
 
@@ -293,10 +289,9 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
   a.most = static_cast<int>(max_keep);
   const bool w = wide(a.c);
   a.code_columns = a.c.row_bytes / (w ? 16 : 2);
-  a.scale_columns = cache->fmt == LQ_FMT_F16 ? 0 : a.c.head_dim / 32;
-  const int64_t columns = 2LL * a.c.kv_heads * (a.code_columns + a.scale_columns);
-  const dim3 grid(static_cast<unsigned>(a.b.batch), static_cast<unsigned>((columns + kKeepThreads - 1) / kKeepThreads));
-  if (grid.y > 65535) return LQ_ERR_UNSUPPORTED;
+  a.columns = a.code_columns + (cache->fmt == LQ_FMT_F16 ? 0 : a.c.head_dim / 32);  // (at most 264)
+  a.rows = std::min(kKeepThreads, kKeepThreads * kKeepPieces / a.columns);
+  const dim3 grid(static_cast<unsigned>(a.b.batch), static_cast<unsigned>(2 * a.c.kv_heads));
   const void* kernel = w ? reinterpret_cast<const void*>(keep_kernel<uint4>) : reinterpret_cast<const void*>(keep_kernel<unsigned short>);
   return launch(kernel, grid, kKeepThreads, &a, static_cast<cudaStream_t>(stream));
 }
@@ -323,7 +318,9 @@ lq_status lq_kv_copy(const lq_kv_cache* cache, const int32_t* copies, int64_t n,
 lq_status lq_beam_pages(const int32_t* parent, int64_t groups, int64_t beams, const int32_t* table, int64_t max_pages,
                         const int32_t* kv_len, int64_t page_size, int32_t* table_out, int32_t* copies, void* stream) {
   if (groups < 0 || beams < 1 || max_pages < 0 || page_size < 1 || page_size > 65536) return LQ_ERR_INVALID_ARG;
-  if (beams > LQ_BEAM_MAX || groups * beams > (1LL << 30) || max_pages * page_size > (1LL << 30)) return LQ_ERR_UNSUPPORTED;
+  if (beams > LQ_BEAM_MAX || groups * beams > (1LL << 30) || max_pages * page_size > (1LL << 30) ||
+      beams * max_pages > (1LL << 30))
+    return LQ_ERR_UNSUPPORTED;
   if (groups == 0) return LQ_OK;
   for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(kv_len), static_cast<const void*>(copies)})
     if (!p || !aligned_to(p, 4)) return LQ_ERR_INVALID_ARG;
@@ -338,7 +335,8 @@ lq_status lq_beam_pages(const int32_t* parent, int64_t groups, int64_t beams, co
   a.beams = static_cast<int>(beams);
   a.max_pages = static_cast<int>(max_pages);
   a.page_size = static_cast<int>(page_size);
-  const int64_t parts = std::min<int64_t>(std::max<int64_t>((max_pages + kMapThreads - 1) / kMapThreads, 1), 64);
+  // (four entries a thread)
+  const int64_t parts = std::min<int64_t>(std::max<int64_t>((beams * max_pages + 4 * kMapThreads - 1) / (4 * kMapThreads), 1), 1024);
   const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(parts));
   return launch(reinterpret_cast<const void*>(pages_kernel), grid, kMapThreads, &a, static_cast<cudaStream_t>(stream));
 }

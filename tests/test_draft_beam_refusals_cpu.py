@@ -154,7 +154,7 @@ def test_beam_refusals(lq):
     for kw in (dict(parent=0), dict(parent=P + 1), dict(table=0), dict(out=0), dict(lens=0), dict(copies=0), dict(out=P), dict(groups=-1),
                dict(beams=0), dict(most=-1), dict(page=0), dict(page=65537), dict(copies=P + 2)):
         assert pages(**kw) == bad, kw
-    assert pages(beams=65) == big and pages(most=1 << 30) == big and pages(groups=1 << 29) == big
+    assert pages(beams=65) == big and pages(most=1 << 30) == big and pages(groups=1 << 29) == pages(beams=64, most=1 << 25, page=1) == big
     assert pages(groups=0, parent=0) == lq.LQ_OK
 
     for kw in BAD_CACHES:
