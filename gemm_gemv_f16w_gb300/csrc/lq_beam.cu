@@ -16,7 +16,7 @@
 // The candidates. If each of the 8 warps has ceil(k / 8) maxima (of what a thread has
 // seen) at or above a limit, k logits of the part are: the least of the warps'
 // ceil(k / 8)-th largest maxima, taken in the 1st, 4th, 16th ... round of 4096 logits,
-// costs a sort of 32 values by shuffles. Of the 16 logits that a thread has of a round
+// costs a vote or two (fewer warps where the row is short). Of the 16 logits that a thread has of a round
 // only the largest is noted, and only at or above the limit: the k best logits are
 // among the 16 of the k best notes (were one in another, k notes would rank above it),
 // and those few are read once more when the part ends. Should the notes run full (rows
@@ -105,13 +105,13 @@ struct Notes {
   unsigned long long all[LQ_BEAM_MAX * kPer];  // the logits of the best notes' rounds
   unsigned long long few[kThreads];
   float2 sum[kWarps];
-  float limit[kWarps];
+  unsigned limit[kWarps];
 };
 struct Join {
   Pick pick[kPicks];
   Pick few[kThreads];
   Pair lse[LQ_BEAM_MAX];
-  unsigned long long limit[kWarps];
+  unsigned limit[kWarps];
   float score[LQ_BEAM_MAX], base[LQ_BEAM_MAX];  // base NaN: an ended beam
   int start[LQ_BEAM_MAX + 1], part[LQ_BEAM_MAX];  // lists before a beam's, and its first part
   int count;
@@ -134,48 +134,62 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
   const unsigned hi = static_cast<unsigned>(key >> 32);
   return __uint_as_float((hi & 0x80000000u) ? (hi & 0x7FFFFFFFu) : ~hi);
 }
-// The warp's values in descending order, one a lane.
-template <class T>
-__device__ __forceinline__ T sorted(T x, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size *= 2) {
-#pragma unroll
-    for (int step = size / 2; step > 0; step /= 2) {
-      const T y = __shfl_xor_sync(0xffffffffu, x, step);
-      const bool larger = ((lane & step) == 0) == ((lane & size) == 0);  // this lane keeps the larger one
-      x = larger == (x > y) ? x : y;
-    }
+__device__ __forceinline__ unsigned ordered(float x) {
+  const unsigned u = __float_as_uint(x + 0.0f);  // -0 as +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+// A key's place in the order by its upper 32 bits alone: a float as `ordered` has it.
+__device__ __forceinline__ unsigned upper(unsigned long long k) { return static_cast<unsigned>(k >> 32); }
+__device__ __forceinline__ unsigned upper(const Pick& p) { return upper(p.hi); }
+
+// The q-th largest (1 <= q <= 32) of the warp's values, one a lane.
+__device__ __forceinline__ unsigned nth_of_warp(unsigned x, int q, int lane) {
+  unsigned top = __reduce_max_sync(0xffffffffu, x);
+#pragma unroll 1
+  for (; q > 1; --q) {
+    const unsigned holders = __ballot_sync(0xffffffffu, x == top);
+    if (lane == __ffs(static_cast<int>(holders)) - 1) x = 0u;  // (taken out; below every float)
+    top = __reduce_max_sync(0xffffffffu, x);
   }
-  return x;
+  return top;
 }
 
 // Leaves the best min(k, n) of n distinct keys, best first, in key[0 .. ), by the
 // whole block; few[kThreads] is scratch.
 template <class K>
 __device__ __noinline__ int best_of(K* key, K* few, int n, int k) {
-  const int tid = static_cast<int>(threadIdx.x);
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   __shared__ int fewer;
-  // Each thread's best, and of those the k-th: no more than k threads have keys at or
-  // above it, and every one of the best k is. So at most k / 256 of the keys
+  __shared__ unsigned limit[kWarps];
+  // More than 256: each thread's best; with ceil(k / 8) of each warp's at or above a key, k
+  // are, and what is below it goes. If too many stay, the k-th of the threads' bests itself
+  // is taken: no more than k threads have keys at or above it, at most k / 256 of the keys
   // stay, rounded up a thread, and the loop ends.
-  while (n > kThreads) {
+  for (int turn = 0; n > kThreads; ++turn) {
     K mine = {};
     for (int i = tid; i < n; i += kThreads) mine = better(key[i], mine) ? key[i] : mine;
     few[tid] = mine;
-    __syncthreads();
-    int before = 0;
-    for (int j = 0; j < kThreads; ++j) before += better(few[j], mine) ? 1 : 0;
-    __syncthreads();
-    if (before == k - 1) few[0] = mine;
+    const unsigned nth = nth_of_warp(upper(mine), (k + kWarps - 1) / kWarps, lane);
+    if (lane == 0) limit[warp] = nth;
     if (tid == 0) fewer = 0;
     __syncthreads();
-    const K least = few[0];
+    unsigned lim = limit[0];
+    for (int w = 1; w < kWarps; ++w) lim = min(lim, limit[w]);
+    K least = {};
+    if (turn > 0) {
+      int before = 0;
+      for (int j = 0; j < kThreads; ++j) before += better(few[j], mine) ? 1 : 0;
+      __syncthreads();
+      if (before == k - 1) few[0] = mine;
+      __syncthreads();
+      least = few[0];
+    }
     // in place: a round of the block's reads lies ahead of its writes
     for (int i0 = 0; i0 < n; i0 += kThreads) {
       K x = {};
       if (i0 + tid < n) x = key[i0 + tid];
       __syncthreads();
-      if (is(x) && !better(least, x)) key[atomicAdd(&fewer, 1)] = x;
+      if (is(x) && upper(x) >= lim && !better(least, x)) key[atomicAdd(&fewer, 1)] = x;
       __syncthreads();
     }
     n = fewer;
@@ -186,7 +200,7 @@ __device__ __noinline__ int best_of(K* key, K* few, int n, int k) {
   if (tid < n) {
     x = key[tid];
     rank = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += better(key[j], x) ? 1 : 0;
   }
   __syncthreads();
@@ -202,10 +216,6 @@ __device__ __forceinline__ Pair sum_of(float a, float b) {  // exactly
 __device__ __forceinline__ Pair sum_of(const Pair& a, float b) {
   const Pair t = sum_of(a.hi, b);
   return sum_of(t.hi, t.lo + a.lo);
-}
-__device__ __forceinline__ unsigned ordered(float x) {
-  const unsigned u = __float_as_uint(x + 0.0f);  // -0 as +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ Pick pick_of(const Pair& score, int beam, unsigned long long key) {
   Pick p = {0ull, 0ull};
@@ -260,20 +270,22 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   const int group = static_cast<int>(blockIdx.x), row0 = group * a.beams;
   if (warp == 0) {  // two beams a lane
     int n[2], before = 0;
+    Deal deal;
+    deal.per = __ldcg(a.per);
+    deal.rounds = a.rounds;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int b = 2 * lane + h;
       n[h] = 0;
       if (b < a.beams) {
         const float score = a.scores[row0 + b];
+        const int ended = a.finished ? a.finished[row0 + b] : 0;
+        const int l = __ldcg(a.number + row0 + b);  // (of a row that is read; asked for with the others)
         s.score[b] = score;
-        if (a.finished && a.finished[row0 + b] != 0) {
+        if (ended != 0) {
           s.base[b] = NAN;  // its logits give no candidate
         } else if (!a.scan || score > -INFINITY) {
-          Deal deal;
-          deal.per = __ldcg(a.per);
-          deal.rounds = a.rounds;
-          const int l = __ldcg(a.number + row0 + b), c0 = deal.first_cta(l);
+          const int c0 = deal.first_cta(l);
           s.part[b] = l + c0;
           n[h] = deal.last_cta(l) - c0 + 1;
           s.base[b] = 0.0f;
@@ -350,14 +362,14 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   }
   // A limit: with ceil(k / 8) of each warp's entries at or above it, k are.
   const Pick p = scored(mine_key, mine_beam);
-  const unsigned long long nth = sorted(p.hi, lane);
-  if (lane == (a.k + kWarps - 1) / kWarps - 1) s.limit[warp] = nth;
+  const unsigned nth = nth_of_warp(upper(p), (a.k + kWarps - 1) / kWarps, lane);
+  if (lane == 0) s.limit[warp] = nth;
   __syncthreads();
-  unsigned long long limit = s.limit[0];
+  unsigned limit = s.limit[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) limit = min(limit, s.limit[w]);
-  limit = max(limit, 1ull);  // (scores' own are above it)
-  if (p.hi >= limit) s.pick[atomicAdd(&s.count, 1)] = p;
+  limit = max(limit, 1u);  // (scores' own are above it)
+  if (upper(p) >= limit) s.pick[atomicAdd(&s.count, 1)] = p;
   // The lists are sorted: a thread goes down the rest of each of its own until it is below.
 #pragma unroll 1
   for (int i0 = 0; i0 < lists; i0 += kThreads) {
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const Pick x = scored(key[i], b);
-        on = on && x.hi >= limit;
+        on = on && upper(x) >= limit;
         if (on) {
           const int to = atomicAdd(&s.count, 1);
           if (LQ_IN_BOUNDS(to < kPicks)) s.pick[to] = x;
@@ -570,12 +582,15 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
       if (i == next_limit) {
         while (i > 0 && meet(true)) {
         }
-        const float nth = sorted(highest, lane);  // (a NaN is no maximum)
-        if (lane == (a.k + kWarps - 1) / kWarps - 1) s.limit[warp] = nth;
+        // (of the warps that have logits: a row may end within its first round)
+        const int warps = i > 0 ? kWarps : max(1, min(kWarps, (a.vocab - round * kRound + kRound / kWarps - 1) / (kRound / kWarps)));
+        const int of_each = (a.k + warps - 1) / warps;
+        const unsigned nth = nth_of_warp(ordered(highest), min(of_each, 32), lane);
+        if (lane == 0) s.limit[warp] = nth;
         __syncthreads();
-        float least = s.limit[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) least = fminf(least, s.limit[w]);
+        unsigned lowest = s.limit[0];
+        for (int w = 1; w < warps; ++w) lowest = min(lowest, s.limit[w]);
+        const float least = of_each <= 32 ? value_of(static_cast<unsigned long long>(lowest) << 32) : -INFINITY;
         if (least > lim) {
           lim = least;
           lim_token = 1 << kTokenBits;
