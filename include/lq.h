@@ -604,7 +604,7 @@ lq_status lq_debug_gemm_rings(int a_stages, int raw_stages);
  * default): never. Both give the same results; pairs measured slower, so
  * this is for comparisons. */
 void      lq_debug_gemm_pairs(int on);
-/* lq_attn_paged's kernel: 0 = automatic, 1 = generic (any geometry), 2 =
+/* lq_attn_paged's and lq_attn_tree's kernel: 0 = automatic, 1 = generic (any geometry), 2 =
  * rows of 8 on warp-level MMAs, 3 = tiles of 128 rows on tcgen05
  * (LQ_ERR_UNSUPPORTED where the forced kernel does not take the geometry). */
 lq_status lq_debug_attn_route(int route);
