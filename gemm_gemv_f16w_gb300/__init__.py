@@ -360,7 +360,7 @@ class KVBatch:
                     or (shape and tuple(x.shape) != shape) or x.get_device() != self.gpu:
                 raise LQError(LQ_ERR_INVALID_ARG, "KVBatch: contiguous int32 page_table [batch, max_pages], kv_len [batch] "
                                                   "and q_start [batch + 1] on one device")
-        self.page_table, self.kv_len, self.q_start, self.tokens = page_table, kv_len, q_start, int(tokens)
+        self.page_table, self.kv_len, self.q_start, self.tokens, self.batch = page_table, kv_len, q_start, int(tokens), page_table.shape[0]
         self.struct = KVBatchStruct(page_table.shape[0], page_table.shape[1], int(tokens), int(max_q), _ptr(page_table),
                                     _ptr(kv_len), _ptr(q_start))
         self.ref = ctypes.byref(self.struct)
@@ -615,18 +615,17 @@ def lq_attn_tree(cache, batch, mask, Q, O, scale, positions=None, window=0, sink
 
 
 def lq_tree_accept(batch, parent, token, target, keep, count, next_token, kept_len, stream=None) -> None:
-    """The longest path of the tree that the model's choices (target) confirm:
+    """The path of the tree that the model's choices (target) confirm:
     its rows in keep (int32 [batch, max_keep], -1 behind them), their number in
     count, the choice after the last in next_token and the length of the cache
     with the path in kept_len (int32 [batch] each). See include/lq.h."""
-    t, g, b = batch.tokens, batch.gpu, batch.kv_len.shape[0]
-    rows = [_ints(x, (t,), g, "lq_tree_accept", n) for x, n in ((parent, "parent"), (token, "token"), (target, "target"))]
-    outs = [_ints(x, (b,), g, "lq_tree_accept", n) for x, n in ((count, "count"), (next_token, "next_token"), (kept_len, "kept_len"))]
-    most = keep.shape[-1]
-    st = (_lib or lib()).lq_tree_accept(batch.ref, *rows, _ints(keep, (b, most), g, "lq_tree_accept", "keep"), most, *outs,
-                                        _current_stream() if stream is None else _stream(stream))
+    what, g, t, b, most = "lq_tree_accept", batch.gpu, (batch.tokens,), (batch.batch,), keep.shape[-1]
+    st = (_lib or lib()).lq_tree_accept(batch.ref, _ints(parent, t, g, what, "parent"), _ints(token, t, g, what, "token"),
+                                        _ints(target, t, g, what, "target"), _ints(keep, (batch.batch, most), g, what, "keep"), most,
+                                        _ints(count, b, g, what, "count"), _ints(next_token, b, g, what, "next_token"),
+                                        _ints(kept_len, b, g, what, "kept_len"), _current_stream() if stream is None else _stream(stream))
     if st:
-        _check(st, "lq_tree_accept")
+        _check(st, what)
 
 
 def lq_kv_keep(cache, batch, keep, count, stream=None) -> None:
@@ -634,7 +633,7 @@ def lq_kv_keep(cache, batch, keep, count, stream=None) -> None:
     front of them, in the cache. See include/lq.h."""
     if cache.gpu != batch.gpu:
         _elsewhere(cache, batch, "lq_kv_keep")
-    b, most = batch.kv_len.shape[0], keep.shape[-1]
+    b, most = batch.batch, keep.shape[-1]
     st = (_lib or lib()).lq_kv_keep(cache.ref, batch.ref, _ints(keep, (b, most), batch.gpu, "lq_kv_keep", "keep"), most,
                                     _ints(count, (b,), batch.gpu, "lq_kv_keep", "count"),
                                     _current_stream() if stream is None else _stream(stream))

@@ -34,7 +34,7 @@
 // vocabulary of 151936 take 67 us.)
 //
 // What bounds it: logits are read once, HBM. 32 groups of 8 beams, a fifth of them ended,
-// vocabulary 151936, k 16: 43 us (the parts 33, the join 9; the logits at a copy's rate
+// vocabulary 151936, k 16: 41 us (the parts 33, the join 7; the logits at a copy's rate
 // take 23, those of the live beams 19): the parts begin with the look for the rows that
 // count and end with a wait for the slowest warp, and the join is a chain of four
 // dependent loads and as many barriers. One group of 4 beams, k 8: 11 us. An ended beam

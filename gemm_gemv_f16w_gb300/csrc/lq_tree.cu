@@ -34,7 +34,6 @@ constexpr int kAcceptGroups = 4; // of 32 rows, asked for together
 
 struct PlanArgs {
   kv::Batch b;
-  int page_size;
   const int* parent;
   int* positions;  // may be null
   uint32_t* mask;  // may be null

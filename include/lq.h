@@ -440,8 +440,8 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
  *   rotary_dim and head_dim even, rotary_dim <= head_dim, frequencies of at most
  *   2^32 in size, base > 0, base and factor finite, sections not negative and as
  *   said, interleaved ones such that each axis gets its number, else
- *   LQ_ERR_INVALID_ARG; rotary_dim >
- *   2 * LQ_ROPE_MAX_PAIRS, more axes or head_dim > 65536 -> LQ_ERR_UNSUPPORTED.
+ *   LQ_ERR_INVALID_ARG; rotary_dim > 2 * LQ_ROPE_MAX_PAIRS, more axes or head_dim >
+ *   65536 -> LQ_ERR_UNSUPPORTED.
  *
  * lq_rope turns the rows of Q (heads * head_dim floats, into QO) and of K
  * (kv_heads, into KO) in one launch, each with a leading dimension in floats;
@@ -488,7 +488,7 @@ lq_status lq_rope(const lq_rope_table* table, int64_t tokens, const int32_t* pos
  *   that its bits name, whichever they are. A row with neither gets zeros, and
  *   -inf in lse. All else (work, lse, precision, refusals) as lq_attn_paged.
  *
- * lq_tree_accept: the longest path that the model's own choices confirm. token[t]:
+ * lq_tree_accept: the path that the model's own choices confirm. token[t]:
  *   row t's token; target[t]: the model's choice after row t. The path starts with
  *   row 0 and goes on to the lowest row whose parent is the last one and whose
  *   token is target[last]. Its rows go to keep (batch * max_keep, -1 behind the
@@ -538,7 +538,8 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  *   the own pages of the group's m-th beam without a child, and copies names
  *   what has to be copied into the first of them: groups * beams entries (from
  *   page, to page, tokens), (-1, -1, 0) where nothing is. So every own page keeps
- *   one owner and no copy's target is a source. A parent outside 0 .. beams - 1 gives the
+ *   one owner and no copy's target is a source; full pages that no table names any
+ *   more are the caller's to give out again. A parent outside 0 .. beams - 1 gives the
  *   beam such pages too, and the table of the beam that it takes them from.
  *   table_out must not be table.
  * lq_kv_copy: the first `tokens` tokens of page `from` to page `to`, keys and
