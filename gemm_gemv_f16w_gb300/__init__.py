@@ -540,18 +540,6 @@ def _ints(x, shape, gpu, what, name):
     return x.data_ptr()
 
 
-def _ints_alike(xs, shape, gpu, what, names):
-    """The addresses of int32 tensors of one shape (_ints for several at once)."""
-    if _int32 is None:
-        _types()
-    i32, at = _int32, []
-    for x in xs:
-        if x.dtype is not i32 or x.shape != shape or x.get_device() != gpu or gpu < 0 or not x.is_contiguous():
-            _ints(x, shape, gpu, what, names[len(at)])  # says what is wrong
-        at.append(x.data_ptr())
-    return at
-
-
 def _head_rows(x, tokens, D, gpu, what):
     """(address, leading dimension, heads) of float32 rows [tokens, heads, D] or
     [tokens, heads * D] on one GPU."""
@@ -632,10 +620,10 @@ def lq_tree_accept(batch, parent, token, target, keep, count, next_token, kept_l
     count, the choice after the last in next_token and the length of the cache
     with the path in kept_len (int32 [batch] each). See include/lq.h."""
     what, g, t, b, most = "lq_tree_accept", batch.gpu, (batch.tokens,), (batch.batch,), keep.shape[-1]
-    rows = _ints_alike((parent, token, target), t, g, what, ("parent", "token", "target"))
-    outs = _ints_alike((count, next_token, kept_len), b, g, what, ("count", "next_token", "kept_len"))
-    st = (_lib or lib()).lq_tree_accept(batch.ref, *rows, _ints(keep, (batch.batch, most), g, what, "keep"), most, *outs,
-                                        _current_stream() if stream is None else _stream(stream))
+    st = (_lib or lib()).lq_tree_accept(batch.ref, _ints(parent, t, g, what, "parent"), _ints(token, t, g, what, "token"),
+                                        _ints(target, t, g, what, "target"), _ints(keep, (batch.batch, most), g, what, "keep"), most,
+                                        _ints(count, b, g, what, "count"), _ints(next_token, b, g, what, "next_token"),
+                                        _ints(kept_len, b, g, what, "kept_len"), _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, what)
 
