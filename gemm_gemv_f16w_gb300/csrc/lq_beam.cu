@@ -8,10 +8,16 @@
 // 64-bit arithmetic is slow on this chip and cost the join 1 to 3 us): beams are compared
 // across lse's, where f32's steps (5e-7 at 8) would be ties.
 //
-// The sum. A thread keeps a running maximum M and S = sum 2^(c (x - M)), c = log2(e),
-// in f32; x - M is taken first, so that roundings weigh on distances from the maximum
-// only (and a row of the type's lowest value is a row like any other). Of the
-// terms' errors (2^-22 each) the sum of a vocabulary keeps next to nothing.
+// The sum. Of a round of 4096 logits each warp has M, its largest, and S = sum 2^(c (x -
+// M)), c = log2(e), in f32; x - M is taken first, so that roundings weigh on distances
+// from the maximum only (and a row of the type's lowest value is a row like any other).
+// The warps' eight make the round's, and the join adds a row's rounds in two f32 parts.
+// Which logits are added together, and in which order, is fixed by their places in the
+// row alone: equal rows have equal sums and tie, whichever ranges they are dealt to.
+// log S is off by less than 2^-18, in units of 2^-24: a term 4 for 2^y and 9 for y
+// (2.3 |y| ln 2, and the mean of |y|, weighed by the terms, is at most 5.6 for 512 of them);
+// their sum 9, the warps' 10, the rounds' 10, the logarithm 3. (2^-22 at most in rows of 500 to 2^20
+// normal logits.)
 //
 // The candidates. If each of the 8 warps has ceil(k / 8) maxima (of what a thread has
 // seen) at or above a limit, k logits of the part are: the least of the warps'
@@ -25,7 +31,7 @@
 // the result does not depend on the order in which threads took notes.
 //
 // Split. The rounds of all rows that are read are dealt to the CTAs in equal
-// contiguous ranges; a range's part of a row leaves k candidates and (M, S). Each warp
+// contiguous ranges; a range's part of a row leaves k candidates, and each round (M, S). Each warp
 // streams its own 512 logits of a round by asynchronous copies, two rounds ahead and
 // across rows, and no warp waits for another but where a limit is taken or a row ends.
 // A second kernel, a CTA a group, joins the parts: the sums of each beam by a warp, a
@@ -34,10 +40,11 @@
 // vocabulary of 151936 take 67 us.)
 //
 // What bounds it: logits are read once, HBM. 32 groups of 8 beams, a fifth of them ended,
-// vocabulary 151936, k 16: 41 us (the parts 33, the join 7; the logits at a copy's rate
+// vocabulary 151936, k 16: 42 us (the parts 34, the join 7; the logits at a copy's rate
 // take 23, those of the live beams 19): the parts begin with the look for the rows that
 // count and end with a wait for the slowest warp, and the join is a chain of four
-// dependent loads and as many barriers. One group of 4 beams, k 8: 11 us. An ended beam
+// dependent loads and as many barriers. (With one M and S for a range's part of a row, whose
+// roundings then go by the range, 41.) One group of 4 beams, k 8: 10.5 us. An ended beam
 // (one candidate, its score as it is) and one with a score of -inf are not read at all.
 #include <algorithm>
 #include <atomic>
@@ -63,6 +70,8 @@ constexpr int kCtas = 152 * 3;             // ranges that the rounds are dealt t
 constexpr int kScanRows = 4096;            // rows up to which those that are not read are left out of the deal
 constexpr int kPicks = 1024;               // candidates that a join ranks together
 constexpr int kAtOnce = 2;                 // of a list, in a join
+constexpr int kSumsAtOnce = 2;             // of a lane, in a join
+constexpr int kSums = 64;                  // rounds whose sums are in shared memory, a warp's each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTokenBits = 26;             // of a vocabulary
 
@@ -75,7 +84,7 @@ struct BeamArgs {
   int* out_tokens;
   int* per;                     // rounds of a range
   int* number;                  // [rows]: of a row among those that are read
-  float2* sums;                 // [parts]: M and S
+  float2* sums;                 // [rows][rounds]: M and S
   unsigned long long* lists;    // [parts][k], best first, 0: none
   long long ld;
   int rows, beams, vocab, k, pad;
@@ -104,7 +113,7 @@ struct Notes {
   unsigned long long key[kNotes];  // the largest of a thread's round
   unsigned long long all[LQ_BEAM_MAX * kPer];  // the logits of the best notes' rounds
   unsigned long long few[kThreads];
-  float2 sum[kWarps];
+  float2 sum[kSums][kWarps];  // M and S of what a warp has of a round
   unsigned limit[kWarps];
 };
 struct Join {
@@ -128,6 +137,12 @@ struct Scan {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest of the warp's values, of those that are numbers.
+__device__ __forceinline__ float max_of_warp(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float value_of(unsigned long long key) {
@@ -216,6 +231,10 @@ __device__ __forceinline__ Pair sum_of(float a, float b) {  // exactly
 __device__ __forceinline__ Pair sum_of(const Pair& a, float b) {
   const Pair t = sum_of(a.hi, b);
   return sum_of(t.hi, t.lo + a.lo);
+}
+__device__ __forceinline__ Pair sum_of(const Pair& a, const Pair& b) {
+  const Pair t = sum_of(a.hi, b.hi);
+  return sum_of(t.hi, t.lo + (a.lo + b.lo));
 }
 __device__ __forceinline__ Pick pick_of(const Pair& score, int beam, unsigned long long key) {
   Pick p = {0ull, 0ull};
@@ -327,22 +346,35 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   for (int i = 0; i < kAtOnce; ++i) key[i] = tid < lists ? key_of(tid, own_beam, (tid < covered ? m : 0) + i) : 0ull;
 #pragma unroll 1
   for (int b = warp; b < a.beams; b += kWarps) {
-    const int n = s.start[b + 1] - s.start[b];
-    float top = -INFINITY, sum = 0.0f;
+    if (s.start[b + 1] == s.start[b]) continue;  // not read
+    const float2* const sums = a.sums + static_cast<long long>(row0 + b) * a.rounds;
+    float top = -INFINITY;
+    Pair sum = {0.0f, 0.0f};
 #pragma unroll 1
-    for (int i = lane; i < n; i += 32) {
-      const float2 m = __ldcg(a.sums + s.part[b] + i);
-      const float to = fmaxf(top, m.x), ref = to == -INFINITY ? 0.0f : to;
-      sum = sum * expf(top - ref) + m.y * expf(m.x - ref);
+    for (int i0 = lane; i0 < a.rounds; i0 += 32 * kSumsAtOnce) {
+      float2 m[kSumsAtOnce];
+      float to = top;
+#pragma unroll
+      for (int i = 0; i < kSumsAtOnce; ++i) m[i] = i0 + 32 * i < a.rounds ? __ldcg(sums + i0 + 32 * i) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kSumsAtOnce; ++i) to = fmaxf(to, m[i].x);
+      const float ref = to == -INFINITY ? 0.0f : to, less = expf(top - ref);
+      sum.hi = __fmul_rn(sum.hi, less);
+      sum.lo = __fmul_rn(sum.lo, less);
+#pragma unroll
+      for (int i = 0; i < kSumsAtOnce; ++i) sum = sum_of(sum, __fmul_rn(m[i].y, expf(m[i].x - ref)));
       top = to;
     }
-    float all = top;
+    const float all = max_of_warp(top), ref = all == -INFINITY ? 0.0f : all, less = expf(top - ref);
+    sum.hi = __fmul_rn(sum.hi, less);
+    sum.lo = __fmul_rn(sum.lo, less);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    const float ref = all == -INFINITY ? 0.0f : all;
-    sum = warp_sum(sum * expf(top - ref));
+    for (int o = 16; o > 0; o >>= 1) {
+      const Pair other = {__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)};
+      sum = sum_of(sum, other);
+    }
     // log sum: f32's logarithm, and by how much it misses the sum
-    const float l = logf(sum), miss = fmaf(sum, expf(-l), -1.0f);
+    const float l = logf(sum.hi), part = expf(-l), miss = fmaf(sum.hi, part, -1.0f) + sum.lo * part;
     if (lane == 0) {
       const Pair all_of = sum_of(sum_of(ref, l), miss);
       s.lse[b] = s.base[b] != s.base[b] ? Pair{NAN, 0.0f} : all_of;
@@ -526,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
     }
     __syncthreads();
     const int rounds = min(R - round, left);  // here
-    float M = -INFINITY, S = 0.0f, highest = -INFINITY;
+    float highest = -INFINITY;
     float lim = -3.402823466e38f;     // logits above are noted, and those equal to it
     int lim_token = 1 << kTokenBits;  // whose tokens are below this one
     auto meet = [&](bool done) {
@@ -536,24 +568,43 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
       lim_token = limit.token;
       return more;
     };
+    // The warps' sums of n rounds, the last of them round `last`, become the rounds'. (No
+    // fused operation: the compiler might form it in one place and not in another.)
+    auto add_warps = [&](int n, int last) {
+      if (tid >= n) return;
+      const float2* const of = s.sum[tid];
+      float all = of[0].x, term[kWarps];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) all = fmaxf(all, of[w].x);
+      const float ref = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) term[w] = __fmul_rn(of[w].y, ex2((of[w].x - ref) * kLog2e));
+#pragma unroll
+      for (int half = kWarps / 2; half > 0; half /= 2)
+#pragma unroll
+        for (int w = 0; w < half; ++w) term[w] += term[w + half];
+      a.sums[static_cast<long long>(row) * R + (last - n + 1 + tid)] = make_float2(all, term[0]);
+    };
     int next_limit = 0;
 #pragma unroll 1
     for (int i = 0; i < rounds; ++i, ++round) {
+      if (i > 0 && i % kSums == 0) {
+        while (meet(true)) {
+        }
+        add_warps(kSums, round - 1);
+        __syncthreads();
+      }
       wait_copies<kStages - 2>();
+      if constexpr (!VEC) __syncwarp();  // what other lanes have copied
       float v[kPer];
       const float* const at = ring + stage * kRound;
-      if constexpr (VEC) {
 #pragma unroll
-        for (int n = 0; n < kPer / 4; ++n) {
-          const float4 f = *reinterpret_cast<const float4*>(at + (n * 32 + lane) * 4);
-          v[4 * n] = f.x;
-          v[4 * n + 1] = f.y;
-          v[4 * n + 2] = f.z;
-          v[4 * n + 3] = f.w;
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < kPer; ++n) v[n] = at[n * 32 + lane];
+      for (int n = 0; n < kPer / 4; ++n) {
+        const float4 f = *reinterpret_cast<const float4*>(at + (n * 32 + lane) * 4);
+        v[4 * n] = f.x;
+        v[4 * n + 1] = f.y;
+        v[4 * n + 2] = f.z;
+        v[4 * n + 3] = f.w;
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
       copy();
@@ -561,22 +612,25 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
       if (base + kRound / kWarps > a.vocab) {
 #pragma unroll
         for (int n = 0; n < kPer; ++n)
-          if (base + (VEC ? ((n / 4) * 32 + lane) * 4 + n % 4 : n * 32 + lane) >= a.vocab) v[n] = -INFINITY;
+          if (base + ((n / 4) * 32 + lane) * 4 + n % 4 >= a.vocab) v[n] = -INFINITY;
       }
       float top = v[0];
 #pragma unroll
       for (int n = 1; n < kPer; ++n) top = fmaxf(top, v[n]);
       // the sum
-      const float to = fmaxf(M, top), ref = to == -INFINITY ? 0.0f : to;
-      S *= ex2((M - ref) * kLog2e);
-      M = to;
-      float2 sum = make_float2(0.0f, 0.0f);
+      const float whole = max_of_warp(top), ref = whole == -INFINITY ? 0.0f : whole;
+      float2 term[kPer / 2];
 #pragma unroll
-      for (int n = 0; n < kPer; n += 2) {
-        const float2 y = fmul2(fadd2(make_float2(v[n], v[n + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
-        sum = fadd2(sum, make_float2(ex2(y.x), ex2(y.y)));
+      for (int n = 0; n < kPer / 2; ++n) {
+        const float2 y = fmul2(fadd2(make_float2(v[2 * n], v[2 * n + 1]), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+        term[n] = make_float2(ex2(y.x), ex2(y.y));
       }
-      S += sum.x + sum.y;
+#pragma unroll
+      for (int half = kPer / 4; half > 0; half /= 2)
+#pragma unroll
+        for (int n = 0; n < half; ++n) term[n] = fadd2(term[n], term[n + half]);
+      const float sum = warp_sum(term[0].x + term[0].y);
+      if (lane == 0) s.sum[i % kSums][warp] = make_float2(whole, sum);
       // the candidates
       highest = fmaxf(highest, top);
       if (i == next_limit) {
@@ -597,14 +651,14 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
         }
         next_limit = 4 * i + 3;
       }
-      if (__any_sync(0xffffffffu, top >= lim)) {
+      if (whole >= lim) {
         // (eight warps take no more than kStep notes between this and their next looks)
         while (__shfl_sync(0xffffffffu, *static_cast<volatile int*>(&count), 0) > kNotes - kStep) meet(false);
         if (top >= lim) {
           int n = kPer - 1;  // the first of the largest
 #pragma unroll
           for (int m = kPer - 2; m >= 0; --m) n = v[m] == top ? m : n;
-          const int j = base + (VEC ? ((n / 4) * 32 + lane) * 4 + n % 4 : n * 32 + lane);
+          const int j = base + ((n / 4) * 32 + lane) * 4 + n % 4;
           if (top > lim || j < lim_token) {
             const int to_note = atomicAdd(&count, 1);
             if (LQ_IN_BOUNDS(to_note < kNotes)) s.key[to_note] = amax::make_key(top, static_cast<unsigned>(j));
@@ -614,15 +668,9 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
       }
     }
     left -= rounds;
-    // the block's sum
-    float top = M;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float w = warp_sum(S * ex2((M - ref) * kLog2e));
     while (meet(true)) {
     }
-    if (lane == 0) s.sum[warp] = make_float2(top, w);
+    add_warps((rounds - 1) % kSums + 1, round - 1);
     const int notes = best_of(s.key, s.few, count, a.k);  // (a barrier, too)
     if (tid == 0) count = 0;
     __syncthreads();
@@ -631,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
     for (int e = tid; e < notes * kPer; e += kThreads) {
       const int j = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(s.key[e / kPer])), n = e % kPer;
       const int within = j % (kRound / kWarps), first = j - within;  // of the warp's 512
-      const int token = first + (VEC ? (n / 4) * 128 + within % 128 / 4 * 4 + n % 4 : n * 32 + within % 32);
+      const int token = first + (n / 4) * 128 + within % 128 / 4 * 4 + n % 4;
       if (token >= a.vocab || !LQ_IN_BOUNDS(token >= 0)) continue;
       const float x = a.logits[row * a.ld + token];
       const unsigned long long key = x > -INFINITY ? amax::make_key(x, static_cast<unsigned>(token)) : 0ull;
@@ -644,13 +692,6 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs a) {
     const int n = best_of(s.all, s.few, count, a.k);
     const int part = number + cta;
     if (tid < a.k) a.lists[static_cast<long long>(part) * a.k + tid] = tid < n ? s.all[tid] : 0ull;
-    if (warp == 1 && lane == 0) {
-      float all = -INFINITY, total = 0.0f;
-      for (int i = 0; i < kWarps; ++i) all = fmaxf(all, s.sum[i].x);
-      const float r = all == -INFINITY ? 0.0f : all;
-      for (int i = 0; i < kWarps; ++i) total += s.sum[i].y * ex2((s.sum[i].x - r) * kLog2e);
-      a.sums[part] = make_float2(all, total);
-    }
     __syncthreads();  // the notes are free
     if (round == R && left > 0) {
       round = 0;
@@ -687,7 +728,8 @@ extern "C" {
 size_t lq_beam_work_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
   if (groups < 1 || groups > (1LL << 24) || !sizes_fit(groups, beams, vocab, k)) return 0;
   const size_t lists = static_cast<size_t>(groups * beams) + kCtas;  // a part ends where a row or a range does
-  return number_bytes(groups * beams) + lists * (sizeof(float2) + static_cast<size_t>(k) * 8);
+  return number_bytes(groups * beams) + lists * static_cast<size_t>(k) * 8 +
+         static_cast<size_t>(groups * beams) * static_cast<size_t>(row_rounds(vocab)) * sizeof(float2);
 }
 
 lq_status lq_beam_select(const float* logits, int64_t ld, const float* scores, int64_t groups, int64_t beams, int64_t vocab, int64_t k,

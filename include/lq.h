@@ -518,7 +518,10 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  *     scores[b] + (logits[b, j] - log sum_j exp(logits[b, j])),
  *   best first: out_scores (f32), out_parents (the beam within its group) and
  *   out_tokens, groups * k each. Scores are compared in two f32 parts (48 bits); equal
- *   ones go by the lower beam, then the larger logit, then the lower token. Logits
+ *   ones go by the lower beam, then the larger logit, then the lower token. The log is
+ *   off by less than 2^-18, by the same amount for all of a row's tokens, and out_scores are
+ *   rounded once more; it depends on the row's logits alone, so that equal rows with
+ *   equal scores tie, and a group's results are the same bits alone and in any batch. Logits
  *   and scores that are not finite, and sums beyond f32's range, are never chosen (a
  *   row with NaN or +inf among its logits gives no candidate); with fewer than k
  *   candidates the rest are (-inf, -1, -1). finished (NULL or groups * beams): a beam
@@ -526,7 +529,7 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  *   its logits do not count.
  *   logits: row b of group g at logits + (g * beams + b) * ld. work:
  *   lq_beam_work_bytes(...) bytes of DEVICE scratch memory, 16-byte aligned, one call at
- *   a time (0 for sizes out of range). The same inputs give the same bits.
+ *   a time (0 for sizes out of range).
  *   ld >= vocab, 0 <= pad < vocab, else LQ_ERR_INVALID_ARG; beams or k >
  *   LQ_BEAM_MAX, vocab > 2^26 or more than 2^24 rows -> LQ_ERR_UNSUPPORTED.
  *
