@@ -6,8 +6,11 @@
 // Angles of far positions have to be reduced with more bits than f32 has: at
 // position 10^6 an f32 product is off by 0.06. Here a frequency is held as turns
 // a position in units of 2^-64, so that the 64-bit integer product with the
-// position is the angle modulo one turn by itself (off by at most 2^-33 of a turn at
-// any 32-bit position); its upper 32 bits go to sincospif as a value in [-1, 1).
+// position is the angle modulo one turn by itself (the frequency is off by 1.5 units
+// at most, the angle by 2^-32 of a turn at any 32-bit position). Of its upper 32 bits the
+// nearest quarter is taken off in integers and turned by exactly; what is left, an eighth
+// of a turn at most, goes to sincospif in f32, which rounds it by 2^-28 of a turn at most
+// (the whole angle in f32 would be off by 2^-26).
 //
 // Split. A warp takes one token and a range of its heads; a lane owns a unit of
 // eight values (four pairs) at the same place of every head, so that cosines
@@ -104,8 +107,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
         const int j = u * W + i;
         const long long p = a.pos[a.r.axis[j] * a.ldp + t];
         const unsigned long long turn = static_cast<unsigned long long>(p) * a.r.turns[j];
-        const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-        sincospif(half_turns, &s[i], &c[i]);
+        const unsigned part = static_cast<unsigned>((turn + (1ull << 31)) >> 32), quarter = (part + (1u << 29)) >> 30;
+        float sn, cs;
+        sincospif(static_cast<float>(static_cast<int>(part - (quarter << 30))) * 0x1p-31f, &sn, &cs);
+        const float x = quarter & 1u ? sn : cs, y = quarter & 1u ? cs : sn;
+        c[i] = quarter == 1u || quarter == 2u ? -x : x;
+        s[i] = quarter >= 2u ? -y : y;
         c[i] *= a.r.factor;
         s[i] *= a.r.factor * a.sign;
       }

@@ -448,8 +448,10 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
  * heads or kv_heads 0: that side is left out. QO may be Q (and KO K) with the same
  * leading dimension; any other overlap is not allowed. positions: DEVICE
  * int32, row x at positions + x * ldp, any sign. inverse != 0 turns backwards (and
- * multiplies by factor all the same). Angles are exact to 2^-31 of a turn at every
- * position; the result is within 6 * 2^-24 of |factor| (|x_a| + |x_b|). */
+ * multiplies by factor all the same). Angles are those of the frequencies as the table
+ * holds them, off by less than 2^-27 of a turn at every position (those made from base >=
+ * 1 are rounded to doubles first, at position 2^31 up to 2^-24 of a turn); the result is
+ * within 6 * 2^-24 of |factor| (|x_a| + |x_b|). */
 #define LQ_ROPE_MAX_PAIRS 128
 #define LQ_ROPE_MAX_AXES 4
 enum { LQ_ROPE_HALVES = 0, LQ_ROPE_ADJACENT = 1 };
