@@ -562,8 +562,8 @@ def _head_rows(x, tokens, D, gpu, what):
 def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, stream=None) -> None:
     """Turns the rows of Q and, if given, K (float32 [tokens, heads, head_dim],
     slices of a fused projection's rows allowed) by their positions (int32
-    [tokens] or [axes, tokens]), in place or into q_out and k_out. See
-    include/lq.h."""
+    [tokens] or [axes, tokens]; one row expanded to all axes will do), in
+    place or into q_out and k_out. See include/lq.h."""
     if _int32 is None:
         _types()
     tokens, gpu, D, axes = Q.shape[0], Q.get_device(), rope.head_dim, rope.axes

@@ -250,7 +250,8 @@ lq_status lq_rope(const lq_rope_table* table, int64_t tokens, const int32_t* pos
   if (tokens == 0 || heads + kv_heads == 0) return LQ_OK;
   const int64_t d = table->head_dim;
   if (heads > 65536 || kv_heads > 65536 || tokens > (1LL << 30)) return LQ_ERR_UNSUPPORTED;
-  if (!positions || !aligned_to(positions, 4) || (table->axes > 1 && ldp < tokens)) return LQ_ERR_INVALID_ARG;
+  // (ldp 0: all axes go by one row, which is only read)
+  if (!positions || !aligned_to(positions, 4) || (table->axes > 1 && ldp != 0 && ldp < tokens)) return LQ_ERR_INVALID_ARG;
   RopeArgs a = {};
   a.r = *table;
   a.pos = positions;

@@ -447,7 +447,8 @@ lq_status lq_attn_paged(const lq_kv_cache* cache, const lq_kv_batch* batch, cons
  * (kv_heads, into KO) in one launch, each with a leading dimension in floats;
  * heads or kv_heads 0: that side is left out. QO may be Q (and KO K) with the same
  * leading dimension; any other overlap is not allowed. positions: DEVICE
- * int32, row x at positions + x * ldp, any sign. inverse != 0 turns backwards (and
+ * int32, any sign, axis x's row at positions + x * ldp, ldp >= tokens or 0 (all axes go
+ * by one row, as those of plain text do). inverse != 0 turns backwards (and
  * multiplies by factor all the same). Angles are those of the frequencies as the table
  * holds them, off by less than 2^-27 of a turn at every position (those made from base >=
  * 1 are rounded to doubles first, at position 2^31 up to 2^-24 of a turn); the result is

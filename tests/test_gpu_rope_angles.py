@@ -38,3 +38,23 @@ def test_cosine_and_sine(lq, cuda_dev, d, rotary, far, adjacent):
     for got, want in ((y[:, at], cos), (y[:, at + (1 if adjacent else half)], sin)):
         assert (np.abs(got - want) <= 2 * math.pi * (2.0**-28 + 2.0**-33) + 2.0**-23 * np.abs(want) + 1e-15).all()
     assert lq.last_device_error() == lq.LQ_OK
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 70])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_one_row_of_positions_for_all_axes(lq, cuda_dev, tokens, interleaved):
+    """Text has one position on every axis: an expanded row gives the bits of a
+    copied one, and of a table with one axis."""
+    rng = np.random.default_rng(tokens)
+    rope = lq.Rope(128, sections=[24, 20, 20], interleaved=interleaved)
+    row = torch.from_numpy(rng.integers(0, 10**6, tokens).astype(np.int32)).to(cuda_dev)
+    q = torch.from_numpy(rng.standard_normal((tokens, 5, 128)).astype(np.float32)).to(cuda_dev)
+    k = torch.from_numpy(rng.standard_normal((tokens, 2, 128)).astype(np.float32)).to(cuda_dev)
+    results = []
+    for table, positions in ((rope, row.expand(3, tokens)), (rope, row.expand(3, tokens).contiguous()), (lq.Rope(128), row)):
+        out = torch.full_like(q, float("nan")), torch.full_like(k, float("nan"))
+        lq.lq_rope(table, positions, q, k, q_out=out[0], k_out=out[1])
+        results.append(out)
+    for out in results[1:]:
+        assert torch.equal(out[0], results[0][0]) and torch.equal(out[1], results[0][1])
+    assert torch.isfinite(results[0][0]).all() and lq.last_device_error() == lq.LQ_OK
