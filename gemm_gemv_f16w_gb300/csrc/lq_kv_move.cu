@@ -318,8 +318,9 @@ lq_status lq_kv_copy(const lq_kv_cache* cache, const int32_t* copies, int64_t n,
 lq_status lq_beam_pages(const int32_t* parent, int64_t groups, int64_t beams, const int32_t* table, int64_t max_pages,
                         const int32_t* kv_len, int64_t page_size, int32_t* table_out, int32_t* copies, void* stream) {
   if (groups < 0 || beams < 1 || max_pages < 0 || page_size < 1 || page_size > 65536) return LQ_ERR_INVALID_ARG;
-  if (beams > LQ_BEAM_MAX || groups * beams > (1LL << 30) || max_pages * page_size > (1LL << 30) ||
-      beams * max_pages > (1LL << 30))
+  const int64_t most = 1LL << 30;  // (each by itself, too: the products are to fit 64 bits)
+  if (beams > LQ_BEAM_MAX || groups > most || max_pages > most || groups * beams > most || max_pages * page_size > most ||
+      beams * max_pages > most)
     return LQ_ERR_UNSUPPORTED;
   if (groups == 0) return LQ_OK;
   for (const void* p : {static_cast<const void*>(parent), static_cast<const void*>(kv_len), static_cast<const void*>(copies)})
