@@ -660,8 +660,8 @@ def lq_beam_select(logits, scores, beams, k, out_scores, out_parents, out_tokens
     """The k best continuations of each group of ``beams`` rows of logits
     (float32 [groups * beams, vocab], rows may be strided) by scores (float32
     [groups * beams]) + log softmax: out_scores, out_parents, out_tokens
-    [groups, k], work: beam_buffers(...). finished: int32 [groups * beams] or
-    None. See include/lq.h."""
+    [groups, k], work: beam_buffers(...). out_scores may be scores where k is
+    beams. finished: int32 [groups * beams] or None. See include/lq.h."""
     what = "lq_beam_select"
     (n, vocab), gpu = logits.shape, logits.get_device()
     groups = n // beams if beams > 0 else 0

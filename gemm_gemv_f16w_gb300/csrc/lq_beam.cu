@@ -744,6 +744,10 @@ lq_status lq_beam_select(const float* logits, int64_t ld, const float* scores, i
                         static_cast<const void*>(out_parents), static_cast<const void*>(out_tokens)})
     if (!p || !aligned_to(p, 4)) return LQ_ERR_INVALID_ARG;
   if (!work || !aligned_to(work, 16) || !aligned_to(finished, 4)) return LQ_ERR_INVALID_ARG;
+  // a group's scores are read before its results are written, which are in their place
+  // only where there are as many
+  const uintptr_t in = reinterpret_cast<uintptr_t>(scores), out = reinterpret_cast<uintptr_t>(out_scores);
+  if (in < out + groups * k * sizeof(float) && out < in + groups * beams * sizeof(float) && !(in == out && k == beams)) return LQ_ERR_INVALID_ARG;
   BeamArgs a = {};
   a.logits = logits;
   a.ld = ld;

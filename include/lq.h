@@ -529,11 +529,12 @@ lq_status lq_kv_keep(const lq_kv_cache* cache, const lq_kv_batch* batch, const i
  *   row with NaN or +inf among its logits gives no candidate); with fewer than k
  *   candidates the rest are (-inf, -1, -1). finished (NULL or groups * beams): a beam
  *   where it is not 0 stands for one candidate, its score as it is and token `pad`;
- *   its logits do not count.
+ *   its logits do not count. out_scores may be scores where k == beams; nothing else
+ *   that is written may overlap what is read.
  *   logits: row b of group g at logits + (g * beams + b) * ld. work:
  *   lq_beam_work_bytes(...) bytes of DEVICE scratch memory, 16-byte aligned, one call at
  *   a time (0 for sizes out of range).
- *   ld >= vocab, 0 <= pad < vocab, else LQ_ERR_INVALID_ARG; beams or k >
+ *   ld >= vocab, 0 <= pad < vocab, scores and out_scores as said, else LQ_ERR_INVALID_ARG; beams or k >
  *   LQ_BEAM_MAX, vocab > 2^26 or more than 2^24 rows -> LQ_ERR_UNSUPPORTED.
  *
  * lq_beam_pages: the beams' page tables (groups * beams rows of max_pages) for the

@@ -78,3 +78,13 @@ def test_rows_of_one_value(lq, cuda_dev, vocab, value):
     assert np.array_equal(p, order) and np.array_equal(t, [[0, 1 if two else 0]] * 2)
     want = scores.reshape(2, 3).astype(np.float64)[[[0], [1]], order] - np.log(float(vocab))
     assert (np.abs(s - want) <= 1.25 * 2.0**-23 + 2.0**-24 * np.abs(want)).all()
+
+
+def test_scores_in_place(lq, cuda_dev):
+    """As many results as beams may take the scores' place."""
+    rng = np.random.default_rng(9)
+    x, scores = rng.standard_normal((240, 5000)).astype(np.float32), (-9 * rng.random(240)).astype(np.float32)
+    X, S = torch.from_numpy(x).to(cuda_dev), torch.from_numpy(scores).to(cuda_dev)
+    _, out_p, out_t, work = lq.beam_buffers(60, 4, 5000, 4)
+    lq.lq_beam_select(X, S, 4, 4, S.view(60, 4), out_p, out_t, work)
+    _check([S.view(60, 4).cpu().numpy(), out_p.cpu().numpy(), out_t.cpu().numpy()], _best(_scores(x, scores), 4, 4))
