@@ -589,7 +589,7 @@ def lq_rope(rope, positions, Q, K=None, q_out=None, k_out=None, inverse=False, s
 def lq_tree_plan(batch, parent, positions=None, mask=None, window=0, sinks=0, stream=None) -> None:
     """Positions (int32 [tokens]) and masks (int32 [tokens, words], a bit a row
     of the sequence) of the batch's new tokens from their parents (int32
-    [tokens]). See include/lq.h."""
+    [tokens]). kv_len must lie within the table's pages. See include/lq.h."""
     t, g = batch.tokens, batch.gpu
     p = _ints(parent, (t,), g, "lq_tree_plan", "parent")
     pos = 0 if positions is None else _ints(positions, (t,), g, "lq_tree_plan", "positions")
@@ -618,7 +618,8 @@ def lq_tree_accept(batch, parent, token, target, keep, count, next_token, kept_l
     """The path of the tree that the model's choices (target) confirm:
     its rows in keep (int32 [batch, max_keep], -1 behind them), their number in
     count, the choice after the last in next_token and the length of the cache
-    with the path in kept_len (int32 [batch] each). See include/lq.h."""
+    with the path in kept_len (int32 [batch] each). kv_len must lie within the
+    table's pages. See include/lq.h."""
     what, g, t, b, most = "lq_tree_accept", batch.gpu, (batch.tokens,), (batch.batch,), keep.shape[-1]
     st = (_lib or lib()).lq_tree_accept(batch.ref, _ints(parent, t, g, what, "parent"), _ints(token, t, g, what, "token"),
                                         _ints(target, t, g, what, "target"), _ints(keep, (batch.batch, most), g, what, "keep"), most,

@@ -334,7 +334,8 @@ lq_status lq_matmul_swiglu(int fmt, const float* A, const void* W, float* H,
  *     window has left behind) is never accessed: writes to it are dropped,
  *     reads give zeros, its keys are invisible to attention. Rows outside
  *     0 .. tokens-1 and positions below 0 or past max_pages * page_size are
- *     treated likewise; kv_len beyond max_pages * page_size counts as that.
+ *     treated likewise; kv_len beyond max_pages * page_size counts as that
+ *     (but for lq_tree_plan and lq_tree_accept, which see no cache).
  *   - `tokens` is the number of rows of K, V, Q and O; rows that belong to
  *     no sequence are left as they are. max_q is the largest number of new
  *     tokens of a sequence, or 0 if unknown; it only steers which kernels run
@@ -476,7 +477,10 @@ lq_status lq_rope(const lq_rope_table* table, int64_t tokens, const int32_t* pos
  * sequence's rows, of the row that row t follows; anything that is not below t's
  * own number (-1, say) makes it a root. Row r of a sequence is stored in slot base
  * + r, base = kv_len - rows, as lq_kv_write does; its position in the text is
- * base + its depth.
+ * base + its depth. lq_tree_plan and lq_tree_accept see no cache: they take kv_len
+ * as it is, and it must not pass max_pages * page_size. (The other calls would count a
+ * longer one as that: positions and kept_len would then lie behind the slots that are
+ * written, read and kept, so that the next step took old rows for the path.)
  *
  * lq_tree_plan: from the parents, once a step,
  *   positions (NULL or tokens): base + depth, for lq_rope and lq_attn_tree;
