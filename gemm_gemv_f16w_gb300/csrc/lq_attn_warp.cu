@@ -360,12 +360,16 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::W * 32, 1) attn_warp_kernel(c
   // in parts of 16 tiles). Otherwise all tiles in equal ranges.
   const bool whole_units = one_pass && short_units && units <= gridDim.x;
   long long per = max(kv::quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
-  // One tree: where the parts of a unit would be joined in two rounds, a few more than kJoin - 1
-  // of them, ranges that make one round of it, though some SMs stay idle. 7 tokens of 32 heads
+  // One tree, whose units are all alike (several sequences' are not): where the parts of a
+  // unit would be joined in two rounds, a few more than kJoin - 1 of them, ranges that make
+  // one round of it, though some SMs stay idle. 7 tokens of 32 heads
   // over 8 of 128, f16 | Q8_0: over 2000 positions 13.9 | 14.7 us against 15.8 | 16.8, over 4000 16.8 |
-  // 18.5 against 17.6 | 19.1; over 8000 21.7 | 24.8 against 21.2 | 23.9.
+  // 18.5 against 17.6 | 19.1; over 8000 21.7 | 24.8 against 21.2 | 23.9. Of 264 shapes of heads
+  // of 64 and 128 that it applies to (3 to 24 tokens, 16 to 64 heads over 2 to 8, 1200 to 4400
+  // positions, three formats) times are 0.84 to 1.03 of those without it, 0.985 in the mean;
+  // heads of 256 gain nothing (180 shapes, 0.93 to 1.05, 1.00) and do without.
   constexpr int kShortTiles = 300;
-  if (kTree && a.b.batch == 1) {
+  if (kTree && D < 256 && a.b.batch == 1) {
     const Cost one = cost(0);
     if (one.n <= kShortTiles && one.units * (kJoin - 1) * 10 >= static_cast<int>(gridDim.x) * 6)
       per = max(per, static_cast<long long>((one.n + START + kJoin - 2) / (kJoin - 1)));
