@@ -88,3 +88,30 @@ def test_scores_in_place(lq, cuda_dev):
     _, out_p, out_t, work = lq.beam_buffers(60, 4, 5000, 4)
     lq.lq_beam_select(X, S, 4, 4, S.view(60, 4), out_p, out_t, work)
     _check([S.view(60, 4).cpu().numpy(), out_p.cpu().numpy(), out_t.cpu().numpy()], _best(_scores(x, scores), 4, 4))
+
+
+@pytest.mark.parametrize("k", [4, 64])
+def test_ranges_of_many_rounds(lq, cuda_dev, k):
+    """Parts of more rounds than shared memory keeps sums of (64): a group among 32
+    has the bits that it has alone, where its rows are cut into short parts; and
+    the scores are those of the sums in 64 bits. One row grows, one has one value."""
+    groups, beams, vocab = 32, 4, 2**20 + 5
+    g = torch.Generator(device=cuda_dev).manual_seed(k)
+    x = 2.5 * torch.randn(groups * beams, vocab, generator=g, device=cuda_dev)
+    x[4 * 7 + 1] = torch.arange(vocab, device=cuda_dev) / 65536.0
+    x[4 * 7 + 2] = 3.75
+    scores = -9 * torch.rand(groups * beams, generator=g, device=cuda_dev)
+    out = lq.beam_buffers(groups, beams, vocab, k)
+    lq.lq_beam_select(x, scores, beams, k, *out)
+    for at in (0, 7, 15, 31):
+        one = lq.beam_buffers(1, beams, vocab, k)
+        lq.lq_beam_select(x[at * beams:(at + 1) * beams], scores[at * beams:(at + 1) * beams].contiguous(), beams, k, *one)
+        for a, b in zip(out[:3], one[:3]):
+            assert torch.equal(a[at], b[0]), at
+    lse = torch.stack([torch.logsumexp(r.double(), 0) for r in x])
+    rows = out[1].long() + torch.arange(groups, device=cuda_dev)[:, None] * beams
+    want = scores.double()[rows] + (x[rows, out[2].long()].double() - lse[rows])
+    assert (out[1] >= 0).all() and ((out[0].double() - want).abs() <= 2.0**-24 * want.abs() + 2.0**-18).all()
+    best = (scores.double()[:, None] - lse[:, None] + x.topk(k, 1).values.double()).view(groups, -1).sort(1, descending=True).values[:, :k]
+    assert ((out[0].double() - best).abs() <= 2.0**-24 * best.abs() + 2.0**-18).all()
+    assert lq.last_device_error() == lq.LQ_OK
